@@ -1,0 +1,380 @@
+// Attention of a tile of R = 16 RT rows over a run of keys and values, streamed
+// once: o = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m), s_j = c q.k_j in the
+// log2 domain, with the running maximum m and sum kept per row in fp32.
+//
+// Rows. The rows of a (sequence, kv head) are its tokens times the G query
+// heads that share the kv head: row r is token r / G, head r % G, so that every
+// key and value read serves all of them.
+//
+// Work of a workgroup: four waves; a step gives each wave 32 consecutive
+// tokens. Each wave keeps its own m, sum and output over its tokens (no barrier
+// while streaming) and the four are joined at the end. A wave holds the next
+// step's keys and values in registers while it works on the current ones, which
+// lie in its own part of LDS.
+//
+// Products (16 x 16 matrix instructions, 32-deep). S^T = K Q^T puts a row's
+// scores for tokens 16 b + 4 g + i (g = lane / 16) into registers of the lanes
+// of that row, so the softmax needs two lane swaps per step. These registers
+// are the B operand of O^T = V^T P^T as they are, once V^T's fragments take the
+// tokens in the same order {4 g + 0..3, 16 + 4 g + 0..3}, which the transposing
+// LDS reads give without any movement of P.
+#pragma once
+
+#include "kda_attn_device.h"
+
+namespace kda {
+
+constexpr int kWaves = 4;
+constexpr int kStepWave = 32;                  // tokens per wave and step
+constexpr int kStep = kWaves * kStepWave;      // tokens per workgroup and step
+
+template <int K, int V, int RT, typename TC> struct Stream {
+    using Frag = typename mma_of<TC>::frag;
+    using Elem = typename mma_of<TC>::elem;  // of q
+    static constexpr int R = 16 * RT;
+    static constexpr int ES = sizeof(TC);
+    static constexpr bool kCodes = sizeof(TC) == 1;
+    static constexpr int CK = K * ES / 16, CV = V * ES / 16;  // 16-byte chunks per row
+    static constexpr int NK = kStepWave * CK / 64, NV = kStepWave * CV / 64;  // chunks per lane and step
+    static constexpr int KT = K / 32, VT = V / 16;
+    static constexpr int KB = kStepWave * K * ES, VB = kStepWave * V * ES;    // LDS bytes per wave
+    static constexpr int kJoinRow = V + 4;                                    // floats per row of a join tile
+    static constexpr int kJoin = kWaves * 16 * kJoinRow * 4;
+    static constexpr int kRing = kWaves * (KB + VB);
+    static constexpr int kLds = kRing > kJoin ? kRing : kJoin;
+
+    // Chunk places in LDS: the tokens that one read instruction takes from a
+    // column of chunks are spread over the banks.
+    static __device__ __forceinline__ int swz_k(int t) { return t & (CK < 8 ? CK - 1 : 7); }
+    static __device__ __forceinline__ int swz_v(int t) {
+        if (ES == 2) return (2 * t) & (CV - 1);
+        if (ES == 1) return (t + (t >> 4) * 4) & (CV - 1);
+        return (4 * (t >> 2)) & (CV - 1);
+    }
+
+    Frag q[RT][KT];
+    f32x4 o[VT][RT];
+    float m[RT], l[RT];  // per row l % 16 of each 16-row block; l is this lane's share
+    u32x4 kr[NK], vr[NV];
+    uint32_t ke[2], ve[2];
+
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int d = 0; d < VT; ++d) o[d][i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+        }
+    }
+
+    // Row tile rt of (sequence rows from `start`, kv head g): fragments of q.
+    // Rows past `rows` repeat the last one and are not stored.
+    __device__ __forceinline__ void load_q(const AttnArgs &a, int start, int kvh, int r0, int rows, int lane) {
+        const int g = lane >> 4;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int r = r0 + min(16 * i + (lane & 15), rows - 1);
+            const int tok = r / a.G, h = kvh * a.G + (r - tok * a.G);
+            const Elem *p = static_cast<const Elem *>(a.q) + static_cast<int64_t>(start + tok) * a.qs + h * K + 8 * g;
+#pragma unroll
+            for (int s = 0; s < KT; ++s) q[i][s] = load_frag(p + 32 * s);
+        }
+    }
+
+    // ---- sources: chunk x of a wave's 32 tokens from position p0 on
+    // cache: pg[b] is the page of tokens 16 b .. 16 b + 15 (a page ends at a multiple of 16)
+    __device__ __forceinline__ void load_cache(const AttnArgs &a, int kvh, int p0, const int (&pg)[2], int lane) {
+        const int ps = 1 << a.page_shift, lane_ = lane;
+        int64_t base[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+            base[b] = (static_cast<int64_t>(max(pg[b], 0)) * a.Hk + kvh) * ps + ((p0 + 16 * b) & (ps - 1));
+#pragma unroll
+        for (int x = 0; x < NK; ++x) {
+            const int e = x * 64 + lane_, t = e / CK, c = e % CK;
+            kr[x] = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.k) +
+                                                     (base[t >> 4] + (t & 15)) * (K * ES) + 16 * c);
+        }
+#pragma unroll
+        for (int x = 0; x < NV; ++x) {
+            const int e = x * 64 + lane_, t = e / CV, c = e % CV;
+            vr[x] = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.v) +
+                                                     (base[t >> 4] + (t & 15)) * (V * ES) + 16 * c);
+        }
+        if (kCodes) {
+            const int g = lane >> 4;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                ke[b] = *reinterpret_cast<const uint32_t *>(a.kexp + base[b] + 4 * g);
+                ve[b] = *reinterpret_cast<const uint32_t *>(a.vexp + base[b] + 4 * g);
+            }
+        }
+    }
+    // packed tokens of the call: a position past the last token reads the last one and is masked
+    __device__ __forceinline__ void load_packed(const AttnArgs &a, int start, int kvh, int p0, int lane) {
+#pragma unroll
+        for (int x = 0; x < NK; ++x) {
+            const int e = x * 64 + lane, t = e / CK, c = e % CK;
+            const int64_t row = min(start + p0 + t, a.T - 1);
+            kr[x] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(
+                        static_cast<const TC *>(a.k) + row * a.ks + kvh * K) + 16 * c);
+        }
+#pragma unroll
+        for (int x = 0; x < NV; ++x) {
+            const int e = x * 64 + lane, t = e / CV, c = e % CV;
+            const int64_t row = min(start + p0 + t, a.T - 1);
+            vr[x] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(
+                        static_cast<const TC *>(a.v) + row * a.vs + kvh * V) + 16 * c);
+        }
+    }
+
+    // Registers to this wave's LDS. `masked`: tokens that nobody may see (here[b] false,
+    // or position >= end) get zero values, and the result says whether any of the others
+    // holds an infinity or NaN.
+    __device__ __forceinline__ bool stage(char *lk, char *lv, bool masked, int p0, int end, const bool (&here)[2], int lane) {
+        bool odd = false;
+        if (masked) {
+#pragma unroll
+            for (int x = 0; x < NV; ++x) {
+                const int t = (x * 64 + lane) / CV;
+                if (p0 + t >= end || !(t < 16 ? here[0] : here[1])) vr[x] = (u32x4){0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) odd |= not_finite<TC>(vr[x][j]);
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < NK; ++x) {
+            const int e = x * 64 + lane, t = e / CK, c = e % CK;
+            *reinterpret_cast<u32x4 *>(lk + t * (K * ES) + 16 * (c ^ swz_k(t))) = kr[x];
+        }
+#pragma unroll
+        for (int x = 0; x < NV; ++x) {
+            const int e = x * 64 + lane, t = e / CV, c = e % CV;
+            *reinterpret_cast<u32x4 *>(lv + t * (V * ES) + 16 * (c ^ swz_v(t))) = vr[x];
+        }
+        return masked && __any(odd);
+    }
+
+    __device__ __forceinline__ Frag k_frag(const char *lk, int b, int s, int lane) const {
+        const int t = 16 * b + (lane & 15), g = lane >> 4;
+        const char *row = lk + t * (K * ES);
+        if constexpr (ES == 2) {
+            return *reinterpret_cast<const Frag *>(row + 16 * ((4 * s + g) ^ swz_k(t)));
+        } else if constexpr (ES == 1) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(row + 16 * ((2 * s + (g >> 1)) ^ swz_k(t)) + 8 * (g & 1));
+            return codes_to_bf16(w.x, w.y);
+        } else {
+            const f32x4 x = *reinterpret_cast<const f32x4 *>(row + 16 * ((8 * s + 2 * g) ^ swz_k(t)));
+            const f32x4 y = *reinterpret_cast<const f32x4 *>(row + 16 * ((8 * s + 2 * g + 1) ^ swz_k(t)));
+            return (f32x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+        }
+    }
+    // V^T: channel 16 d + l % 16, tokens 4 g + 0..3 and 16 + 4 g + 0..3
+    __device__ __forceinline__ Frag v_frag(const char *lv, int d, int lane) const {
+        const int i = lane & 15, g = lane >> 4;
+        if constexpr (ES == 2) {
+            typedef __attribute__((address_space(3))) i16x4 lds4;
+            const int t = 4 * g + (i >> 2), c = 2 * d + ((i >> 1) & 1);
+            const char *p = lv + t * (V * 2) + 16 * (c ^ swz_v(t)) + 8 * (i & 1);
+            const char *p2 = lv + (t + 16) * (V * 2) + 16 * (c ^ swz_v(t + 16)) + 8 * (i & 1);
+            const bf16x4 x = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p));
+            const bf16x4 y = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p2));
+            return (bf16x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+        } else if constexpr (ES == 1) {
+            typedef __attribute__((address_space(3))) i32x2 lds2;
+            const int r = i >> 1, t = (r & 3) + 4 * g + (r >> 2) * 16;
+            const char *p = lv + t * V + 16 * (d ^ swz_v(t)) + 8 * (i & 1);
+            const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds2 *)p);
+            return codes_to_bf16(w[0], w[1]);
+        } else {
+            f32x8 x;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int t = (j & 3) + 4 * g + (j >> 2) * 16, ch = 16 * d + i;
+                x[j] = *reinterpret_cast<const float *>(lv + t * (V * 4) + 16 * ((ch >> 2) ^ swz_v(t)) + 4 * (ch & 3));
+            }
+            return x;
+        }
+    }
+    // channels 16 d + 4 g + 0..3 of token t, as floats (the slow product below)
+    __device__ __forceinline__ f32x4 v_row(const char *lv, int t, int d, int lane) const {
+        const int ch = 16 * d + 4 * (lane >> 4), byte = ch * ES;
+        const char *p = lv + t * (V * ES) + 16 * ((byte >> 4) ^ swz_v(t)) + (byte & 15);
+        if constexpr (ES == 4) return *reinterpret_cast<const f32x4 *>(p);
+        if constexpr (ES == 2) {
+            const float4 x = io<bf16_t>::load4(reinterpret_cast<const bf16_t *>(p));
+            return (f32x4){x.x, x.y, x.z, x.w};
+        }
+        const bf16x8 x = codes_to_bf16(*reinterpret_cast<const uint32_t *>(p), 0);
+        return (f32x4){static_cast<float>(x[0]), static_cast<float>(x[1]), static_cast<float>(x[2]), static_cast<float>(x[3])};
+    }
+
+    // One step over the 32 staged tokens. sees[i] bit (4 b + j): row l % 16 of block i sees
+    // token 16 b + 4 g + j (read only when masked). e: exponents of these tokens.
+    __device__ __forceinline__ void step(const char *lk, const char *lv, float c, bool masked, const uint32_t (&sees)[RT],
+                                         bool odd, const uint32_t (&kx)[2], const uint32_t (&vx)[2], int lane) {
+        f32x4 s[2][RT];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i) s[b][i] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < KT; ++ks) {
+                const Frag kf = k_frag(lk, b, ks, lane);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) s[b][i] = mma16(kf, q[i][ks], s[b][i]);
+            }
+        }
+        Frag p[RT];
+        float pf[RT][8];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] = s[j >> 2][i][j & 3] * c;
+                if (kCodes) x[j] = scaled_by(x[j], kx[j >> 2], j & 3);
+                if (masked) x[j] = (sees[i] >> j) & 1u ? x[j] : -INFINITY;
+            }
+            float t = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+            t = swap32_max(swap16_max(t));
+            // The reference m only has to keep 2^(s - m) in range, so it moves when the
+            // step's maximum passes it by more than 2^8, not at every step.
+            if (__any(t > m[i] + 8.f)) {
+                const float mn = fmaxf(m[i], t);
+                const float f = mn == -INFINITY ? 1.f : exp2f(m[i] - mn);
+                m[i] = mn;
+                l[i] *= f;
+#pragma unroll
+                for (int d = 0; d < VT; ++d) o[d][i] *= f;
+            }
+            const float ref = m[i] == -INFINITY ? 0.f : m[i];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                pf[i][j] = __builtin_amdgcn_exp2f(x[j] - ref);
+                l[i] += pf[i][j];
+                if (kCodes) pf[i][j] = scaled_by(pf[i][j], vx[j >> 2], j & 3);
+            }
+            p[i] = to_frag(pf[i], Frag{});
+        }
+        if (!odd) {
+#pragma unroll
+            for (int d = 0; d < VT; ++d) {
+                const Frag vf = v_frag(lv, d, lane);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) o[d][i] = mma16(vf, p[i], o[d][i]);
+            }
+            return;
+        }
+        // An infinity or NaN among values that some row does not see: a zero weight would
+        // not keep it out of a matrix product, so each token is added to the rows that see it.
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+#pragma unroll 1
+            for (int g = 0; g < 4; ++g) {
+                const int t = 16 * (j >> 2) + 4 * g + (j & 3), src = 16 * g + (lane & 15);
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    const float w = __shfl(pf[i][j], src);
+                    const uint32_t see = __shfl(sees[i], src);
+#pragma unroll
+                    for (int d = 0; d < VT; ++d) {
+                        const f32x4 x = v_row(lv, t, d, lane);
+                        if ((see >> j) & 1u) o[d][i] += x * w;
+                    }
+                }
+            }
+        }
+    }
+
+    // Which tokens the lane's rows see in a masked step: positions before `ctx`, and new
+    // token b = position - ctx if bit b of the row's mask is set or, without a mask, b <= own.
+    // Positions from `end` on, and pages that are not there, are seen by none.
+    __device__ __forceinline__ void visible(uint32_t (&sees)[RT], const AttnArgs &a, int start, int r0, int rows, int p0,
+                                            int ctx, int end, const bool (&here)[2], int lane) const {
+        const int g = lane >> 4;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const int tok = (r0 + min(16 * i + (lane & 15), rows - 1)) / a.G;
+            const uint64_t bits = a.mask ? a.mask[start + tok] : 0;
+            uint32_t v = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int pos = p0 + 16 * (j >> 2) + 4 * g + (j & 3), b = pos - ctx;
+                bool see = b < 0 || (a.mask ? b < 64 && ((bits >> (b & 63)) & 1u) : b <= tok);
+                see = see && pos < end && here[j >> 2];
+                v |= static_cast<uint32_t>(see) << j;
+            }
+            sees[i] = v;
+        }
+    }
+
+    // Join the four waves' results and hand out rows: put(row in tile, channel, sum m, float4 of
+    // unnormalised outputs, l). Every thread of the workgroup calls it.
+    template <typename Put>
+    __device__ __forceinline__ void join(char *lds, float (&stat)[2][kWaves][R], int w, int lane, int rows, Put put) {
+        const int r = lane & 15, g = lane >> 4, tid = w * 64 + lane;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            l[i] = swap32_sum(swap16_sum(l[i]));
+            if (g == 0) stat[0][w][16 * i + r] = m[i];
+        }
+        __syncthreads();
+        float f[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            float mm = stat[0][0][16 * i + r];
+#pragma unroll
+            for (int u = 1; u < kWaves; ++u) mm = fmaxf(mm, stat[0][u][16 * i + r]);
+            f[i] = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mm);
+            // a wave that saw nothing of a row holds zeros for it; f keeps NaN and infinity as they are
+            if (g == 0) stat[1][w][16 * i + r] = l[i] * f[i];
+        }
+        float *tile = reinterpret_cast<float *>(lds);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            if (16 * i < rows) {
+#pragma unroll
+                for (int d = 0; d < VT; ++d)
+                    *reinterpret_cast<f32x4 *>(tile + (w * 16 + r) * kJoinRow + 16 * d + 4 * g) = o[d][i] * f[i];
+            }
+            __syncthreads();
+            if (16 * i < rows) {
+                for (int e = tid; e < 16 * (V / 4); e += 64 * kWaves) {
+                    const int rr = e / (V / 4), ch = 4 * (e % (V / 4)), row = 16 * i + rr;
+                    if (row < rows) {
+                        f32x4 x = *reinterpret_cast<const f32x4 *>(tile + rr * kJoinRow + ch);
+                        float mm = stat[0][0][row], ll = stat[1][0][row];
+#pragma unroll
+                        for (int u = 1; u < kWaves; ++u) {
+                            x += *reinterpret_cast<const f32x4 *>(tile + (u * 16 + rr) * kJoinRow + ch);
+                            mm = fmaxf(mm, stat[0][u][row]);
+                            ll += stat[1][u][row];
+                        }
+                        put(row, ch, mm, x, ll);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+    }
+};
+
+// o of one row: channels ch .. ch + 3 of row r of a tile
+__device__ __forceinline__ void store_out(const AttnArgs &a, int start, int kvh, int r, int ch, f32x4 x, float l) {
+    const int tok = r / a.G, h = kvh * a.G + (r - tok * a.G);
+    const int64_t at = (static_cast<int64_t>(start + tok) * a.H + h) * a.V + ch;
+    // l is 0 only where nothing was seen; each output is one division
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (l == 0.f) x = (f32x4){0.f, 0.f, 0.f, 0.f};
+    x *= inv;
+    if (a.out_dtype == KDA_BF16) {
+        const bf16x2 lo = pack_bf16(x[0], x[1]), hi = pack_bf16(x[2], x[3]);
+        *reinterpret_cast<bf16x4 *>(static_cast<bf16_t *>(a.o) + at) = (bf16x4){lo[0], lo[1], hi[0], hi[1]};
+    } else {
+        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.o) + at) = x;
+    }
+}
+
+}  // namespace kda
