@@ -50,17 +50,272 @@ __global__ __launch_bounds__(64 * kWaves) void attn_prompt_kernel(AttnArgs a, in
     });
 }
 
-template <int K, int V, int RT, typename TC>
-hipError_t launch_rt(const AttnArgs &a, hipStream_t st) {
+// ---- bf16
+//
+// NW waves of 32 rows each share a tile of 64 keys and values in LDS, copied
+// there directly from memory one tile ahead (two buffers). 32 x 32 matrix
+// instructions, 16-deep: S^T = K Q^T leaves the scores of row l % 32 for tokens
+// 32 b + 8 (i / 4) + 4 (l / 32) + i % 4 in register i of lane l, and those
+// registers, rounded to bf16, are the B operand of O^T = V^T P^T when V^T's
+// fragments take the tokens in the same order, which the transposing LDS reads
+// do. P never moves between lanes.
+__device__ __forceinline__ f32x16 mma32(bf16x8 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// 16 bytes per lane from `src` to LDS at dst (wave-uniform) + 16 * lane. Unknown to the
+// compiler's wait insertion: awaited by wait_copies() before a barrier.
+__device__ __forceinline__ void copy_to_lds(uint32_t dst, const void *src) {
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src) : "memory");
+}
+__device__ __forceinline__ void wait_copies() { __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+constexpr int kTile = 64;  // tokens per tile
+
+template <int K, int V, int NW> struct Prompt {
+    static constexpr int R = 32 * NW;
+    static constexpr int CK = K / 8, CV = V / 8;            // 16-byte chunks per row
+    static constexpr int KB = kTile * K * 2, VB = kTile * V * 2;
+    static constexpr int NK = KB / (1024 * NW), NV = VB / (1024 * NW);  // copies per wave and tile
+    static constexpr int KS = K / 16, DB = V / 32;
+    static_assert(NK >= 1 && NV >= 1, "a tile is at least one copy per wave");
+
+    // chunk c of token t lies at chunk c ^ swz(t) of its row: the tokens that one read takes
+    // the same chunk of are spread over the banks
+    static __device__ __forceinline__ int swz_k(int t) { return CK == 16 ? t & 15 : (t >> 1) & 7; }
+    static __device__ __forceinline__ int swz_v(int t) { return CV == 16 ? (t & 3) * 4 : ((t >> 1) & 1) * 4; }
+
+    static __device__ __forceinline__ void copy_tile(const AttnArgs &a, uint32_t lk, uint32_t lv, int start, int kvh, int p0,
+                                                     int w, int lane) {
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+            const int e = (i * NW + w) * 64 + lane, t = e / CK, c = (e % CK) ^ swz_k(t);
+            const int64_t row = min(start + p0 + t, a.T - 1);
+            copy_to_lds(lk + (i * NW + w) * 1024, static_cast<const bf16_t *>(a.k) + row * a.ks + kvh * K + 8 * c);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = (i * NW + w) * 64 + lane, t = e / CV, c = (e % CV) ^ swz_v(t);
+            const int64_t row = min(start + p0 + t, a.T - 1);
+            copy_to_lds(lv + (i * NW + w) * 1024, static_cast<const bf16_t *>(a.v) + row * a.vs + kvh * V + 8 * c);
+        }
+    }
+
+    bf16x8 q[KS];
+    f32x16 o[DB], s[2];
+    bf16x8 p[4];
+    float m, l;
+
+    __device__ __forceinline__ void scores(const char *lk, int lane) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            s[b] = f32x16{};
+            const int t = 32 * b + (lane & 31);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(lk + t * (2 * K) + 16 * ((2 * ks + (lane >> 5)) ^ swz_k(t)));
+                s[b] = mma32(kf, q[ks], s[b]);
+            }
+        }
+    }
+
+    // 2^(c s - m) in bf16, the running maximum and sum; `own`: the last position the lane's row sees
+    template <bool MASKED> __device__ __forceinline__ void softmax(float c, int p0, int own, int lane) {
+        if (MASKED) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    s[b][i] = p0 + 32 * b + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) <= own ? s[b][i] * c : -INFINITY;
+        } else {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) s[b] *= c;
+        }
+        float t = fmaxf(s[0][0], s[1][0]);
+#pragma unroll
+        for (int i = 1; i < 16; ++i) t = fmaxf(t, fmaxf(s[0][i], s[1][i]));
+        t = swap32_max(t);
+        // m only has to keep the powers in range: it moves when the tile passes it by more than 2^8
+        if (__any(t > m + 8.f)) {
+            const float mn = fmaxf(m, t);
+            const float f = mn == -INFINITY ? 1.f : exp2f(m - mn);
+            m = mn;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DB; ++d) o[d] *= f;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[b][i] = __builtin_amdgcn_exp2f(s[b][i] - ref);
+                l += s[b][i];
+            }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float e[8] = {s[x >> 1][8 * (x & 1)],     s[x >> 1][8 * (x & 1) + 1], s[x >> 1][8 * (x & 1) + 2],
+                                s[x >> 1][8 * (x & 1) + 3], s[x >> 1][8 * (x & 1) + 4], s[x >> 1][8 * (x & 1) + 5],
+                                s[x >> 1][8 * (x & 1) + 6], s[x >> 1][8 * (x & 1) + 7]};
+            p[x] = to_frag(e, bf16x8{});
+        }
+    }
+
+    // channels 32 d + l % 32, tokens 16 x + {0..3, 8..11} + 4 (l / 32)
+    static __device__ __forceinline__ bf16x8 v_frag(const char *lv, int x, int d, int lane) {
+        typedef __attribute__((address_space(3))) i16x4 lds4;
+        const int i = lane & 15, t = 16 * x + 4 * (lane >> 5) + (i >> 2);
+        const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
+        const char *at = lv + t * (2 * V) + 16 * (c ^ swz_v(t)) + 8 * (i & 1);
+        const char *at2 = lv + (t + 8) * (2 * V) + 16 * (c ^ swz_v(t + 8)) + 8 * (i & 1);
+        const bf16x4 y = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)at));
+        const bf16x4 z = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)at2));
+        return (bf16x8){y[0], y[1], y[2], y[3], z[0], z[1], z[2], z[3]};
+    }
+
+    __device__ __forceinline__ void values(const char *lv, int lane) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int d = 0; d < DB; ++d) o[d] = mma32(v_frag(lv, x, d, lane), p[x], o[d]);
+    }
+
+    // The same where some rows do not see some tokens: 16 tokens that no row of the wave sees
+    // take no part (they may lie behind the sequence), and where one of 16 that some row does
+    // not see holds an infinity or NaN, a weight of zero would not keep it out of a product, so
+    // each token is added to the rows that see it.
+    __device__ __forceinline__ void values_masked(const char *lv, int p0, int own, int tok0, int tok1, int lane) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (p0 + 16 * x > tok1) break;
+            bf16x8 vf[DB];
+            bool odd = false;
+#pragma unroll
+            for (int d = 0; d < DB; ++d) vf[d] = v_frag(lv, x, d, lane);
+            if (p0 + 16 * x + 15 > tok0) {
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    const u32x4 u = __builtin_bit_cast(u32x4, vf[d]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) odd |= not_finite<bf16_t>(u[j]);
+                }
+            }
+            if (!__any(odd)) {
+#pragma unroll
+                for (int d = 0; d < DB; ++d) o[d] = mma32(vf[d], p[x], o[d]);
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const int t = 16 * x + 8 * (j >> 2) + 4 * h + (j & 3);
+                    const float w = __shfl(s[x >> 1][8 * (x & 1) + j], 32 * h + (lane & 31));
+                    if (p0 + t > own) continue;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int ch = 32 * d + 8 * i + 4 * (lane >> 5);
+                            const float4 y = io<bf16_t>::load4(reinterpret_cast<const bf16_t *>(
+                                lv + t * (2 * V) + 16 * ((ch >> 3) ^ swz_v(t)) + 2 * (ch & 7)));
+                            o[d][4 * i] = fmaf(w, y.x, o[d][4 * i]);
+                            o[d][4 * i + 1] = fmaf(w, y.y, o[d][4 * i + 1]);
+                            o[d][4 * i + 2] = fmaf(w, y.z, o[d][4 * i + 2]);
+                            o[d][4 * i + 3] = fmaf(w, y.w, o[d][4 * i + 3]);
+                        }
+                }
+        }
+    }
+};
+
+template <int K, int V, int NW>
+__global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a, int slots) {
+    using P = Prompt<K, V, NW>;
+    __shared__ __align__(1024) char lds[2 * (P::KB + P::VB)];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    const int kvh = blockIdx.x % a.Hk;
+    const int64_t slot = slots - 1 - static_cast<int>(blockIdx.x / a.Hk);  // the longest first
+    const int n = seq_of_slot(a.cu, a.N, a.T, a.G, P::R, slot);
+    int start, count;
+    seq_rows(a.cu, n, a.T, start, count);
+    const int64_t first = (slot - static_cast<int64_t>(start) * a.G / P::R - n) * P::R;
+    const int64_t all = static_cast<int64_t>(count) * a.G;
+    if (first < 0 || first >= all) return;
+    const int last = static_cast<int>((min(first + P::R, all) - 1) / a.G);  // last token of the tile
+
+    // this wave's rows; rows past the sequence's repeat its last one and are not stored
+    const int64_t wr0 = first + 32 * w, wr1 = min(wr0 + 32, all);
+    const bool some = wr0 < all;
+    const int tok0 = static_cast<int>(min(wr0, all - 1) / a.G), tok1 = static_cast<int>((max(wr1, static_cast<int64_t>(1)) - 1) / a.G);
+    const int64_t row = min(wr0 + (lane & 31), all - 1);
+    const int own = static_cast<int>(row / a.G), h = kvh * a.G + static_cast<int>(row - static_cast<int64_t>(own) * a.G);
+
+    P st;
+    {
+        const bf16_t *src = static_cast<const bf16_t *>(a.q) + static_cast<int64_t>(start + own) * a.qs + h * K + 8 * (lane >> 5);
+#pragma unroll
+        for (int ks = 0; ks < P::KS; ++ks) st.q[ks] = load_frag(src + 16 * ks);
+    }
+    st.m = -INFINITY;
+    st.l = 0.f;
+#pragma unroll
+    for (int d = 0; d < P::DB; ++d) st.o[d] = f32x16{};
+
+    const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char *)lds));
+    P::copy_tile(a, base, base + P::KB, start, kvh, 0, w, lane);
+    int buf = 0;
+    for (int p0 = 0; p0 <= last; p0 += kTile, buf ^= P::KB + P::VB) {
+        wait_copies();
+        __syncthreads();  // the tile is there for all waves, and all are done with the other buffer
+        if (p0 + kTile <= last) {
+            const uint32_t nb = base + (buf ^ (P::KB + P::VB));
+            P::copy_tile(a, nb, nb + P::KB, start, kvh, p0 + kTile, w, lane);
+        }
+        if (!some || p0 > tok1) continue;
+        const char *lk = lds + buf, *lv = lk + P::KB;
+        st.scores(lk, lane);
+        if (p0 + kTile - 1 > tok0) {
+            st.template softmax<true>(a.c, p0, own, lane);
+            st.values_masked(lv, p0, own, tok0, tok1, lane);
+        } else {
+            st.template softmax<false>(a.c, p0, own, lane);
+            st.values(lv, lane);
+        }
+    }
+    if (wr0 + (lane & 31) >= all) return;
+    const float l = swap32_sum(st.l);
+#pragma unroll
+    for (int d = 0; d < P::DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            store_out(a, start, kvh, static_cast<int>(row), 32 * d + 8 * i + 4 * (lane >> 5),
+                      (f32x4){st.o[d][4 * i], st.o[d][4 * i + 1], st.o[d][4 * i + 2], st.o[d][4 * i + 3]}, l);
+}
+
+template <int K, int V, int NW> hipError_t launch_bf16(const AttnArgs &a, hipStream_t st) {
+    const int64_t slots = static_cast<int64_t>(a.T) * a.G / (32 * NW) + a.N;
+    hipLaunchKernelGGL((attn_prompt_bf16_kernel<K, V, NW>), dim3(static_cast<unsigned>(slots * a.Hk)), dim3(64 * NW), 0, st, a,
+                       static_cast<int>(slots));
+    return hipGetLastError();
+}
+
+template <int K, int V, int RT>
+hipError_t launch_f32(const AttnArgs &a, hipStream_t st) {
     const int64_t slots = static_cast<int64_t>(a.T) * a.G / (16 * RT) + a.N;
-    hipLaunchKernelGGL((attn_prompt_kernel<K, V, RT, TC>), dim3(static_cast<unsigned>(slots * a.Hk)), dim3(64 * kWaves), 0, st,
+    hipLaunchKernelGGL((attn_prompt_kernel<K, V, RT, float>), dim3(static_cast<unsigned>(slots * a.Hk)), dim3(64 * kWaves), 0, st,
                        a, static_cast<int>(slots));
     return hipGetLastError();
 }
 
 template <int K, int V> hipError_t launch_dims(const AttnArgs &a, hipStream_t st) {
-    if (a.in_dtype == KDA_F32) return launch_rt<K, V, 2, float>(a, st);
-    return launch_rt<K, V, 4, bf16_t>(a, st);
+    if (a.in_dtype == KDA_F32) return launch_f32<K, V, 2>(a, st);
+#ifdef KDA_NW
+    return launch_bf16<K, V, KDA_NW>(a, st);
+#else
+    return launch_bf16<K, V, 8>(a, st);
+#endif
 }
 
 }  // namespace
