@@ -70,6 +70,21 @@ __device__ __forceinline__ void copy_to_lds(uint32_t dst, const void *src) {
 }
 __device__ __forceinline__ void wait_copies() { __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
+// One instruction, where fmaxf of two would first make quiet NaNs of its operands. A NaN
+// operand is passed over, as by fmaxf.
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    __asm__("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
+    return r;
+}
+
+// A workgroup barrier that nothing is moved across, without waiting for copies.
+__device__ __forceinline__ void phase_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    __asm__ volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 constexpr int kTile = 64;  // tokens per tile
 
 template <int K, int V, int NW> struct Prompt {
@@ -85,19 +100,21 @@ template <int K, int V, int NW> struct Prompt {
     static __device__ __forceinline__ int swz_k(int t) { return CK == 16 ? t & 15 : (t >> 1) & 7; }
     static __device__ __forceinline__ int swz_v(int t) { return CV == 16 ? (t & 3) * 4 : ((t >> 1) & 1) * 4; }
 
-    static __device__ __forceinline__ void copy_tile(const AttnArgs &a, uint32_t lk, uint32_t lv, int start, int kvh, int p0,
-                                                     int w, int lane) {
+    // rows p0 .. p0 + 63 of the sequence's keys (values) to LDS
+    static __device__ __forceinline__ void copy_k(const AttnArgs &a, uint32_t dst, int start, int kvh, int p0, int w, int lane) {
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
             const int e = (i * NW + w) * 64 + lane, t = e / CK, c = (e % CK) ^ swz_k(t);
             const int64_t row = min(start + p0 + t, a.T - 1);
-            copy_to_lds(lk + (i * NW + w) * 1024, static_cast<const bf16_t *>(a.k) + row * a.ks + kvh * K + 8 * c);
+            copy_to_lds(dst + (i * NW + w) * 1024, static_cast<const bf16_t *>(a.k) + row * a.ks + kvh * K + 8 * c);
         }
+    }
+    static __device__ __forceinline__ void copy_v(const AttnArgs &a, uint32_t dst, int start, int kvh, int p0, int w, int lane) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int e = (i * NW + w) * 64 + lane, t = e / CV, c = (e % CV) ^ swz_v(t);
             const int64_t row = min(start + p0 + t, a.T - 1);
-            copy_to_lds(lv + (i * NW + w) * 1024, static_cast<const bf16_t *>(a.v) + row * a.vs + kvh * V + 8 * c);
+            copy_to_lds(dst + (i * NW + w) * 1024, static_cast<const bf16_t *>(a.v) + row * a.vs + kvh * V + 8 * c);
         }
     }
 
@@ -119,22 +136,25 @@ template <int K, int V, int NW> struct Prompt {
         }
     }
 
-    // 2^(c s - m) in bf16, the running maximum and sum; `own`: the last position the lane's row sees
+    // 2^(c s - m) in bf16, the running maximum and sum (c >= 0: q carries the scale's sign);
+    // `own`: the last position the lane's row sees
     template <bool MASKED> __device__ __forceinline__ void softmax(float c, int p0, int own, int lane) {
         if (MASKED) {
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    s[b][i] = p0 + 32 * b + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) <= own ? s[b][i] * c : -INFINITY;
-        } else {
-#pragma unroll
-            for (int b = 0; b < 2; ++b) s[b] *= c;
+                    if (p0 + 32 * b + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3) > own) s[b][i] = -INFINITY;
         }
-        float t = fmaxf(s[0][0], s[1][0]);
+        float t = max3(s[0][0], s[1][0], s[0][1]), u = max3(s[1][1], s[0][2], s[1][2]);
 #pragma unroll
-        for (int i = 1; i < 16; ++i) t = fmaxf(t, fmaxf(s[0][i], s[1][i]));
-        t = swap32_max(t);
+        for (int i = 3; i < 15; i += 2) {
+            t = max3(t, s[0][i], s[1][i]);
+            u = max3(u, s[0][i + 1], s[1][i + 1]);
+        }
+        t = max3(t, s[0][15], s[1][15]);
+        t = swap32_max(fmaxf(t, u));
+        t = t == -INFINITY ? t : t * c;  // a scale of 0 leaves "nothing seen" as it is
         // m only has to keep the powers in range: it moves when the tile passes it by more than 2^8
         if (__any(t > m + 8.f)) {
             const float mn = fmaxf(m, t);
@@ -145,18 +165,22 @@ template <int K, int V, int NW> struct Prompt {
             for (int d = 0; d < DB; ++d) o[d] *= f;
         }
         const float ref = m == -INFINITY ? 0.f : m;
+        float sum[2] = {0.f, 0.f};
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                s[b][i] = __builtin_amdgcn_exp2f(s[b][i] - ref);
-                l += s[b][i];
+                // with a scale of 0, -infinity would be 0 * infinity
+                const float x = MASKED && s[b][i] == -INFINITY ? -INFINITY : fmaf(s[b][i], c, -ref);
+                s[b][i] = __builtin_amdgcn_exp2f(x);
+                sum[i & 1] += s[b][i];
             }
+        l += sum[0] + sum[1];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const float e[8] = {s[x >> 1][8 * (x & 1)],     s[x >> 1][8 * (x & 1) + 1], s[x >> 1][8 * (x & 1) + 2],
-                                s[x >> 1][8 * (x & 1) + 3], s[x >> 1][8 * (x & 1) + 4], s[x >> 1][8 * (x & 1) + 5],
-                                s[x >> 1][8 * (x & 1) + 6], s[x >> 1][8 * (x & 1) + 7]};
+            float e[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] = s[x >> 1][8 * (x & 1) + j];
             p[x] = to_frag(e, bf16x8{});
         }
     }
@@ -205,26 +229,28 @@ template <int K, int V, int NW> struct Prompt {
                 for (int d = 0; d < DB; ++d) o[d] = mma32(vf[d], p[x], o[d]);
                 continue;
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    const int t = 16 * x + 8 * (j >> 2) + 4 * h + (j & 3);
-                    const float w = __shfl(s[x >> 1][8 * (x & 1) + j], 32 * h + (lane & 31));
-                    if (p0 + t > own) continue;
+            for (int j = 0; j < 16; ++j) {  // token 16 x + j: in the lanes of half (j / 4) % 2
+                float w = 0.f;
 #pragma unroll
-                    for (int d = 0; d < DB; ++d)
+                for (int i = 0; i < 8; ++i)
+                    if (i == (j >> 3) * 4 + (j & 3)) w = s[x >> 1][8 * (x & 1) + i];
+                w = __shfl(w, 32 * ((j >> 2) & 1) + (lane & 31));
+                const int t = 16 * x + j;
+                if (p0 + t > own) continue;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int ch = 32 * d + 8 * i + 4 * (lane >> 5);
-                            const float4 y = io<bf16_t>::load4(reinterpret_cast<const bf16_t *>(
-                                lv + t * (2 * V) + 16 * ((ch >> 3) ^ swz_v(t)) + 2 * (ch & 7)));
-                            o[d][4 * i] = fmaf(w, y.x, o[d][4 * i]);
-                            o[d][4 * i + 1] = fmaf(w, y.y, o[d][4 * i + 1]);
-                            o[d][4 * i + 2] = fmaf(w, y.z, o[d][4 * i + 2]);
-                            o[d][4 * i + 3] = fmaf(w, y.w, o[d][4 * i + 3]);
-                        }
-                }
+                for (int d = 0; d < DB; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int ch = 32 * d + 8 * i + 4 * (lane >> 5);
+                        const float4 y = io<bf16_t>::load4(reinterpret_cast<const bf16_t *>(
+                            lv + t * (2 * V) + 16 * ((ch >> 3) ^ swz_v(t)) + 2 * (ch & 7)));
+                        o[d][4 * i] = fmaf(w, y.x, o[d][4 * i]);
+                        o[d][4 * i + 1] = fmaf(w, y.y, o[d][4 * i + 1]);
+                        o[d][4 * i + 2] = fmaf(w, y.z, o[d][4 * i + 2]);
+                        o[d][4 * i + 3] = fmaf(w, y.w, o[d][4 * i + 3]);
+                    }
+            }
         }
     }
 };
@@ -256,33 +282,75 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
     {
         const bf16_t *src = static_cast<const bf16_t *>(a.q) + static_cast<int64_t>(start + own) * a.qs + h * K + 8 * (lane >> 5);
 #pragma unroll
-        for (int ks = 0; ks < P::KS; ++ks) st.q[ks] = load_frag(src + 16 * ks);
+        for (int ks = 0; ks < P::KS; ++ks) {
+            st.q[ks] = load_frag(src + 16 * ks);
+            if (a.c < 0.f) st.q[ks] = -st.q[ks];
+        }
     }
+    const float c = fabsf(a.c);
     st.m = -INFINITY;
     st.l = 0.f;
 #pragma unroll
     for (int d = 0; d < P::DB; ++d) st.o[d] = f32x16{};
 
     const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char *)lds));
-    P::copy_tile(a, base, base + P::KB, start, kvh, 0, w, lane);
-    int buf = 0;
-    for (int p0 = 0; p0 <= last; p0 += kTile, buf ^= P::KB + P::VB) {
+    // LDS: keys of even and odd tiles, values of even and odd tiles
+    auto lk = [&](int j) { return (j & 1) * P::KB; };
+    auto lv = [&](int j) { return 2 * P::KB + (j & 1) * P::VB; };
+    auto copy_k = [&](int j) {
+        if (j * kTile <= last) P::copy_k(a, base + lk(j), start, kvh, j * kTile, w, lane);
+    };
+    auto copy_v = [&](int j) {
+        if (j * kTile <= last) P::copy_v(a, base + lv(j), start, kvh, j * kTile, w, lane);
+    };
+    // Tiles that every row of the workgroup sees whole. The two waves of a SIMD take turns: one
+    // is in its products (the values of the tile before, the scores of this one) while the other
+    // is in its softmax, and every barrier swaps them. Copies for a tile are issued two turns
+    // before its first use, which is when the last reader of that buffer has gone.
+    const int J = (static_cast<int>(first / a.G) + 1) / kTile;
+    const bool ahead = w < NW / 2;
+    copy_k(0);
+    if (J > 0) {
         wait_copies();
-        __syncthreads();  // the tile is there for all waves, and all are done with the other buffer
-        if (p0 + kTile <= last) {
-            const uint32_t nb = base + (buf ^ (P::KB + P::VB));
-            P::copy_tile(a, nb, nb + P::KB, start, kvh, p0 + kTile, w, lane);
+        phase_barrier();
+        if (!ahead) {
+            copy_k(1);
+            copy_v(0);
+            phase_barrier();
         }
+        for (int j = 0; j < J; ++j) {
+            if (ahead) {
+                copy_k(j + 1);
+                copy_v(j);
+            }
+            if (j > 0) st.values(lds + lv(j - 1), lane);
+            st.scores(lds + lk(j), lane);
+            if (!ahead) wait_copies();
+            phase_barrier();
+            if (!ahead) {
+                if (j + 1 < J) copy_k(j + 2);
+                copy_v(j + 1);
+            }
+            st.template softmax<false>(c, 0, own, lane);
+            if (ahead) wait_copies();
+            phase_barrier();
+        }
+        if (ahead) copy_v(J);
+        st.values(lds + lv(J - 1), lane);
+        if (ahead) phase_barrier();
+    } else {
+        copy_v(0);
+    }
+    for (int j = J; j * kTile <= last; ++j) {
+        const int p0 = j * kTile;
+        wait_copies();
+        phase_barrier();  // the tile is there for all waves, and all are done with the other buffers
+        copy_k(j + 1);
+        copy_v(j + 1);
         if (!some || p0 > tok1) continue;
-        const char *lk = lds + buf, *lv = lk + P::KB;
-        st.scores(lk, lane);
-        if (p0 + kTile - 1 > tok0) {
-            st.template softmax<true>(a.c, p0, own, lane);
-            st.values_masked(lv, p0, own, tok0, tok1, lane);
-        } else {
-            st.template softmax<false>(a.c, p0, own, lane);
-            st.values(lv, lane);
-        }
+        st.scores(lds + lk(j), lane);
+        st.template softmax<true>(c, p0, own, lane);
+        st.values_masked(lds + lv(j), p0, own, tok0, tok1, lane);
     }
     if (wr0 + (lane & 31) >= all) return;
     const float l = swap32_sum(st.l);
