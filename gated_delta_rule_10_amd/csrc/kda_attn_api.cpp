@@ -21,7 +21,7 @@ bool dtype_pair_ok(kda_dtype_t in, kda_dtype_t out) { return in == KDA_BF16 || o
 bool kv_pair_ok(kda_dtype_t in, kda_kv_dtype_t kv) { return (in == KDA_F32) == (kv == KDA_KV_F32); }
 
 bool stride_ok(int64_t stride, int64_t heads, int32_t d) {
-    return stride >= heads * d && stride % 8 == 0 && stride <= (int64_t(1) << 40);
+    return stride >= heads * d && stride % 8 == 0 && stride <= (int64_t(1) << 24);
 }
 
 // Sizes shared by all entry points. d_k and d_v are checked separately (KDA_ERR_UNSUPPORTED).

@@ -63,10 +63,10 @@ __device__ __forceinline__ f32x16 mma32(bf16x8 a, bf16x8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// 16 bytes per lane from `src` to LDS at dst (wave-uniform) + 16 * lane. Unknown to the
+// 16 bytes per lane from base (wave-uniform) + off to LDS at dst (wave-uniform) + 16 * lane. Unknown to the
 // compiler's wait insertion: awaited by wait_copies() before a barrier.
-__device__ __forceinline__ void copy_to_lds(uint32_t dst, const void *src) {
-    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src) : "memory");
+__device__ __forceinline__ void copy_to_lds(uint32_t dst, const void *base, uint32_t off) {
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void wait_copies() { __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
@@ -100,21 +100,19 @@ template <int K, int V, int NW> struct Prompt {
     static __device__ __forceinline__ int swz_k(int t) { return CK == 16 ? t & 15 : (t >> 1) & 7; }
     static __device__ __forceinline__ int swz_v(int t) { return CV == 16 ? (t & 3) * 4 : ((t >> 1) & 1) * 4; }
 
-    // rows p0 .. p0 + 63 of the sequence's keys (values) to LDS
-    static __device__ __forceinline__ void copy_k(const AttnArgs &a, uint32_t dst, int start, int kvh, int p0, int w, int lane) {
+    // 64 rows of keys or values (D channels, `stride` elements apart) to LDS. `row`: the first
+    // one's index among the T rows; past the last row the last one is copied.
+    template <int D, bool KEYS>
+    static __device__ __forceinline__ void copy_rows(uint32_t dst, const bf16_t *src, int64_t stride, int row, int T, int w, int lane) {
+        constexpr int C = D / 8, N = kTile * D * 2 / (1024 * NW);
+        const int left = T - 1 - row;  // of the tile's rows after the first
+        const bf16_t *base = src + row * stride;
 #pragma unroll
-        for (int i = 0; i < NK; ++i) {
-            const int e = (i * NW + w) * 64 + lane, t = e / CK, c = (e % CK) ^ swz_k(t);
-            const int64_t row = min(start + p0 + t, a.T - 1);
-            copy_to_lds(dst + (i * NW + w) * 1024, static_cast<const bf16_t *>(a.k) + row * a.ks + kvh * K + 8 * c);
-        }
-    }
-    static __device__ __forceinline__ void copy_v(const AttnArgs &a, uint32_t dst, int start, int kvh, int p0, int w, int lane) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int e = (i * NW + w) * 64 + lane, t = e / CV, c = (e % CV) ^ swz_v(t);
-            const int64_t row = min(start + p0 + t, a.T - 1);
-            copy_to_lds(dst + (i * NW + w) * 1024, static_cast<const bf16_t *>(a.v) + row * a.vs + kvh * V + 8 * c);
+        for (int i = 0; i < N; ++i) {
+            const int e = (i * NW + w) * 64 + lane, t = e / C, c = (e % C) ^ (KEYS ? swz_k(t) : swz_v(t));
+            // 64 rows are less than 2^31 bytes: strides are at most 2^24 elements
+            const uint32_t off = 2 * (static_cast<uint32_t>(left >= kTile - 1 ? t : min(t, left)) * static_cast<uint32_t>(stride) + 8 * c);
+            copy_to_lds(dst + (i * NW + w) * 1024, base, off);
         }
     }
 
@@ -124,16 +122,38 @@ template <int K, int V, int NW> struct Prompt {
     float m, l;
 
     __device__ __forceinline__ void scores(const char *lk, int lane) {
+        s[0] = s[1] = f32x16{};
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            s[b] = f32x16{};
-            const int t = 32 * b + (lane & 31);
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
+            for (int b = 0; b < 2; ++b) {
+                const int t = 32 * b + (lane & 31);
                 const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(lk + t * (2 * K) + 16 * ((2 * ks + (lane >> 5)) ^ swz_k(t)));
                 s[b] = mma32(kf, q[ks], s[b]);
             }
+    }
+
+    // Order of the LDS reads (two per value fragment, one per key fragment) and products of a
+    // values() [if VALUES] and scores() in a row: reads run kAhead products ahead of their use,
+    // which covers their latency. Left to itself the compiler reads right before each product.
+    template <bool VALUES> static __device__ __forceinline__ void interleave() {
+        constexpr int kAhead = 4, PV = VALUES ? 4 * DB : 0, QK = 2 * KS;
+        auto reads = [](int i) { return i < PV ? 2 : i < PV + QK ? 1 : 0; };
+        int first = 0;
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) first += reads(i);
+        group_reads(first);
+#pragma unroll
+        for (int i = 0; i < PV + QK; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            group_reads(reads(i + kAhead));
         }
+    }
+    static __device__ __forceinline__ void group_reads(int n) {
+        if (n >= 8) __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+        else if (n >= 4) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+        else if (n == 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        else if (n == 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
 
     // 2^(c s - m) in bf16, the running maximum and sum (c >= 0: q carries the scale's sign);
@@ -297,18 +317,19 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
     // LDS: keys of even and odd tiles, values of even and odd tiles
     auto lk = [&](int j) { return (j & 1) * P::KB; };
     auto lv = [&](int j) { return 2 * P::KB + (j & 1) * P::VB; };
+    const bf16_t *ksrc = static_cast<const bf16_t *>(a.k) + kvh * K, *vsrc = static_cast<const bf16_t *>(a.v) + kvh * V;
     auto copy_k = [&](int j) {
-        if (j * kTile <= last) P::copy_k(a, base + lk(j), start, kvh, j * kTile, w, lane);
+        if (j * kTile <= last) P::template copy_rows<K, true>(base + lk(j), ksrc, a.ks, start + j * kTile, a.T, w, lane);
     };
     auto copy_v = [&](int j) {
-        if (j * kTile <= last) P::copy_v(a, base + lv(j), start, kvh, j * kTile, w, lane);
+        if (j * kTile <= last) P::template copy_rows<V, false>(base + lv(j), vsrc, a.vs, start + j * kTile, a.T, w, lane);
     };
     // Tiles that every row of the workgroup sees whole. The two waves of a SIMD take turns: one
     // is in its products (the values of the tile before, the scores of this one) while the other
     // is in its softmax, and every barrier swaps them. Copies for a tile are issued two turns
     // before its first use, which is when the last reader of that buffer has gone.
     const int J = (static_cast<int>(first / a.G) + 1) / kTile;
-    const bool ahead = w < NW / 2;
+        const bool ahead = w < NW / 2;
     copy_k(0);
     if (J > 0) {
         wait_copies();
@@ -323,8 +344,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
                 copy_k(j + 1);
                 copy_v(j);
             }
-            if (j > 0) st.values(lds + lv(j - 1), lane);
-            st.scores(lds + lk(j), lane);
+            if (j > 0) {
+                st.values(lds + lv(j - 1), lane);
+                st.scores(lds + lk(j), lane);
+                P::template interleave<true>();
+            } else {
+                st.scores(lds + lk(0), lane);
+                P::template interleave<false>();
+            }
             if (!ahead) wait_copies();
             phase_barrier();
             if (!ahead) {

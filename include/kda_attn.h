@@ -32,7 +32,7 @@
  *  - d_k and d_v are 64 or 128, each on its own.
  *  - q, k and v may be parts of wider rows (a fused projection): element
  *    (t, h, i) is at t * stride + h * d + i, with the token stride in elements,
- *    at least heads * d and a multiple of 8. Outputs are dense.
+ *    at least heads * d, at most 2^24 and a multiple of 8. Outputs are dense.
  *  - cu_seqlens [N + 1] int32: sequence n has rows [cu_seqlens[n],
  *    cu_seqlens[n + 1]) of the packed token axis. Rows from cu_seqlens[N] on
  *    are neither read nor written.
