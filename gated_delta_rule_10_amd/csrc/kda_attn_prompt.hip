@@ -91,30 +91,47 @@ template <int K, int V, int NW> struct Prompt {
     static constexpr int R = 32 * NW;
     static constexpr int CK = K / 8, CV = V / 8;            // 16-byte chunks per row
     static constexpr int KB = kTile * K * 2, VB = kTile * V * 2;
-    static constexpr int NK = KB / (1024 * NW), NV = VB / (1024 * NW);  // copies per wave and tile
     static constexpr int KS = K / 16, DB = V / 32;
-    static_assert(NK >= 1 && NV >= 1, "a tile is at least one copy per wave");
+    static_assert(KB >= 1024 * NW && VB >= 1024 * NW, "a tile is at least one copy per wave");
 
     // chunk c of token t lies at chunk c ^ swz(t) of its row: the tokens that one read takes
     // the same chunk of are spread over the banks
     static __device__ __forceinline__ int swz_k(int t) { return CK == 16 ? t & 15 : (t >> 1) & 7; }
     static __device__ __forceinline__ int swz_v(int t) { return CV == 16 ? (t & 3) * 4 : ((t >> 1) & 1) * 4; }
 
-    // 64 rows of keys or values (D channels, `stride` elements apart) to LDS. `row`: the first
-    // one's index among the T rows; past the last row the last one is copied.
-    template <int D, bool KEYS>
-    static __device__ __forceinline__ void copy_rows(uint32_t dst, const bf16_t *src, int64_t stride, int row, int T, int w, int lane) {
-        constexpr int C = D / 8, N = kTile * D * 2 / (1024 * NW);
-        const int left = T - 1 - row;  // of the tile's rows after the first
-        const bf16_t *base = src + row * stride;
+    // Copies of the tiles of keys or values (D channels), in order: 64 rows from the next one on
+    // to LDS at dst.
+    template <int D, bool KEYS> struct Copier {
+        static constexpr int C = D / 8, N = kTile * D * 2 / (1024 * NW);
+        const bf16_t *next;
+        int64_t stride;
+        int left;         // rows that the packed tensor has from `next` on
+        uint32_t off[N];  // this lane's, for 64 rows that are all there
+
+        __device__ __forceinline__ void begin(const bf16_t *src, int64_t stride_, int row, int T, int w, int lane) {
+            next = src + row * stride_;
+            stride = stride_;
+            left = T - row;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int e = (i * NW + w) * 64 + lane, t = e / C, c = (e % C) ^ (KEYS ? swz_k(t) : swz_v(t));
-            // 64 rows are less than 2^31 bytes: strides are at most 2^24 elements
-            const uint32_t off = 2 * (static_cast<uint32_t>(left >= kTile - 1 ? t : min(t, left)) * static_cast<uint32_t>(stride) + 8 * c);
-            copy_to_lds(dst + (i * NW + w) * 1024, base, off);
+            for (int i = 0; i < N; ++i) off[i] = place(i, kTile - 1, w, lane);
         }
-    }
+        // bytes of chunk i from row 0, rows past `top` replaced by it: less than 2^31, strides are at most 2^24 elements
+        __device__ __forceinline__ uint32_t place(int i, int top, int w, int lane) const {
+            const int e = (i * NW + w) * 64 + lane, t = e / C, c = (e % C) ^ (KEYS ? swz_k(t) : swz_v(t));
+            return 2 * (static_cast<uint32_t>(min(t, top)) * static_cast<uint32_t>(stride) + 8 * c);
+        }
+        __device__ __forceinline__ void tile(uint32_t dst, int w, int lane) {
+            if (left >= kTile) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) copy_to_lds(dst + (i * NW + w) * 1024, next, off[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) copy_to_lds(dst + (i * NW + w) * 1024, next, place(i, left - 1, w, lane));
+            }
+            next += kTile * stride;
+            left -= kTile;
+        }
+    };
 
     bf16x8 q[KS];
     f32x16 o[DB], s[2];
@@ -224,52 +241,57 @@ template <int K, int V, int NW> struct Prompt {
             for (int d = 0; d < DB; ++d) o[d] = mma32(v_frag(lv, x, d, lane), p[x], o[d]);
     }
 
-    // The same where some rows do not see some tokens: 16 tokens that no row of the wave sees
-    // take no part (they may lie behind the sequence), and where one of 16 that some row does
-    // not see holds an infinity or NaN, a weight of zero would not keep it out of a product, so
-    // each token is added to the rows that see it.
+    // The same where some rows do not see some tokens. A weight of zero would not keep an
+    // infinity or NaN out of a product: such values are taken out of the fragments of 16 tokens
+    // that some row does not see, and added to the rows that see them.
     __device__ __forceinline__ void values_masked(const char *lv, int p0, int own, int tok0, int tok1, int lane) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            if (p0 + 16 * x > tok1) break;
+            if (p0 + 16 * x > tok1) continue;  // no row of the wave sees any of the 16
             bf16x8 vf[DB];
-            bool odd = false;
+            uint32_t odd = 0;
 #pragma unroll
-            for (int d = 0; d < DB; ++d) vf[d] = v_frag(lv, x, d, lane);
-            if (p0 + 16 * x + 15 > tok0) {
+            for (int d = 0; d < DB; ++d) {
+                vf[d] = v_frag(lv, x, d, lane);
+                const u32x4 u = __builtin_bit_cast(u32x4, vf[d]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) odd |= (u[i] & 0x7F807F80u) + 0x00800080u;  // an exponent of ones carries
+            }
+            const bool strange = p0 + 16 * x + 15 > tok0 && __any(odd & 0x80008000u);
+            if (strange) {
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
-                    const u32x4 u = __builtin_bit_cast(u32x4, vf[d]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) odd |= not_finite<bf16_t>(u[j]);
-                }
-            }
-            if (!__any(odd)) {
-#pragma unroll
-                for (int d = 0; d < DB; ++d) o[d] = mma32(vf[d], p[x], o[d]);
-                continue;
-            }
-#pragma unroll 1
-            for (int j = 0; j < 16; ++j) {  // token 16 x + j: in the lanes of half (j / 4) % 2
-                float w = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i == (j >> 3) * 4 + (j & 3)) w = s[x >> 1][8 * (x & 1) + i];
-                w = __shfl(w, 32 * ((j >> 2) & 1) + (lane & 31));
-                const int t = 16 * x + j;
-                if (p0 + t > own) continue;
-#pragma unroll
-                for (int d = 0; d < DB; ++d)
+                    u32x4 u = __builtin_bit_cast(u32x4, vf[d]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int ch = 32 * d + 8 * i + 4 * (lane >> 5);
-                        const float4 y = io<bf16_t>::load4(reinterpret_cast<const bf16_t *>(
-                            lv + t * (2 * V) + 16 * ((ch >> 3) ^ swz_v(t)) + 2 * (ch & 7)));
-                        o[d][4 * i] = fmaf(w, y.x, o[d][4 * i]);
-                        o[d][4 * i + 1] = fmaf(w, y.y, o[d][4 * i + 1]);
-                        o[d][4 * i + 2] = fmaf(w, y.z, o[d][4 * i + 2]);
-                        o[d][4 * i + 3] = fmaf(w, y.w, o[d][4 * i + 3]);
+                        const uint32_t t = ((u[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                        u[i] &= ~((t >> 15) * 0xFFFFu);
                     }
+                    vf[d] = __builtin_bit_cast(bf16x8, u);
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < DB; ++d) o[d] = mma32(vf[d], p[x], o[d]);
+            if (strange) {
+#pragma unroll 1
+                for (int j = 0; j < 16; ++j) {  // token 16 x + j: its weights are in the lanes of half (j / 4) % 2
+                    float w = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i == (j >> 3) * 4 + (j & 3)) w = s[x >> 1][8 * (x & 1) + i];
+                    w = __shfl(w, 32 * ((j >> 2) & 1) + (lane & 31));
+                    const int t = 16 * x + j;
+                    const bool see = p0 + t <= own;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int ch = 32 * d + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
+                            const float y = bf16_to_f32(*reinterpret_cast<const bf16_t *>(
+                                lv + t * (2 * V) + 16 * ((ch >> 3) ^ swz_v(t)) + 2 * (ch & 7)));
+                            if (see && !(fabsf(y) < INFINITY)) o[d][i] = fmaf(w, y, o[d][i]);
+                        }
+                }
             }
         }
     }
@@ -317,68 +339,69 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
     // LDS: keys of even and odd tiles, values of even and odd tiles
     auto lk = [&](int j) { return (j & 1) * P::KB; };
     auto lv = [&](int j) { return 2 * P::KB + (j & 1) * P::VB; };
-    const bf16_t *ksrc = static_cast<const bf16_t *>(a.k) + kvh * K, *vsrc = static_cast<const bf16_t *>(a.v) + kvh * V;
-    auto copy_k = [&](int j) {
-        if (j * kTile <= last) P::template copy_rows<K, true>(base + lk(j), ksrc, a.ks, start + j * kTile, a.T, w, lane);
-    };
-    auto copy_v = [&](int j) {
-        if (j * kTile <= last) P::template copy_rows<V, false>(base + lv(j), vsrc, a.vs, start + j * kTile, a.T, w, lane);
-    };
-    // Tiles that every row of the workgroup sees whole. The two waves of a SIMD take turns: one
-    // is in its products (the values of the tile before, the scores of this one) while the other
-    // is in its softmax, and every barrier swaps them. Copies for a tile are issued two turns
-    // before its first use, which is when the last reader of that buffer has gone.
-    const int J = (static_cast<int>(first / a.G) + 1) / kTile;
-        const bool ahead = w < NW / 2;
-    copy_k(0);
-    if (J > 0) {
-        wait_copies();
+    typename P::template Copier<K, true> kc;
+    typename P::template Copier<V, false> vc;
+    kc.begin(static_cast<const bf16_t *>(a.k) + kvh * K, a.ks, start, a.T, w, lane);
+    vc.begin(static_cast<const bf16_t *>(a.v) + kvh * V, a.vs, start, a.T, w, lane);
+    // The two waves of a SIMD take turns: one is in its products (the values of the tile before,
+    // the scores of this one) while the other is in its softmax, and every barrier swaps them.
+    // Copies for a tile are issued two turns before its first use, which is when the last reader
+    // of that buffer has gone. The first J tiles are seen whole by every row of the workgroup.
+    const int J = (static_cast<int>(first / a.G) + 1) / kTile, tiles = last / kTile + 1;
+    const bool ahead = w < NW / 2;
+    auto copy_k = [&](int j) { if (j < tiles) kc.tile(base + lk(j), w, lane); };
+    auto copy_v = [&](int j) { if (j < tiles) vc.tile(base + lv(j), w, lane); };
+    auto swap = [&](bool wait) {
+        if (wait) wait_copies();
         phase_barrier();
-        if (!ahead) {
-            copy_k(1);
-            copy_v(0);
-            phase_barrier();
-        }
-        for (int j = 0; j < J; ++j) {
-            if (ahead) {
-                copy_k(j + 1);
-                copy_v(j);
-            }
-            if (j > 0) {
-                st.values(lds + lv(j - 1), lane);
-                st.scores(lds + lk(j), lane);
-                P::template interleave<true>();
-            } else {
-                st.scores(lds + lk(0), lane);
-                P::template interleave<false>();
-            }
-            if (!ahead) wait_copies();
-            phase_barrier();
-            if (!ahead) {
-                if (j + 1 < J) copy_k(j + 2);
-                copy_v(j + 1);
-            }
-            st.template softmax<false>(c, 0, own, lane);
-            if (ahead) wait_copies();
-            phase_barrier();
-        }
-        if (ahead) copy_v(J);
-        st.values(lds + lv(J - 1), lane);
-        if (ahead) phase_barrier();
-    } else {
+    };
+    auto sees = [&](int j) { return some && j * kTile <= tok1; };  // the wave has work in tile j
+    copy_k(0);
+    swap(true);
+    if (!ahead) {
+        copy_k(1);
         copy_v(0);
+        swap(false);
     }
-    for (int j = J; j * kTile <= last; ++j) {
-        const int p0 = j * kTile;
-        wait_copies();
-        phase_barrier();  // the tile is there for all waves, and all are done with the other buffers
-        copy_k(j + 1);
-        copy_v(j + 1);
-        if (!some || p0 > tok1) continue;
-        st.scores(lds + lk(j), lane);
-        st.template softmax<true>(c, p0, own, lane);
-        st.values_masked(lds + lv(j), p0, own, tok0, tok1, lane);
+    int j = 0;
+    for (; j < J; ++j) {
+        if (ahead) {
+            copy_k(j + 1);
+            copy_v(j);
+        }
+        if (j > 0) {
+            st.values(lds + lv(j - 1), lane);
+            st.scores(lds + lk(j), lane);
+            P::template interleave<true>();
+        } else {
+            st.scores(lds + lk(0), lane);
+            P::template interleave<false>();
+        }
+        swap(!ahead);
+        if (!ahead) {
+            copy_k(j + 2);
+            copy_v(j + 1);
+        }
+        st.template softmax<false>(c, 0, own, lane);
+        swap(ahead);
     }
+    for (; j < tiles; ++j) {
+        if (ahead) {
+            copy_k(j + 1);
+            copy_v(j);
+        }
+        if (j > 0 && sees(j - 1)) st.values_masked(lds + lv(j - 1), (j - 1) * kTile, own, tok0, tok1, lane);
+        if (sees(j)) st.scores(lds + lk(j), lane);
+        swap(!ahead);
+        if (!ahead) {
+            copy_k(j + 2);
+            copy_v(j + 1);
+        }
+        if (sees(j)) st.template softmax<true>(c, j * kTile, own, lane);
+        swap(ahead);
+    }
+    if (sees(j - 1)) st.values_masked(lds + lv(j - 1), (j - 1) * kTile, own, tok0, tok1, lane);
+    if (ahead) swap(false);
     if (wr0 + (lane & 31) >= all) return;
     const float l = swap32_sum(st.l);
 #pragma unroll
