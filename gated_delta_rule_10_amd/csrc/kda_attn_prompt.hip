@@ -321,14 +321,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
     const int own = static_cast<int>(row / a.G), h = kvh * a.G + static_cast<int>(row - static_cast<int64_t>(own) * a.G);
 
     P st;
-    {
-        const bf16_t *src = static_cast<const bf16_t *>(a.q) + static_cast<int64_t>(start + own) * a.qs + h * K + 8 * (lane >> 5);
-#pragma unroll
-        for (int ks = 0; ks < P::KS; ++ks) {
-            st.q[ks] = load_frag(src + 16 * ks);
-            if (a.c < 0.f) st.q[ks] = -st.q[ks];
-        }
-    }
     const float c = fabsf(a.c);
     st.m = -INFINITY;
     st.l = 0.f;
@@ -357,18 +349,32 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
     };
     auto sees = [&](int j) { return some && j * kTile <= tok1; };  // the wave has work in tile j
     copy_k(0);
+    {
+        const bf16_t *src = static_cast<const bf16_t *>(a.q) + static_cast<int64_t>(start + own) * a.qs + h * K + 8 * (lane >> 5);
+#pragma unroll
+        for (int ks = 0; ks < P::KS; ++ks) st.q[ks] = load_frag(src + 16 * ks);
+        const uint32_t sign = a.c < 0.f ? 0x80008000u : 0u;  // a negative scale is q's sign
+#pragma unroll
+        for (int ks = 0; ks < P::KS; ++ks)
+            st.q[ks] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, st.q[ks]) ^ (u32x4){sign, sign, sign, sign});
+    }
     swap(true);
     if (!ahead) {
         copy_k(1);
         copy_v(0);
         swap(false);
     }
+    // The wave in its products issues first where they are the longer turn (two heads of 64
+    // channels have half the products for the same softmax): 7.27 against 7.41 ms for 32768
+    // tokens at 128 channels, and 191 against 188 us for 4 x 4096 at 64.
+    constexpr bool kProductsFirst = K + V > 128;
     int j = 0;
     for (; j < J; ++j) {
         if (ahead) {
             copy_k(j + 1);
             copy_v(j);
         }
+        if (kProductsFirst) __builtin_amdgcn_s_setprio(1);
         if (j > 0) {
             st.values(lds + lv(j - 1), lane);
             st.scores(lds + lk(j), lane);
@@ -377,6 +383,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
             st.scores(lds + lk(0), lane);
             P::template interleave<false>();
         }
+        if (kProductsFirst) __builtin_amdgcn_s_setprio(0);
         swap(!ahead);
         if (!ahead) {
             copy_k(j + 2);
