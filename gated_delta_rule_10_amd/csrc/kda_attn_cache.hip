@@ -4,6 +4,14 @@
 // takes all rows of a (sequence, kv head), the new tokens times the query heads
 // of the group, in tiles of R rows, over a run of steps of 128 cached tokens.
 //
+// Two kernels, by the rows that a (sequence, kv head) has on average:
+//  - up to 16 (single tokens, with the group's heads): the steps of a run are shared out
+//    among the four waves, each of which streams its own tokens without a barrier
+//    (kda_attn_stream.h). fp32 caches take this one for any number of rows.
+//  - more (several or drafted tokens): the waves share each tile of 64 tokens in LDS and
+//    take 32 rows each, up to 128 (kda_attn_rows.h). Tiles are copied to LDS two or more
+//    ahead, two workgroups to a compute unit.
+//
 // Split. Sequences differ in length and only the device knows it, so the steps
 // of all (sequence, kv head, row tile)s are laid on one line and each of W
 // workgroups takes an equal piece of it. A (sequence, kv head, row tile) that
@@ -23,14 +31,14 @@ struct Seq {
     __device__ __forceinline__ int64_t units(int Hk) const { return static_cast<int64_t>(Hk) * tiles * steps; }
 };
 
-__device__ __forceinline__ Seq seq_of(const AttnArgs &a, int n, int R) {
+template <int R, int STEP> __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int n) {
     Seq s;
     seq_rows(a.cu, n, a.T, s.start, s.count);
     const int len = max(ld_meta(a.lens, n), 0);
     s.ctx = len - s.count;
     s.end = min(len, a.max_pages << a.page_shift);
     s.tiles = static_cast<int>((static_cast<int64_t>(s.count) * a.G + R - 1) / R);
-    s.steps = max((s.end + kStep - 1) / kStep, 1);  // at least one, which writes the rows
+    s.steps = max((s.end + STEP - 1) / STEP, 1);  // at least one, which writes the rows
     return s;
 }
 
@@ -60,14 +68,14 @@ __host__ __device__ inline size_t prefix_bytes(int N) { return (static_cast<size
 
 // Total of the line, and the sequence that holds unit u with the units before it. Workgroup-uniform.
 // Every thread of the workgroup calls it. prefix: written if not nullptr.
-template <int R> struct Line {
+template <int R, int STEP> struct Line {
     int64_t total;
     __device__ __forceinline__ void scan(const AttnArgs &a, int tid, int64_t (&sh)[kWaves], int64_t *prefix) {
         const int lane = tid & 63, w = tid >> 6;
         int64_t base = 0;
         for (int n0 = 0; n0 < a.N; n0 += 64 * kWaves) {
             const int n = n0 + tid;
-            const int64_t mine = n < a.N ? seq_of(a, min(n, a.N - 1), R).units(a.Hk) : 0;
+            const int64_t mine = n < a.N ? seq_of<R, STEP>(a, min(n, a.N - 1)).units(a.Hk) : 0;
             const int64_t inc = wave_scan(mine, lane);
             if (lane == 63) sh[w] = inc;
             __syncthreads();
@@ -91,7 +99,7 @@ template <int R> struct Line {
         int64_t base = 0;
         for (int n0 = 0; n0 < a.N; n0 += 64 * kWaves) {
             const int n = n0 + tid;
-            const int64_t mine = n < a.N ? seq_of(a, min(n, a.N - 1), R).units(a.Hk) : 0;
+            const int64_t mine = n < a.N ? seq_of<R, STEP>(a, min(n, a.N - 1)).units(a.Hk) : 0;
             const int64_t inc = wave_scan(mine, lane);
             if (lane == 63) sh[w] = inc;
             __syncthreads();
@@ -127,7 +135,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_cache_kernel(AttnArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     char *lk = lds + w * (S::KB + S::VB), *lv = lk + S::KB;
 
-    Line<R> line;
+    Line<R, kStep> line;
     line.scan(a, tid, sh, blockIdx.x == 0 ? static_cast<int64_t *>(a.ws) : nullptr);
     const int64_t U = line.total;
     if (U == 0) return;
@@ -139,14 +147,14 @@ __global__ __launch_bounds__(64 * kWaves) void attn_cache_kernel(AttnArgs a) {
     int n;
     int64_t before;
     line.find(a, u, tid, sh, n, before, sh_n, sh_before);
-    Seq q = seq_of(a, n, R);
+    Seq q = seq_of<R, kStep>(a, n);
     bool first = true;
 
     S st;
     while (u < u_end) {
         while (u >= before + q.units(a.Hk)) {  // the next sequence with work: there is one, u < U
             before += q.units(a.Hk);
-            q = seq_of(a, ++n, R);
+            q = seq_of<R, kStep>(a, ++n);
         }
         const int64_t in = u - before;
         const int item = static_cast<int>(in / q.steps), t0 = static_cast<int>(in - static_cast<int64_t>(item) * q.steps);
@@ -214,7 +222,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_cache_kernel(AttnArgs a) {
 // One workgroup per output row (token, query head): joins the pieces of its
 // (sequence, kv head, row tile) if the line was cut inside it.
 constexpr int kJoinThreads = 256;
-template <int V, int R>
+template <int V, int R, int STEP>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
     constexpr int LPR = V / 4, GR = kJoinThreads / LPR;
     __shared__ __align__(16) f32x4 red[GR][LPR];
@@ -222,7 +230,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
     const int tid = threadIdx.x;
     const int tok = blockIdx.x / a.H, h = blockIdx.x - tok * a.H, kvh = h / a.G;
     const int n = seq_of_token(a.cu, a.N, tok);
-    const Seq q = seq_of(a, n, R);
+    const Seq q = seq_of<R, STEP>(a, n);
     if (tok < q.start || tok >= q.start + q.count) return;
     const int64_t *prefix = static_cast<const int64_t *>(a.ws);
     const int64_t U = prefix[a.N], W = line_workgroups(U, a.W);
@@ -266,32 +274,219 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
     }
 }
 
-// Rows per tile by the call's mean rows per (sequence, kv head). More rows than that
-// cost registers and products on rows that do not exist; fewer read the cache again.
-int row_blocks(int64_t T, int64_t N, int64_t G, bool f32) {
-    const int64_t rows = (T + N - 1) / N * G;
-    if (rows <= 16) return 1;
-    return rows <= 32 || f32 ? 2 : 4;
+// ---- more than 16 rows
+//
+// Four waves of 32 rows. Ring of kStages tiles in LDS; the copies of a tile are issued when
+// the tile kStages - 1 before it has been read, and awaited by count, so that up to
+// kStages - 1 tiles are on their way. Two workgroups share a compute unit, so one's softmax
+// runs under the other's products. The pages of the next tile to copy are read one tile ahead.
+template <int K, int V, typename TC> struct Tiles {
+    using X = Rows<K, V, TC>;
+    static constexpr int NW = 4, R = 32 * NW;
+    static constexpr int XB = X::kCodes ? 256 : 0;  // exponents: 64 of keys, 64 of values, 128 bytes of padding
+    static constexpr int kTileBytes = X::KB + X::VB + XB;
+    static constexpr int kStages = 65536 / (X::KB + X::VB) > 4 ? 4 : 65536 / (X::KB + X::VB);
+    static constexpr int NK = X::KB / (1024 * NW), NV = X::VB / (1024 * NW);
+    static constexpr int kCopies = NK + NV + (X::kCodes ? 1 : 0);  // memory operations per wave and tile
+    static_assert(NK >= 1 && NV >= 1 && kStages >= 2, "tile sizes");
+
+    // pages of the four groups of 16 tokens from position p0 on; -1 where there is none
+    static __device__ __forceinline__ void pages(const AttnArgs &a, const int32_t *table, int p0, int last, int (&pg)[4]) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int pos = p0 + 16 * g;
+            const int id = pos < last ? ld_meta(table, pos >> a.page_shift) : -1;
+            pg[g] = id < a.num_pages ? id : -1;
+        }
+    }
+    // the rows of group g: first row in the cache's [pages, Hk, page] rows
+    static __device__ __forceinline__ int64_t group_row(const AttnArgs &a, int kvh, int p0, int g, int page) {
+        const int ps = 1 << a.page_shift;
+        return (static_cast<int64_t>(max(page, 0)) * a.Hk + kvh) * ps + ((p0 + 16 * g) & (ps - 1));
+    }
+    static __device__ __forceinline__ void copy(const AttnArgs &a, uint32_t dst, int kvh, int p0, const int (&pg)[4], int w, int lane) {
+        int64_t row[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) row[g] = group_row(a, kvh, p0, g, pg[g]);
+#pragma unroll
+        for (int i = 0; i < NK; ++i) rows<X::CK, K, true>(dst + (i * NW + w) * 1024, a.k, row, i, w, lane);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) rows<X::CV, V, false>(dst + X::KB + (i * NW + w) * 1024, a.v, row, i, w, lane);
+        if (X::kCodes) {
+            // words 0-15: keys' exponents, 16-31: values', 32-63: again. Every wave writes the same
+            // bytes, so that all have as many operations to await.
+            const int g = (lane & 15) >> 2;
+            const int64_t r = (g == 0 ? row[0] : g == 1 ? row[1] : g == 2 ? row[2] : row[3]) + 4 * (lane & 3);
+            copy_word_to_lds(dst + X::KB + X::VB, (lane & 16 ? a.vexp : a.kexp) + r);
+        }
+    }
+    // 1024 bytes: 64 chunks of C to a row, all in one group of 16 tokens
+    template <int C, int D, bool KEYS>
+    static __device__ __forceinline__ void rows(uint32_t dst, const void *cache, const int64_t (&row)[4], int i, int w, int lane) {
+        const int e = (i * NW + w) * 64, t0 = e / C;
+        const int t = t0 + lane / C, c = (lane % C) ^ (KEYS ? X::swz_k(t) : X::swz_v(t));
+        const int g = t0 >> 4;
+        const int64_t r = g == 0 ? row[0] : g == 1 ? row[1] : g == 2 ? row[2] : row[3];
+        const char *base = static_cast<const char *>(cache) + (r + (t0 & 15)) * (D * X::ES);
+        copy_to_lds(dst, base, (lane / C) * (D * X::ES) + 16 * c);
+    }
+};
+
+template <int K, int V, typename TC>
+__global__ __launch_bounds__(256, 2) void attn_cache_rows_kernel(AttnArgs a) {
+    using T = Tiles<K, V, TC>;
+    using X = Rows<K, V, TC>;
+    constexpr int R = T::R;
+    __shared__ __align__(1024) char lds[T::kStages * T::kTileBytes];
+    __shared__ int64_t sh[kWaves];
+    __shared__ int sh_n;
+    __shared__ int64_t sh_before;
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    Line<R, kTile> line;
+    line.scan(a, tid, sh, blockIdx.x == 0 ? static_cast<int64_t *>(a.ws) : nullptr);
+    const int64_t U = line.total;
+    if (U == 0) return;
+    const int64_t W = line_workgroups(U, a.W);
+    if (static_cast<int64_t>(blockIdx.x) >= W) return;
+    int64_t u = line_begin(blockIdx.x, U, W);
+    const int64_t u_end = line_begin(blockIdx.x + 1, U, W);
+    if (u >= u_end) return;
+    int n;
+    int64_t before;
+    line.find(a, u, tid, sh, n, before, sh_n, sh_before);
+    Seq q = seq_of<R, kTile>(a, n);
+    bool first = true;
+    const uint32_t base = lds_address(lds);
+    const float c = fabsf(a.c);
+
+    X st;
+    while (u < u_end) {
+        while (u >= before + q.units(a.Hk)) {  // the next sequence with work: there is one, u < U
+            before += q.units(a.Hk);
+            q = seq_of<R, kTile>(a, ++n);
+        }
+        const int64_t in = u - before;
+        const int item = static_cast<int>(in / q.steps), t0 = static_cast<int>(in - static_cast<int64_t>(item) * q.steps);
+        const int t1 = static_cast<int>(min(static_cast<int64_t>(q.steps), t0 + (u_end - u)));
+        const int kvh = item / q.tiles, r0 = (item - kvh * q.tiles) * R;
+        const int rows = static_cast<int>(min(static_cast<int64_t>(R), static_cast<int64_t>(q.count) * a.G - r0));
+        const bool whole = t0 == 0 && t1 == q.steps;
+        const int tok0 = r0 / a.G, tok1 = (r0 + rows - 1) / a.G;
+        // tokens below `open` are seen by all rows, none from `last` on is seen by any
+        const int open = min(q.end, a.mask ? q.ctx : q.ctx + tok0 + 1);
+        const int last = min(q.end, a.mask ? q.end : q.ctx + tok1 + 1);
+        const int te = min(t1, (max(last, 0) + kTile - 1) / kTile);  // tiles that hold something
+
+        // this lane's row; rows past the last repeat it and are not stored
+        const bool some = 32 * w < rows;
+        const int r = r0 + min(32 * w + (lane & 31), rows - 1), tok = r / a.G, h = kvh * a.G + (r - tok * a.G);
+        const uint64_t bits = a.mask ? a.mask[q.start + tok] : 0;
+        st.reset();
+        st.load_q(static_cast<const bf16_t *>(a.q) + static_cast<int64_t>(q.start + tok) * a.qs + h * K, a.c < 0.f, lane);
+
+        const int32_t *table = a.table + static_cast<int64_t>(n) * a.max_pages;
+        int pg[4];
+        uint32_t here = 0;  // of the tiles in the ring: four bits each, the oldest lowest
+        auto copy = [&](int t) {
+            T::copy(a, base + (t % T::kStages) * T::kTileBytes, kvh, t * kTile, pg, w, lane);
+            const int at = 4 * (t % T::kStages);
+            here &= ~(15u << at);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) here |= (pg[g] >= 0 ? 1u : 0u) << (at + g);
+            if (t + 1 < te) T::pages(a, table, (t + 1) * kTile, last, pg);
+        };
+        phase_barrier();  // all are done with the ring
+        if (t0 < te) T::pages(a, table, t0 * kTile, last, pg);
+#pragma unroll
+        for (int i = 0; i < T::kStages - 1; ++i)
+            if (t0 + i < te) copy(t0 + i);
+        // Tile t is there for all waves, and all are done with the one before: its groups that exist.
+        auto turn = [&](int t) {
+            // as many younger tiles are on their way as there are, up to kStages - 2
+            if (te - 1 - t >= T::kStages - 2) wait_copies<(T::kStages - 2) * T::kCopies>();
+            else wait_copies();
+            phase_barrier();
+            const uint32_t there = (here >> (4 * (t % T::kStages))) & 15u;
+            if (t + T::kStages - 1 < te) copy(t + T::kStages - 1);
+            return there;
+        };
+        auto tile = [&](int t) { return lds + (t % T::kStages) * T::kTileBytes; };
+        int t = t0;
+        uint32_t there = 0;
+        // tiles that all rows see whole, then from the first other one on
+        for (; t < te; ++t) {
+            there = turn(t);
+            if ((t + 1) * kTile > open || there != 15u) break;
+            if (!some) continue;
+            const char *lk = tile(t), *lv = lk + X::KB, *lx = lv + X::VB;
+            st.scores(lk, lx, lane);
+            st.template softmax<false>(c, 0, lx, lane);
+            st.values(lv, lane);
+        }
+        for (; t < te; ++t, there = t < te ? turn(t) : 0) {
+            if (!some) continue;
+            uint32_t sees = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int pos = t * kTile + X::token(i, lane), b = pos - q.ctx;
+                bool see = b < 0 || (a.mask ? b < 64 && ((bits >> (b & 63)) & 1u) : b <= tok);
+                see = see && pos < q.end && ((there >> (i >> 3)) & 1u);
+                sees |= static_cast<uint32_t>(see) << i;
+            }
+            const char *lk = tile(t), *lv = lk + X::KB, *lx = lv + X::VB;
+            st.scores(lk, lx, lane);
+            st.template softmax<true>(c, sees, lx, lane);
+            st.values_masked(lv, sees, lane);
+        }
+        if (32 * w + (lane & 31) < rows) {
+            const float l = swap32_sum(st.l);
+            if (whole) {
+                st.each(lane, [&](int ch, f32x4 x) { store_out(a, q.start, kvh, r, ch, x, l); });
+            } else {
+                float *part = reinterpret_cast<float *>(static_cast<char *>(a.ws) + prefix_bytes(a.N)) +
+                              (2 * static_cast<size_t>(blockIdx.x) + (first ? 0 : 1)) * part_floats(R, V);
+                const int row = r - r0;
+                st.each(lane, [&](int ch, f32x4 x) { *reinterpret_cast<f32x4 *>(part + row * V + ch) = x; });
+                if (lane < 32) {
+                    part[R * V + row] = st.m;
+                    part[R * V + R + row] = l;
+                }
+            }
+        }
+        first = false;
+        u += t1 - t0;
+    }
 }
 
-template <int K, int V, int RT, typename TC>
-hipError_t launch_rt(const AttnArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL((attn_cache_kernel<K, V, RT, TC>), dim3(a.W), dim3(64 * kWaves), 0, st, a);
-    hipError_t e = hipGetLastError();
+// Rows of a tile: 16 where the mean rows of a (sequence, kv head) fit them, else 128
+// (32 for fp32).
+int tile_rows(int64_t T, int64_t N, int64_t G, bool f32) {
+    const int64_t rows = (T + N - 1) / N * G;
+    return rows <= 16 ? 16 : f32 ? 32 : 128;
+}
+
+template <int V, int R, int STEP> hipError_t launch_join(const AttnArgs &a, hipStream_t st) {
+    const hipError_t e = hipGetLastError();
     // one step per (sequence, kv head, row tile) at most: the line is never cut inside one
-    if (e != hipSuccess || (a.max_pages << a.page_shift) <= kStep) return e;
-    hipLaunchKernelGGL((attn_join_kernel<V, 16 * RT>), dim3(static_cast<unsigned>(a.T) * a.H), dim3(kJoinThreads), 0, st, a);
+    if (e != hipSuccess || (a.max_pages << a.page_shift) <= STEP) return e;
+    hipLaunchKernelGGL((attn_join_kernel<V, R, STEP>), dim3(static_cast<unsigned>(a.T) * a.H), dim3(kJoinThreads), 0, st, a);
     return hipGetLastError();
+}
+template <int K, int V, int RT, typename TC> hipError_t launch_stream(const AttnArgs &a, hipStream_t st) {
+    hipLaunchKernelGGL((attn_cache_kernel<K, V, RT, TC>), dim3(a.W), dim3(64 * kWaves), 0, st, a);
+    return launch_join<V, 16 * RT, kStep>(a, st);
+}
+template <int K, int V, typename TC> hipError_t launch_rows(const AttnArgs &a, hipStream_t st) {
+    hipLaunchKernelGGL((attn_cache_rows_kernel<K, V, TC>), dim3(a.W), dim3(256), 0, st, a);
+    return launch_join<V, Tiles<K, V, TC>::R, kTile>(a, st);
 }
 
 template <int K, int V> hipError_t launch_dims(const AttnArgs &a, hipStream_t st) {
-    const int rt = row_blocks(a.T, a.N, a.G, a.in_dtype == KDA_F32);
-    if (a.kv_dtype == KDA_KV_F32) return rt == 1 ? launch_rt<K, V, 1, float>(a, st) : launch_rt<K, V, 2, float>(a, st);
-    if (a.kv_dtype == KDA_KV_BF16)
-        return rt == 1 ? launch_rt<K, V, 1, bf16_t>(a, st) : rt == 2 ? launch_rt<K, V, 2, bf16_t>(a, st)
-                                                                    : launch_rt<K, V, 4, bf16_t>(a, st);
-    return rt == 1 ? launch_rt<K, V, 1, e4m3_t>(a, st) : rt == 2 ? launch_rt<K, V, 2, e4m3_t>(a, st)
-                                                                : launch_rt<K, V, 4, e4m3_t>(a, st);
+    const bool one = tile_rows(a.T, a.N, a.G, a.in_dtype == KDA_F32) == 16;
+    if (a.kv_dtype == KDA_KV_F32) return one ? launch_stream<K, V, 1, float>(a, st) : launch_stream<K, V, 2, float>(a, st);
+    if (a.kv_dtype == KDA_KV_BF16) return one ? launch_stream<K, V, 1, bf16_t>(a, st) : launch_rows<K, V, bf16_t>(a, st);
+    return one ? launch_stream<K, V, 1, e4m3_t>(a, st) : launch_rows<K, V, e4m3_t>(a, st);
 }
 
 }  // namespace
@@ -299,7 +494,7 @@ template <int K, int V> hipError_t launch_dims(const AttnArgs &a, hipStream_t st
 int32_t attn_cache_workgroups() { return 2 * compute_units(); }
 
 size_t attn_cache_workspace(int32_t N, int32_t T, int32_t H, int32_t Hk, int32_t V, kda_dtype_t in_dtype) {
-    const int R = 16 * row_blocks(T, N, H / Hk, in_dtype == KDA_F32);
+    const int R = tile_rows(T, N, H / Hk, in_dtype == KDA_F32);
     return prefix_bytes(N) + 2 * static_cast<size_t>(attn_cache_workgroups()) * part_floats(R, V) * sizeof(float);
 }
 

@@ -20,7 +20,7 @@
 // LDS reads give without any movement of P.
 #pragma once
 
-#include "kda_attn_device.h"
+#include "kda_attn_rows.h"
 
 namespace kda {
 
@@ -163,7 +163,7 @@ template <int K, int V, int RT, typename TC> struct Stream {
             return *reinterpret_cast<const Frag *>(row + 16 * ((4 * s + g) ^ swz_k(t)));
         } else if constexpr (ES == 1) {
             const uint2 w = *reinterpret_cast<const uint2 *>(row + 16 * ((2 * s + (g >> 1)) ^ swz_k(t)) + 8 * (g & 1));
-            return codes_to_bf16(w.x, w.y);
+            return codes_to_bf16(w.x, w.y, 1.f);
         } else {
             const f32x4 x = *reinterpret_cast<const f32x4 *>(row + 16 * ((8 * s + 2 * g) ^ swz_k(t)));
             const f32x4 y = *reinterpret_cast<const f32x4 *>(row + 16 * ((8 * s + 2 * g + 1) ^ swz_k(t)));
@@ -186,7 +186,7 @@ template <int K, int V, int RT, typename TC> struct Stream {
             const int r = i >> 1, t = (r & 3) + 4 * g + (r >> 2) * 16;
             const char *p = lv + t * V + 16 * (d ^ swz_v(t)) + 8 * (i & 1);
             const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds2 *)p);
-            return codes_to_bf16(w[0], w[1]);
+            return codes_to_bf16(w[0], w[1], 1.f);
         } else {
             f32x8 x;
 #pragma unroll
@@ -206,7 +206,7 @@ template <int K, int V, int RT, typename TC> struct Stream {
             const float4 x = io<bf16_t>::load4(reinterpret_cast<const bf16_t *>(p));
             return (f32x4){x.x, x.y, x.z, x.w};
         }
-        const bf16x8 x = codes_to_bf16(*reinterpret_cast<const uint32_t *>(p), 0);
+        const bf16x8 x = codes_to_bf16(*reinterpret_cast<const uint32_t *>(p), 0, 1.f);
         return (f32x4){static_cast<float>(x[0]), static_cast<float>(x[1]), static_cast<float>(x[2]), static_cast<float>(x[3])};
     }
 
@@ -360,21 +360,5 @@ template <int K, int V, int RT, typename TC> struct Stream {
         }
     }
 };
-
-// o of one row: channels ch .. ch + 3 of row r of a tile
-__device__ __forceinline__ void store_out(const AttnArgs &a, int start, int kvh, int r, int ch, f32x4 x, float l) {
-    const int tok = r / a.G, h = kvh * a.G + (r - tok * a.G);
-    const int64_t at = (static_cast<int64_t>(start + tok) * a.H + h) * a.V + ch;
-    // l is 0 only where nothing was seen; each output is one division
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (l == 0.f) x = (f32x4){0.f, 0.f, 0.f, 0.f};
-    x *= inv;
-    if (a.out_dtype == KDA_BF16) {
-        const bf16x2 lo = pack_bf16(x[0], x[1]), hi = pack_bf16(x[2], x[3]);
-        *reinterpret_cast<bf16x4 *>(static_cast<bf16_t *>(a.o) + at) = (bf16x4){lo[0], lo[1], hi[0], hi[1]};
-    } else {
-        *reinterpret_cast<f32x4 *>(static_cast<float *>(a.o) + at) = x;
-    }
-}
 
 }  // namespace kda

@@ -83,7 +83,7 @@ __device__ __forceinline__ void read_row(T *dst, const void *cache, const uint8_
     float x[8];
     if constexpr (KV == KDA_KV_E4M3) {
         const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(cache) + row * D + 8 * c);
-        const bf16x8 v = codes_to_bf16(w.x, w.y);
+        const bf16x8 v = codes_to_bf16(w.x, w.y, 1.f);
         const int e = static_cast<int>(exps[row]) - 127;
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = __builtin_ldexpf(static_cast<float>(v[i]), e);
