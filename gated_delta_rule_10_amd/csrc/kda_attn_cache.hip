@@ -123,6 +123,52 @@ template <int R, int STEP> struct Line {
     }
 };
 
+// A run of a sequence's page table in registers: lane i of `now` holds page first + i, and
+// `next` the 64 after those. A scalar load would share its counter with the LDS reads and
+// hold the first of them up at every step.
+struct Pages {
+    const int32_t *table;
+    int first, max_pages, num_pages;
+    int now, next;
+    uint64_t there;  // bit i: page first + i exists
+
+    __device__ __forceinline__ int load(int p, int lane) const {
+        const int i = p + lane;
+        return i < max_pages ? table[i] : -1;
+    }
+    __device__ __forceinline__ void check() {
+        const bool ok = now >= 0 && now < num_pages;
+        there = __ballot(ok);
+        now = ok ? now : 0;  // a page that is not there is read as page 0, and masked
+    }
+    // runs start at a multiple of a step's pages, so a step never lies in two of them
+    __device__ __forceinline__ void begin(const AttnArgs &a, int n, int pos, int lane) {
+        table = a.table + static_cast<int64_t>(n) * a.max_pages;
+        max_pages = a.max_pages;
+        num_pages = a.num_pages;
+        first = pos >> a.page_shift;
+        now = load(first, lane);
+        next = load(first + 64, lane);
+        check();
+    }
+    // position pos of the next step (not below the last one)
+    __device__ __forceinline__ void reach(const AttnArgs &a, int pos, int lane) {
+        if ((pos >> a.page_shift) - first < 64) return;
+        first += 64;
+        now = next;
+        next = load(first + 64, lane);
+        check();
+    }
+    // cache row (of [pages, Hk, page]) of position pos
+    __device__ __forceinline__ int64_t row(const AttnArgs &a, int kvh, int pos) const {
+        const int id = __builtin_amdgcn_readlane(now, ((pos >> a.page_shift) - first) & 63);
+        return ((static_cast<int64_t>(id) * a.Hk + kvh) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+    }
+    __device__ __forceinline__ bool exists(const AttnArgs &a, int pos) const {
+        return (there >> (((pos >> a.page_shift) - first) & 63)) & 1u;
+    }
+};
+
 template <int K, int V, int RT, typename TC>
 __global__ __launch_bounds__(64 * kWaves) void attn_cache_kernel(AttnArgs a) {
     using S = Stream<K, V, RT, TC>;
@@ -169,34 +215,35 @@ __global__ __launch_bounds__(64 * kWaves) void attn_cache_kernel(AttnArgs a) {
 
         st.reset();
         st.load_q(a, q.start, kvh, r0, rows, lane);
-        int pg[2], pn[2];
-        const int32_t *table = a.table + static_cast<int64_t>(n) * a.max_pages;
-        auto pages = [&](int t, int (&p)[2]) {
+        Pages pages;
+        pages.begin(a, n, t0 * kStep, lane);
+        bool here[2] = {false, false}, soon[2] = {false, false};
+        auto load = [&](int t, bool (&there)[2]) {
+            const int p0 = t * kStep + w * kStepWave;
+            pages.reach(a, t * kStep, lane);
+            int64_t row[2];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int pos = t * kStep + w * kStepWave + 16 * b;
-                const int id = pos < last ? ld_meta(table, pos >> a.page_shift) : -1;
-                p[b] = id < a.num_pages ? id : -1;
+                row[b] = pages.row(a, kvh, p0 + 16 * b);
+                there[b] = pages.exists(a, p0 + 16 * b);
             }
+            st.load_cache(a, row, lane);
         };
-        pages(t0, pg);
-        if (t0 * kStep + w * kStepWave < last) st.load_cache(a, kvh, t0 * kStep + w * kStepWave, pg, lane);
+        if (t0 * kStep + w * kStepWave < last) load(t0, here);
         for (int t = t0; t < t1; ++t) {
             const int p0 = t * kStep + w * kStepWave;
             if (p0 >= last) break;  // wave-uniform; later steps lie further on
-            const bool here[2] = {pg[0] >= 0, pg[1] >= 0};
             const bool masked = p0 + kStepWave > open || !here[0] || !here[1];
             const uint32_t kx[2] = {st.ke[0], st.ke[1]}, vx[2] = {st.ve[0], st.ve[1]};
             uint32_t sees[RT];
             if (masked) st.visible(sees, a, q.start, r0, rows, p0, q.ctx, q.end, here, lane);
             const bool odd = st.stage(lk, lv, masked, p0, q.end, here, lane);
-            pages(t + 1 < t1 ? t + 1 : t, pn);
-            if (t + 1 < t1 && p0 + kStep < last) st.load_cache(a, kvh, p0 + kStep, pn, lane);
-            pg[0] = pn[0];
-            pg[1] = pn[1];
+            if (t + 1 < t1 && p0 + kStep < last) load(t + 1, soon);
             __builtin_amdgcn_wave_barrier();
             st.step(lk, lv, a.c, masked, sees, odd, kx, vx, lane);
             __builtin_amdgcn_wave_barrier();
+            here[0] = soon[0];
+            here[1] = soon[1];
         }
         __syncthreads();  // the join takes the waves' LDS
         if (whole) {
@@ -290,44 +337,27 @@ template <int K, int V, typename TC> struct Tiles {
     static constexpr int kCopies = NK + NV + (X::kCodes ? 1 : 0);  // memory operations per wave and tile
     static_assert(NK >= 1 && NV >= 1 && kStages >= 2, "tile sizes");
 
-    // pages of the four groups of 16 tokens from position p0 on; -1 where there is none
-    static __device__ __forceinline__ void pages(const AttnArgs &a, const int32_t *table, int p0, int last, int (&pg)[4]) {
+    // tile at position p0 to LDS at dst
+    static __device__ __forceinline__ void copy(const AttnArgs &a, const Pages &pages, uint32_t dst, int kvh, int p0, int w, int lane) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int pos = p0 + 16 * g;
-            const int id = pos < last ? ld_meta(table, pos >> a.page_shift) : -1;
-            pg[g] = id < a.num_pages ? id : -1;
-        }
-    }
-    // the rows of group g: first row in the cache's [pages, Hk, page] rows
-    static __device__ __forceinline__ int64_t group_row(const AttnArgs &a, int kvh, int p0, int g, int page) {
-        const int ps = 1 << a.page_shift;
-        return (static_cast<int64_t>(max(page, 0)) * a.Hk + kvh) * ps + ((p0 + 16 * g) & (ps - 1));
-    }
-    static __device__ __forceinline__ void copy(const AttnArgs &a, uint32_t dst, int kvh, int p0, const int (&pg)[4], int w, int lane) {
-        int64_t row[4];
+        for (int i = 0; i < NK; ++i) rows<X::CK, K, true>(a, pages, dst + (i * NW + w) * 1024, a.k, kvh, p0, i, w, lane);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) row[g] = group_row(a, kvh, p0, g, pg[g]);
-#pragma unroll
-        for (int i = 0; i < NK; ++i) rows<X::CK, K, true>(dst + (i * NW + w) * 1024, a.k, row, i, w, lane);
-#pragma unroll
-        for (int i = 0; i < NV; ++i) rows<X::CV, V, false>(dst + X::KB + (i * NW + w) * 1024, a.v, row, i, w, lane);
+        for (int i = 0; i < NV; ++i) rows<X::CV, V, false>(a, pages, dst + X::KB + (i * NW + w) * 1024, a.v, kvh, p0, i, w, lane);
         if (X::kCodes) {
             // words 0-15: keys' exponents, 16-31: values', 32-63: again. Every wave writes the same
             // bytes, so that all have as many operations to await.
-            const int g = (lane & 15) >> 2;
-            const int64_t r = (g == 0 ? row[0] : g == 1 ? row[1] : g == 2 ? row[2] : row[3]) + 4 * (lane & 3);
+            const int pos = p0 + 4 * (lane & 15);
+            const int id = __shfl(pages.now, ((pos >> a.page_shift) - pages.first) & 63);
+            const int64_t r = ((static_cast<int64_t>(id) * a.Hk + kvh) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
             copy_word_to_lds(dst + X::KB + X::VB, (lane & 16 ? a.vexp : a.kexp) + r);
         }
     }
-    // 1024 bytes: 64 chunks of C to a row, all in one group of 16 tokens
+    // 1024 bytes: 64 chunks of C to a row, all in one group of 16 tokens and so in one page
     template <int C, int D, bool KEYS>
-    static __device__ __forceinline__ void rows(uint32_t dst, const void *cache, const int64_t (&row)[4], int i, int w, int lane) {
-        const int e = (i * NW + w) * 64, t0 = e / C;
-        const int t = t0 + lane / C, c = (lane % C) ^ (KEYS ? X::swz_k(t) : X::swz_v(t));
-        const int g = t0 >> 4;
-        const int64_t r = g == 0 ? row[0] : g == 1 ? row[1] : g == 2 ? row[2] : row[3];
-        const char *base = static_cast<const char *>(cache) + (r + (t0 & 15)) * (D * X::ES);
+    static __device__ __forceinline__ void rows(const AttnArgs &a, const Pages &pages, uint32_t dst, const void *cache, int kvh,
+                                                int p0, int i, int w, int lane) {
+        const int t0 = (i * NW + w) * 64 / C, t = t0 + lane / C, c = (lane % C) ^ (KEYS ? X::swz_k(t) : X::swz_v(t));
+        const char *base = static_cast<const char *>(cache) + pages.row(a, kvh, p0 + t0) * (D * X::ES);
         copy_to_lds(dst, base, (lane / C) * (D * X::ES) + 16 * c);
     }
 };
@@ -385,46 +415,49 @@ __global__ __launch_bounds__(256, 2) void attn_cache_rows_kernel(AttnArgs a) {
         st.reset();
         st.load_q(static_cast<const bf16_t *>(a.q) + static_cast<int64_t>(q.start + tok) * a.qs + h * K, a.c < 0.f, lane);
 
-        const int32_t *table = a.table + static_cast<int64_t>(n) * a.max_pages;
-        int pg[4];
-        uint32_t here = 0;  // of the tiles in the ring: four bits each, the oldest lowest
+        Pages pages;
+        pages.begin(a, n, t0 * kTile, lane);
+        uint32_t here = 0;  // which groups of 16 tokens of the tiles on their way exist, the next one's lowest
+        int slot = 0, put = 0;  // ring: the tile in work, the next copy
         auto copy = [&](int t) {
-            T::copy(a, base + (t % T::kStages) * T::kTileBytes, kvh, t * kTile, pg, w, lane);
-            const int at = 4 * (t % T::kStages);
-            here &= ~(15u << at);
+            pages.reach(a, t * kTile, lane);
+            T::copy(a, pages, base + put * T::kTileBytes, kvh, t * kTile, w, lane);
+            put = put + 1 == T::kStages ? 0 : put + 1;
+            uint32_t v = 0;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) here |= (pg[g] >= 0 ? 1u : 0u) << (at + g);
-            if (t + 1 < te) T::pages(a, table, (t + 1) * kTile, last, pg);
+            for (int g = 0; g < 4; ++g) v |= (pages.exists(a, t * kTile + 16 * g) ? 1u : 0u) << g;
+            return v;
         };
         phase_barrier();  // all are done with the ring
-        if (t0 < te) T::pages(a, table, t0 * kTile, last, pg);
 #pragma unroll
         for (int i = 0; i < T::kStages - 1; ++i)
-            if (t0 + i < te) copy(t0 + i);
+            if (t0 + i < te) here |= copy(t0 + i) << (4 * i);
         // Tile t is there for all waves, and all are done with the one before: its groups that exist.
         auto turn = [&](int t) {
             // as many younger tiles are on their way as there are, up to kStages - 2
             if (te - 1 - t >= T::kStages - 2) wait_copies<(T::kStages - 2) * T::kCopies>();
             else wait_copies();
             phase_barrier();
-            const uint32_t there = (here >> (4 * (t % T::kStages))) & 15u;
-            if (t + T::kStages - 1 < te) copy(t + T::kStages - 1);
+            const uint32_t there = here & 15u;
+            here >>= 4;
+            if (t + T::kStages - 1 < te) here |= copy(t + T::kStages - 1) << (4 * (T::kStages - 2));
             return there;
         };
-        auto tile = [&](int t) { return lds + (t % T::kStages) * T::kTileBytes; };
+        auto tile = [&]() { return lds + slot * T::kTileBytes; };
+        auto done = [&]() { slot = slot + 1 == T::kStages ? 0 : slot + 1; };
         int t = t0;
         uint32_t there = 0;
         // tiles that all rows see whole, then from the first other one on
-        for (; t < te; ++t) {
+        for (; t < te; ++t, done()) {
             there = turn(t);
             if ((t + 1) * kTile > open || there != 15u) break;
             if (!some) continue;
-            const char *lk = tile(t), *lv = lk + X::KB, *lx = lv + X::VB;
+            const char *lk = tile(), *lv = lk + X::KB, *lx = lv + X::VB;
             st.scores(lk, lx, lane);
             st.template softmax<false>(c, 0, lx, lane);
             st.values(lv, lane);
         }
-        for (; t < te; ++t, there = t < te ? turn(t) : 0) {
+        for (; t < te; ++t, done(), there = t < te ? turn(t) : 0) {
             if (!some) continue;
             uint32_t sees = 0;
 #pragma unroll
@@ -434,7 +467,7 @@ __global__ __launch_bounds__(256, 2) void attn_cache_rows_kernel(AttnArgs a) {
                 see = see && pos < q.end && ((there >> (i >> 3)) & 1u);
                 sees |= static_cast<uint32_t>(see) << i;
             }
-            const char *lk = tile(t), *lv = lk + X::KB, *lx = lv + X::VB;
+            const char *lk = tile(), *lv = lk + X::KB, *lx = lv + X::VB;
             st.scores(lk, lx, lane);
             st.template softmax<true>(c, sees, lx, lane);
             st.values_masked(lv, sees, lane);

@@ -82,32 +82,29 @@ template <int K, int V, int RT, typename TC> struct Stream {
         }
     }
 
-    // ---- sources: chunk x of a wave's 32 tokens from position p0 on
-    // cache: pg[b] is the page of tokens 16 b .. 16 b + 15 (a page ends at a multiple of 16)
-    __device__ __forceinline__ void load_cache(const AttnArgs &a, int kvh, int p0, const int (&pg)[2], int lane) {
-        const int ps = 1 << a.page_shift, lane_ = lane;
-        int64_t base[2];
+    // ---- sources: chunk x of a wave's 32 tokens
+    // cache: row[b] is the cache row of the first of tokens 16 b .. 16 b + 15 (a page ends at a multiple of
+    // 16, so the 16 rows lie behind one another)
+    __device__ __forceinline__ void load_cache(const AttnArgs &a, const int64_t (&row)[2], int lane) {
+        const char *k[2], *v[2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-            base[b] = (static_cast<int64_t>(max(pg[b], 0)) * a.Hk + kvh) * ps + ((p0 + 16 * b) & (ps - 1));
-#pragma unroll
-        for (int x = 0; x < NK; ++x) {
-            const int e = x * 64 + lane_, t = e / CK, c = e % CK;
-            kr[x] = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.k) +
-                                                     (base[t >> 4] + (t & 15)) * (K * ES) + 16 * c);
+        for (int b = 0; b < 2; ++b) {
+            k[b] = static_cast<const char *>(a.k) + row[b] * (K * ES);
+            v[b] = static_cast<const char *>(a.v) + row[b] * (V * ES);
         }
+        const uint32_t at = 16 * lane;
 #pragma unroll
-        for (int x = 0; x < NV; ++x) {
-            const int e = x * 64 + lane_, t = e / CV, c = e % CV;
-            vr[x] = *reinterpret_cast<const u32x4 *>(static_cast<const char *>(a.v) +
-                                                     (base[t >> 4] + (t & 15)) * (V * ES) + 16 * c);
-        }
+        for (int x = 0; x < NK; ++x)
+            kr[x] = *reinterpret_cast<const u32x4 *>(k[2 * x / NK] + at + (x % (NK / 2)) * 1024);
+#pragma unroll
+        for (int x = 0; x < NV; ++x)
+            vr[x] = *reinterpret_cast<const u32x4 *>(v[2 * x / NV] + at + (x % (NV / 2)) * 1024);
         if (kCodes) {
-            const int g = lane >> 4;
+            const uint32_t g = 4 * (lane >> 4);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                ke[b] = *reinterpret_cast<const uint32_t *>(a.kexp + base[b] + 4 * g);
-                ve[b] = *reinterpret_cast<const uint32_t *>(a.vexp + base[b] + 4 * g);
+                ke[b] = *reinterpret_cast<const uint32_t *>(a.kexp + row[b] + g);
+                ve[b] = *reinterpret_cast<const uint32_t *>(a.vexp + row[b] + g);
             }
         }
     }
