@@ -9,8 +9,7 @@
 //    among the four waves, each of which streams its own tokens without a barrier
 //    (kda_attn_stream.h). fp32 caches take this one for any number of rows.
 //  - more (several or drafted tokens): the waves share each tile of 64 tokens in LDS and
-//    take 32 rows each, up to 128 (kda_attn_rows.h). Tiles are copied to LDS two or more
-//    ahead, two workgroups to a compute unit.
+//    take 32 rows each, up to 128 (kda_attn_rows.h).
 //
 // Split. Sequences differ in length and only the device knows it, so the steps
 // of all (sequence, kv head, row tile)s are laid on one line and each of W
@@ -266,108 +265,141 @@ __global__ __launch_bounds__(64 * kWaves) void attn_cache_kernel(AttnArgs a) {
     }
 }
 
-// One workgroup per output row (token, query head): joins the pieces of its
-// (sequence, kv head, row tile) if the line was cut inside it.
-constexpr int kJoinThreads = 256;
+// Joins the pieces of the (sequence, kv head, row tile)s that the line was cut inside: a
+// workgroup takes up to 16 rows of one. Groups of V / 4 lanes take a row each; where there are
+// more groups than rows, several share a row's pieces and are added in the end.
+constexpr int kJoinThreads = 256, kJoinRows = 16;
 template <int V, int R, int STEP>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
-    constexpr int LPR = V / 4, GR = kJoinThreads / LPR;
+    constexpr int LPR = V / 4, GR = kJoinThreads / LPR;  // lanes of a row, groups
     __shared__ __align__(16) f32x4 red[GR][LPR];
-    __shared__ float red_l[GR], red_m[kJoinThreads / 64];
-    const int tid = threadIdx.x;
-    const int tok = blockIdx.x / a.H, h = blockIdx.x - tok * a.H, kvh = h / a.G;
-    const int n = seq_of_token(a.cu, a.N, tok);
+    __shared__ float red_l[GR];
+    const int tid = threadIdx.x, gr = tid / LPR, c = tid % LPR;
+    constexpr int PARTS = R / kJoinRows;
+    const int part_of = blockIdx.x % PARTS, rest = blockIdx.x / PARTS, kvh = rest % a.Hk;
+    const int64_t slot = rest / a.Hk;
+    const int n = seq_of_slot(a.cu, a.N, a.T, a.G, R, slot);
     const Seq q = seq_of<R, STEP>(a, n);
-    if (tok < q.start || tok >= q.start + q.count) return;
+    const int64_t tile = slot - static_cast<int64_t>(q.start) * a.G / R - n;
+    if (tile < 0 || tile >= q.tiles) return;
+    const int64_t r0 = tile * R + part_of * kJoinRows;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kJoinRows), static_cast<int64_t>(q.count) * a.G - r0));
+    if (rows <= 0) return;
     const int64_t *prefix = static_cast<const int64_t *>(a.ws);
     const int64_t U = prefix[a.N], W = line_workgroups(U, a.W);
-    const int r = (tok - q.start) * a.G + (h - kvh * a.G), tile = r / R, row = r - tile * R;
     const int64_t s = prefix[n] + (static_cast<int64_t>(kvh) * q.tiles + tile) * q.steps, e = s + q.steps;
     const int64_t w0 = line_owner(s, U, W), w1 = line_owner(e - 1, U, W);
     if (w0 == w1) return;
+    // piece i of the tile: of workgroup w0 + i, whose first piece it is unless w0 had other work before
     const float *parts = reinterpret_cast<const float *>(static_cast<const char *>(a.ws) + prefix_bytes(a.N));
-    auto part = [&](int64_t w) {
-        const bool last = w == w0 && line_begin(w0, U, W) < s;  // w0 had other work before this
-        return parts + (2 * w + (last ? 1 : 0)) * part_floats(R, V);
-    };
-    float m = -INFINITY;
-    for (int64_t w = w0 + tid; w <= w1; w += kJoinThreads) m = fmaxf(m, part(w)[R * V + row]);
+    const int pieces = static_cast<int>(w1 - w0) + 1;
+    const bool other = line_begin(w0, U, W) < s;
+    const float *p0 = parts + (2 * w0 + (other ? 1 : 0)) * part_floats(R, V), *p1 = parts + 2 * w0 * part_floats(R, V);
+    auto piece = [&](int i) { return i == 0 ? p0 : p1 + 2 * i * part_floats(R, V); };
+
+    int share = 1;  // groups to a row
+    while (share * 2 * rows <= GR) share *= 2;
+    const int per = GR / share;  // rows at a time
+    for (int rb = 0; rb < rows; rb += per) {
+        const int rr = rb + gr / share, sub = gr % share, row = part_of * kJoinRows + min(rr, rows - 1);
+        float m = -INFINITY;
+        for (int i = c; i < pieces; i += LPR) m = fmaxf(m, piece(i)[R * V + row]);
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-    if ((tid & 63) == 0) red_m[tid >> 6] = m;
-    __syncthreads();
-    m = red_m[0];
-#pragma unroll
-    for (int i = 1; i < kJoinThreads / 64; ++i) m = fmaxf(m, red_m[i]);
-    const int gr = tid / LPR, c = tid % LPR;
-    f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    float l = 0.f;
-    for (int64_t w = w0 + gr; w <= w1; w += GR) {
-        const float *p = part(w);
-        const float mw = p[R * V + row], f = mw == -INFINITY ? 0.f : exp2f(mw - m);
-        x += *reinterpret_cast<const f32x4 *>(p + row * V + 4 * c) * f;
-        l += p[R * V + R + row] * f;
-    }
-    red[gr][c] = x;
-    if (c == 0) red_l[gr] = l;
-    __syncthreads();
-    if (gr == 0) {
-#pragma unroll
-        for (int i = 1; i < GR; ++i) {
-            x += red[i][c];
-            l += red_l[i];
+        for (int d = 1; d < LPR; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+        float l = 0.f;
+#pragma unroll 4
+        for (int i = sub; i < pieces; i += share) {
+            const float *p = piece(i);
+            const float mi = p[R * V + row], f = mi == -INFINITY ? 0.f : exp2f(mi - m);
+            x += *reinterpret_cast<const f32x4 *>(p + row * V + 4 * c) * f;
+            l += p[R * V + R + row] * f;
         }
-        store_out(a, q.start, kvh, r, 4 * c, x, l);
+        if (share > 1) {
+            red[gr][c] = x;
+            if (c == 0) red_l[gr] = l;
+            __syncthreads();
+            for (int i = 1; i < share; ++i) {
+                x += red[(gr + i) % GR][c];
+                l += red_l[(gr + i) % GR];
+            }
+            __syncthreads();
+        }
+        if (sub == 0 && rr < rows) store_out(a, q.start, kvh, static_cast<int>(r0) + rr, 4 * c, x, l);
     }
 }
 
 // ---- more than 16 rows
 //
-// Four waves of 32 rows. Ring of kStages tiles in LDS; the copies of a tile are issued when
-// the tile kStages - 1 before it has been read, and awaited by count, so that up to
-// kStages - 1 tiles are on their way. Two workgroups share a compute unit, so one's softmax
-// runs under the other's products. The pages of the next tile to copy are read one tile ahead.
+// Four waves of 32 rows. A ring of two tiles as the cache holds them is copied to LDS ahead;
+// e4m3 tiles are turned to bf16 with their scales by all four waves together, once, into a
+// tile of their own (exactly: four bits of significand and a power of two), so that the
+// products are the bf16 ones. Two workgroups share a compute unit, so that one's softmax and
+// waits run under the other's products.
 template <int K, int V, typename TC> struct Tiles {
-    using X = Rows<K, V, TC>;
-    static constexpr int NW = 4, R = 32 * NW;
-    static constexpr int XB = X::kCodes ? 256 : 0;  // exponents: 64 of keys, 64 of values, 128 bytes of padding
-    static constexpr int kTileBytes = X::KB + X::VB + XB;
-    static constexpr int kStages = 65536 / (X::KB + X::VB) > 4 ? 4 : 65536 / (X::KB + X::VB);
-    static constexpr int NK = X::KB / (1024 * NW), NV = X::VB / (1024 * NW);
-    static constexpr int kCopies = NK + NV + (X::kCodes ? 1 : 0);  // memory operations per wave and tile
-    static_assert(NK >= 1 && NV >= 1 && kStages >= 2, "tile sizes");
+    using X = Rows<K, V>;
+    static constexpr int NW = 4, R = 32 * NW, ES = sizeof(TC);
+    static constexpr bool kCodes = ES == 1;
+    static constexpr int KR = kTile * K * ES, VR = kTile * V * ES;  // bytes of a tile in the cache's type
+    static constexpr int XB = kCodes ? 256 : 0;  // exponents: 64 of keys, 64 of values, and those again
+    static constexpr int kRaw = KR + VR + XB, kStages = 2;
+    static constexpr int kLds = kStages * kRaw + (kCodes ? X::KB + X::VB : 0);
+    static constexpr int NK = KR / (1024 * NW), NV = VR / (1024 * NW);
+    static constexpr int kCopies = NK + NV + (kCodes ? 1 : 0);  // memory operations per wave and tile
+    static_assert(NK >= 1 && NV >= 1, "a tile is at least one copy per wave");
 
     // tile at position p0 to LDS at dst
     static __device__ __forceinline__ void copy(const AttnArgs &a, const Pages &pages, uint32_t dst, int kvh, int p0, int w, int lane) {
 #pragma unroll
-        for (int i = 0; i < NK; ++i) rows<X::CK, K, true>(a, pages, dst + (i * NW + w) * 1024, a.k, kvh, p0, i, w, lane);
+        for (int i = 0; i < NK; ++i) rows<K, true>(a, pages, dst + (i * NW + w) * 1024, a.k, kvh, p0, i, w, lane);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) rows<X::CV, V, false>(a, pages, dst + X::KB + (i * NW + w) * 1024, a.v, kvh, p0, i, w, lane);
-        if (X::kCodes) {
+        for (int i = 0; i < NV; ++i) rows<V, false>(a, pages, dst + KR + (i * NW + w) * 1024, a.v, kvh, p0, i, w, lane);
+        if (kCodes) {
             // words 0-15: keys' exponents, 16-31: values', 32-63: again. Every wave writes the same
             // bytes, so that all have as many operations to await.
             const int pos = p0 + 4 * (lane & 15);
             const int id = __shfl(pages.now, ((pos >> a.page_shift) - pages.first) & 63);
             const int64_t r = ((static_cast<int64_t>(id) * a.Hk + kvh) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-            copy_word_to_lds(dst + X::KB + X::VB, (lane & 16 ? a.vexp : a.kexp) + r);
+            copy_word_to_lds(dst + KR + VR, (lane & 16 ? a.vexp : a.kexp) + r);
         }
     }
-    // 1024 bytes: 64 chunks of C to a row, all in one group of 16 tokens and so in one page
-    template <int C, int D, bool KEYS>
+    // 1024 bytes: 64 chunks, all in one group of 16 tokens and so in one page. bf16 chunks go where
+    // the products read them, codes as they lie.
+    template <int D, bool KEYS>
     static __device__ __forceinline__ void rows(const AttnArgs &a, const Pages &pages, uint32_t dst, const void *cache, int kvh,
                                                 int p0, int i, int w, int lane) {
-        const int t0 = (i * NW + w) * 64 / C, t = t0 + lane / C, c = (lane % C) ^ (KEYS ? X::swz_k(t) : X::swz_v(t));
-        const char *base = static_cast<const char *>(cache) + pages.row(a, kvh, p0 + t0) * (D * X::ES);
-        copy_to_lds(dst, base, (lane / C) * (D * X::ES) + 16 * c);
+        constexpr int C = D * ES / 16;
+        const int t0 = (i * NW + w) * 64 / C, t = t0 + lane / C;
+        const int c = (lane % C) ^ (kCodes ? 0 : KEYS ? X::swz_k(t) : X::swz_v(t));
+        const char *base = static_cast<const char *>(cache) + pages.row(a, kvh, p0 + t0) * (D * ES);
+        copy_to_lds(dst, base, (lane / C) * (D * ES) + 16 * c);
+    }
+
+    // codes of a tile to bf16, at the chunks that the products read. tid: of 256 threads.
+    static __device__ __forceinline__ void convert(const char *raw, char *to, int tid) {
+        part<K, true>(raw, raw + KR + VR, to, tid);
+        part<V, false>(raw + KR, raw + KR + VR + kTile, to + X::KB, tid);
+    }
+    template <int D, bool KEYS> static __device__ __forceinline__ void part(const char *raw, const char *exps, char *to, int tid) {
+        constexpr int C = D / 16;  // chunks of 16 codes to a row
+#pragma unroll
+        for (int i = 0; i < kTile * C / 256; ++i) {
+            const int e = i * 256 + tid, t = e / C, c = e % C, sw = KEYS ? X::swz_k(t) : X::swz_v(t);
+            const u32x4 w = *reinterpret_cast<const u32x4 *>(raw + 16 * e);
+            // the conversion takes a scale's exponent bits
+            const float scale = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint8_t *>(exps + t)) << 23);
+            *reinterpret_cast<bf16x8 *>(to + t * (2 * D) + 16 * ((2 * c) ^ sw)) = codes_to_bf16(w[0], w[1], scale);
+            *reinterpret_cast<bf16x8 *>(to + t * (2 * D) + 16 * ((2 * c + 1) ^ sw)) = codes_to_bf16(w[2], w[3], scale);
+        }
     }
 };
 
 template <int K, int V, typename TC>
 __global__ __launch_bounds__(256, 2) void attn_cache_rows_kernel(AttnArgs a) {
     using T = Tiles<K, V, TC>;
-    using X = Rows<K, V, TC>;
+    using X = Rows<K, V>;
     constexpr int R = T::R;
-    __shared__ __align__(1024) char lds[T::kStages * T::kTileBytes];
+    __shared__ __align__(1024) char lds[T::kLds];
     __shared__ int64_t sh[kWaves];
     __shared__ int sh_n;
     __shared__ int64_t sh_before;
@@ -418,46 +450,51 @@ __global__ __launch_bounds__(256, 2) void attn_cache_rows_kernel(AttnArgs a) {
         Pages pages;
         pages.begin(a, n, t0 * kTile, lane);
         uint32_t here = 0;  // which groups of 16 tokens of the tiles on their way exist, the next one's lowest
-        int slot = 0, put = 0;  // ring: the tile in work, the next copy
         auto copy = [&](int t) {
             pages.reach(a, t * kTile, lane);
-            T::copy(a, pages, base + put * T::kTileBytes, kvh, t * kTile, w, lane);
-            put = put + 1 == T::kStages ? 0 : put + 1;
+            T::copy(a, pages, base + (t & 1) * T::kRaw, kvh, t * kTile, w, lane);
             uint32_t v = 0;
 #pragma unroll
             for (int g = 0; g < 4; ++g) v |= (pages.exists(a, t * kTile + 16 * g) ? 1u : 0u) << g;
             return v;
         };
         phase_barrier();  // all are done with the ring
-#pragma unroll
-        for (int i = 0; i < T::kStages - 1; ++i)
-            if (t0 + i < te) here |= copy(t0 + i) << (4 * i);
-        // Tile t is there for all waves, and all are done with the one before: its groups that exist.
+        if (t0 < te) here = copy(t0);
+        if (T::kCodes && t0 + 1 < te) here |= copy(t0 + 1) << 4;
+        // Makes tile t ready for all waves, once all are done with the one before, and says which of
+        // its groups exist. Copies of bf16 tiles: t + 1 is issued here. Codes: t + 1 is on its
+        // way, and t + 2 follows once t has been turned to bf16.
         auto turn = [&](int t) {
-            // as many younger tiles are on their way as there are, up to kStages - 2
-            if (te - 1 - t >= T::kStages - 2) wait_copies<(T::kStages - 2) * T::kCopies>();
+            if (T::kCodes && t + 1 < te) wait_copies<T::kCopies>();
             else wait_copies();
             phase_barrier();
             const uint32_t there = here & 15u;
             here >>= 4;
-            if (t + T::kStages - 1 < te) here |= copy(t + T::kStages - 1) << (4 * (T::kStages - 2));
+            if (T::kCodes) {
+                T::convert(lds + (t & 1) * T::kRaw, lds + T::kStages * T::kRaw, tid);
+                phase_barrier();
+                if (t + 2 < te) here |= copy(t + 2) << 4;
+            } else if (t + 1 < te) {
+                here |= copy(t + 1);
+            }
             return there;
         };
-        auto tile = [&]() { return lds + slot * T::kTileBytes; };
-        auto done = [&]() { slot = slot + 1 == T::kStages ? 0 : slot + 1; };
+        auto tile = [&](int t) { return lds + (T::kCodes ? T::kStages * T::kRaw : (t & 1) * T::kRaw); };
         int t = t0;
         uint32_t there = 0;
         // tiles that all rows see whole, then from the first other one on
-        for (; t < te; ++t, done()) {
+        for (; t < te; ++t) {
             there = turn(t);
             if ((t + 1) * kTile > open || there != 15u) break;
             if (!some) continue;
-            const char *lk = tile(), *lv = lk + X::KB, *lx = lv + X::VB;
-            st.scores(lk, lx, lane);
-            st.template softmax<false>(c, 0, lx, lane);
+            const char *lk = tile(t), *lv = lk + X::KB;
+            st.scores(lk, lane);
+            X::template interleave<false>();
+            st.template softmax<false>(c, 0);
             st.values(lv, lane);
+            X::template interleave<true, false>();
         }
-        for (; t < te; ++t, done(), there = t < te ? turn(t) : 0) {
+        for (; t < te; ++t, there = t < te ? turn(t) : 0) {
             if (!some) continue;
             uint32_t sees = 0;
 #pragma unroll
@@ -467,9 +504,9 @@ __global__ __launch_bounds__(256, 2) void attn_cache_rows_kernel(AttnArgs a) {
                 see = see && pos < q.end && ((there >> (i >> 3)) & 1u);
                 sees |= static_cast<uint32_t>(see) << i;
             }
-            const char *lk = tile(), *lv = lk + X::KB, *lx = lv + X::VB;
-            st.scores(lk, lx, lane);
-            st.template softmax<true>(c, sees, lx, lane);
+            const char *lk = tile(t), *lv = lk + X::KB;
+            st.scores(lk, lane);
+            st.template softmax<true>(c, sees);
             st.values_masked(lv, sees, lane);
         }
         if (32 * w + (lane & 31) < rows) {
@@ -503,7 +540,9 @@ template <int V, int R, int STEP> hipError_t launch_join(const AttnArgs &a, hipS
     const hipError_t e = hipGetLastError();
     // one step per (sequence, kv head, row tile) at most: the line is never cut inside one
     if (e != hipSuccess || (a.max_pages << a.page_shift) <= STEP) return e;
-    hipLaunchKernelGGL((attn_join_kernel<V, R, STEP>), dim3(static_cast<unsigned>(a.T) * a.H), dim3(kJoinThreads), 0, st, a);
+    const int64_t slots = static_cast<int64_t>(a.T) * a.G / R + a.N;
+    hipLaunchKernelGGL((attn_join_kernel<V, R, STEP>), dim3(static_cast<unsigned>(slots * a.Hk * (R / kJoinRows))),
+                       dim3(kJoinThreads), 0, st, a);
     return hipGetLastError();
 }
 template <int K, int V, int RT, typename TC> hipError_t launch_stream(const AttnArgs &a, hipStream_t st) {

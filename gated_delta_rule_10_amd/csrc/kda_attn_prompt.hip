@@ -95,13 +95,13 @@ __global__ __launch_bounds__(64 * kWaves) void attn_prompt_kernel(AttnArgs a, in
 __device__ __forceinline__ uint32_t seen_upto(int top, int lane) {
     uint32_t v = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v |= static_cast<uint32_t>(Rows<64, 64, bf16_t>::token(i, lane) <= top) << i;
+    for (int i = 0; i < 32; ++i) v |= static_cast<uint32_t>(Rows<64, 64>::token(i, lane) <= top) << i;
     return v;
 }
 
 template <int K, int V, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a, int slots) {
-    using P = Rows<K, V, bf16_t>;
+    using P = Rows<K, V>;
     constexpr int R = 32 * NW;
     __shared__ __align__(1024) char lds[2 * (P::KB + P::VB)];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -169,10 +169,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
         if (kProductsFirst) __builtin_amdgcn_s_setprio(1);
         if (j > 0) {
             st.values(lds + lv(j - 1), lane);
-            st.scores(lds + lk(j), nullptr, lane);
+            st.scores(lds + lk(j), lane);
             P::template interleave<true>();
         } else {
-            st.scores(lds + lk(0), nullptr, lane);
+            st.scores(lds + lk(0), lane);
             P::template interleave<false>();
         }
         if (kProductsFirst) __builtin_amdgcn_s_setprio(0);
@@ -181,7 +181,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
             copy_k(j + 2);
             copy_v(j + 1);
         }
-        st.template softmax<false>(c, 0, nullptr, lane);
+        st.template softmax<false>(c, 0);
         swap(ahead);
     }
     uint32_t seen = ~0u;  // of tile j - 1
@@ -191,7 +191,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
             copy_v(j);
         }
         if (j > 0 && sees(j - 1)) st.values_masked(lds + lv(j - 1), seen, lane);
-        if (sees(j)) st.scores(lds + lk(j), nullptr, lane);
+        if (sees(j)) st.scores(lds + lk(j), lane);
         swap(!ahead);
         if (!ahead) {
             copy_k(j + 2);
@@ -199,7 +199,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
         }
         if (sees(j)) {
             seen = seen_upto(own - j * kTile, lane);
-            st.template softmax<true>(c, seen, nullptr, lane);
+            st.template softmax<true>(c, seen);
         }
         swap(ahead);
     }

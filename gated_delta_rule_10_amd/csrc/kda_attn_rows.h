@@ -1,17 +1,11 @@
-// Attention of 32 rows per wave over tiles of 64 keys and values in LDS, for bf16
-// and e4m3 elements.
+// Attention of 32 rows per wave over tiles of 64 keys and values in LDS, in bf16.
 //
 // 32 x 32 matrix instructions, 16-deep: S^T = K Q^T leaves the scores of row
 // l % 32 for tokens 32 b + 8 (i / 4) + 4 (l / 32) + i % 4 in register i of lane l,
 // and those registers, rounded to bf16, are the B operand of O^T = V^T P^T when
 // V^T's fragments take the tokens in the same order, which the transposing LDS
 // reads do. P never moves between lanes.
-//
-// Codes are turned to bf16 as their fragments are read, exactly: keys with their
-// token's scale, and the scales of values on the weights.
 #pragma once
-
-#include <type_traits>
 
 #include "kda_attn_device.h"
 
@@ -54,36 +48,25 @@ __device__ __forceinline__ void phase_barrier() {
 
 constexpr int kTile = 64;  // tokens per tile
 
-template <int K, int V, typename TC> struct Rows {
-    static constexpr bool kCodes = sizeof(TC) == 1;
-    static constexpr int ES = sizeof(TC);
-    static constexpr int CK = K * ES / 16, CV = V * ES / 16;  // 16-byte chunks per row
-    static constexpr int KB = kTile * K * ES, VB = kTile * V * ES;
+template <int K, int V> struct Rows {
+    static constexpr int CK = K / 8, CV = V / 8;  // 16-byte chunks per row
+    static constexpr int KB = kTile * K * 2, VB = kTile * V * 2;
     static constexpr int KS = K / 16, DB = V / 32;
 
     // chunk c of token t lies at chunk c ^ swz(t) of its row: the tokens that one read takes
     // the same chunk of are spread over the banks
-    static __device__ __forceinline__ int swz_k(int t) {
-        return CK == 16 ? t & 15 : CK == 8 ? (t >> 1) & 7 : (t >> 2) & 3;
-    }
-    static __device__ __forceinline__ int swz_v(int t) {
-        if (kCodes) return CV == 8 ? 2 * ((t >> 1) & 1) + 4 * ((t >> 3) & 1) : 2 * ((t >> 3) & 1);
-        return CV == 16 ? (t & 3) * 4 : ((t >> 1) & 1) * 4;
-    }
+    static __device__ __forceinline__ int swz_k(int t) { return CK == 16 ? t & 15 : (t >> 1) & 7; }
+    static __device__ __forceinline__ int swz_v(int t) { return CV == 16 ? (t & 3) * 4 : ((t >> 1) & 1) * 4; }
 
     bf16x8 q[KS];
     f32x16 o[DB], s[2];
     bf16x8 p[4];
     float m, l;
 
-    // Row: channels that lane half h holds of its row at step ks, as the key fragments take them
-    static __device__ __forceinline__ int channel(int ks, int lane) {
-        return kCodes ? 32 * (ks >> 1) + 16 * (lane >> 5) + 8 * (ks & 1) : 16 * ks + 8 * (lane >> 5);
-    }
     // a negative scale is q's sign
     __device__ __forceinline__ void load_q(const bf16_t *row, bool negative, int lane) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) q[ks] = load_frag(row + channel(ks, lane));
+        for (int ks = 0; ks < KS; ++ks) q[ks] = load_frag(row + 16 * ks + 8 * (lane >> 5));
         const uint32_t sign = negative ? 0x80008000u : 0u;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
@@ -96,41 +79,23 @@ template <int K, int V, typename TC> struct Rows {
         for (int d = 0; d < DB; ++d) o[d] = f32x16{};
     }
 
-    // lx: the tile's exponents (codes only), 64 of keys, then 64 of values
-    __device__ __forceinline__ void scores(const char *lk, const char *lx, int lane) {
+    __device__ __forceinline__ void scores(const char *lk, int lane) {
         s[0] = s[1] = f32x16{};
-        const int h = lane >> 5;
-        if constexpr (!kCodes) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int t = 32 * b + (lane & 31);
-                    const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(lk + t * (2 * K) + 16 * ((2 * ks + h) ^ swz_k(t)));
-                    s[b] = mma32(kf, q[ks], s[b]);
-                }
-        } else {
-            float scale[2];  // the conversion takes a scale's exponent bits
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-                scale[b] = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint8_t *>(lx + 32 * b + (lane & 31))) << 23);
-#pragma unroll
-            for (int u = 0; u < KS / 2; ++u)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int t = 32 * b + (lane & 31);
-                    const u32x4 w = *reinterpret_cast<const u32x4 *>(lk + t * K + 16 * ((2 * u + h) ^ swz_k(t)));
-                    s[b] = mma32(codes_to_bf16(w[0], w[1], scale[b]), q[2 * u], s[b]);
-                    s[b] = mma32(codes_to_bf16(w[2], w[3], scale[b]), q[2 * u + 1], s[b]);
-                }
-        }
+            for (int b = 0; b < 2; ++b) {
+                const int t = 32 * b + (lane & 31);
+                const bf16x8 kf = *reinterpret_cast<const bf16x8 *>(lk + t * (2 * K) + 16 * ((2 * ks + (lane >> 5)) ^ swz_k(t)));
+                s[b] = mma32(kf, q[ks], s[b]);
+            }
     }
 
     // Order of the LDS reads (two per value fragment, one per key fragment) and products of a
-    // values() [if VALUES] and scores() in a row: reads run kAhead products ahead of their use,
+    // values() [if VALUES] and scores() [if SCORES] in a row: reads run kAhead products ahead of their use,
     // which covers their latency. Left to itself the compiler reads right before each product.
-    template <bool VALUES> static __device__ __forceinline__ void interleave() {
-        constexpr int kAhead = 4, PV = VALUES ? 4 * DB : 0, QK = 2 * KS;
+    template <bool VALUES, bool SCORES = true> static __device__ __forceinline__ void interleave() {
+        constexpr int kAhead = 4, PV = VALUES ? 4 * DB : 0, QK = SCORES ? 2 * KS : 0;
         auto reads = [](int i) { return i < PV ? 2 : i < PV + QK ? 1 : 0; };
         int first = 0;
 #pragma unroll
@@ -156,7 +121,7 @@ template <int K, int V, typename TC> struct Rows {
 
     // 2^(c s - m) in bf16, the running maximum and sum (c >= 0: q carries the scale's sign);
     // `sees`: a bit for each of the lane's 32 tokens that its row sees, used if MASKED
-    template <bool MASKED> __device__ __forceinline__ void softmax(float c, uint32_t sees, const char *lx, int lane) {
+    template <bool MASKED> __device__ __forceinline__ void softmax(float c, uint32_t sees) {
         if (MASKED) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -197,52 +162,33 @@ template <int K, int V, typename TC> struct Rows {
             float e[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                if (kCodes) {  // weights with the scales of their values, a power of two
-                    const uint32_t w = *reinterpret_cast<const uint32_t *>(lx + kTile + 16 * x + 8 * (j >> 2) + 4 * (lane >> 5));
-                    s[x >> 1][8 * (x & 1) + j] = scaled_by(s[x >> 1][8 * (x & 1) + j], w, j & 3);
-                }
                 e[j] = s[x >> 1][8 * (x & 1) + j];
             }
             p[x] = to_frag(e, bf16x8{});
         }
     }
 
-    // channels 32 d + l % 32, tokens 16 x + {0..3, 8..11} + 4 (l / 32): as read, and as bf16
-    using VRaw = typename std::conditional<kCodes, i32x2, bf16x8>::type;
-    static __device__ __forceinline__ VRaw v_read(const char *lv, int x, int d, int lane) {
-        const int i = lane & 15, h = lane >> 5, half = (lane >> 4) & 1;
-        if constexpr (kCodes) {
-            typedef __attribute__((address_space(3))) i32x2 lds2;
-            const int r = i >> 1, t = 16 * x + 8 * (r >> 2) + 4 * h + (r & 3);
-            return __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds2 *)(lv + t * V + 16 * ((2 * d + half) ^ swz_v(t)) + 8 * (i & 1)));
-        } else {
-            typedef __attribute__((address_space(3))) i16x4 lds4;
-            const int t = 16 * x + 4 * h + (i >> 2);
-            const int c = 4 * d + 2 * half + ((i >> 1) & 1);
-            const char *at = lv + t * (2 * V) + 16 * (c ^ swz_v(t)) + 8 * (i & 1);
-            const char *at2 = lv + (t + 8) * (2 * V) + 16 * (c ^ swz_v(t + 8)) + 8 * (i & 1);
-            const bf16x4 y = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)at));
-            const bf16x4 z = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)at2));
-            return (bf16x8){y[0], y[1], y[2], y[3], z[0], z[1], z[2], z[3]};
-        }
-    }
-    static __device__ __forceinline__ bf16x8 v_frag(VRaw r) {
-        if constexpr (kCodes) return codes_to_bf16(r[0], r[1], 1.f);
-        else return r;
+    // channels 32 d + l % 32, tokens 16 x + {0..3, 8..11} + 4 (l / 32)
+    static __device__ __forceinline__ bf16x8 v_frag(const char *lv, int x, int d, int lane) {
+        typedef __attribute__((address_space(3))) i16x4 lds4;
+        const int i = lane & 15, t = 16 * x + 4 * (lane >> 5) + (i >> 2);
+        const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
+        const char *at = lv + t * (2 * V) + 16 * (c ^ swz_v(t)) + 8 * (i & 1);
+        const char *at2 = lv + (t + 8) * (2 * V) + 16 * (c ^ swz_v(t + 8)) + 8 * (i & 1);
+        const bf16x4 y = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)at));
+        const bf16x4 z = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)at2));
+        return (bf16x8){y[0], y[1], y[2], y[3], z[0], z[1], z[2], z[3]};
     }
     // channel ch of token t
     static __device__ __forceinline__ float v_at(const char *lv, int t, int ch) {
-        const int byte = ch * ES;
-        const char *p = lv + t * (V * ES) + 16 * ((byte >> 4) ^ swz_v(t)) + (byte & 15);
-        if constexpr (kCodes) return static_cast<float>(codes_to_bf16(*reinterpret_cast<const uint8_t *>(p), 0, 1.f)[0]);
-        else return bf16_to_f32(*reinterpret_cast<const bf16_t *>(p));
+        return bf16_to_f32(*reinterpret_cast<const bf16_t *>(lv + t * (2 * V) + 16 * ((ch >> 3) ^ swz_v(t)) + 2 * (ch & 7)));
     }
 
     __device__ __forceinline__ void values(const char *lv, int lane) {
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int d = 0; d < DB; ++d) o[d] = mma32(v_frag(v_read(lv, x, d, lane)), p[x], o[d]);
+            for (int d = 0; d < DB; ++d) o[d] = mma32(v_frag(lv, x, d, lane), p[x], o[d]);
     }
 
     // The same where some rows do not see some tokens. A weight of zero would not keep an
@@ -257,7 +203,7 @@ template <int K, int V, typename TC> struct Rows {
             uint32_t odd = 0;
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
-                vf[d] = v_frag(v_read(lv, x, d, lane));
+                vf[d] = v_frag(lv, x, d, lane);
                 const u32x4 u = __builtin_bit_cast(u32x4, vf[d]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) odd |= (u[i] & 0x7F807F80u) + 0x00800080u;  // an exponent of ones carries
