@@ -6,7 +6,6 @@ not built, or a tensor is not on a GPU, the functions raise.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import Optional, Tuple
 
@@ -81,33 +80,63 @@ def _offsets(cu_seqlens: torch.Tensor) -> int:
 
 def _cache(N: int, cache_lens, page_table, k_cache, v_cache, k_exp, v_exp) -> KdaKvCache:
     """The call's cache, after checking its tensors against each other."""
-    for name, t in (("cache_lens", cache_lens), ("page_table", page_table), ("k_cache", k_cache), ("v_cache", v_cache)):
-        _dev(t, name)
-    if cache_lens.dtype != torch.int32 or tuple(cache_lens.shape) != (N,):
+    _dev(cache_lens, "cache_lens")
+    _dev(page_table, "page_table")
+    _dev(k_cache, "k_cache")
+    _dev(v_cache, "v_cache")
+    if cache_lens.dtype != torch.int32 or cache_lens.shape != (N,):
         raise ValueError("cache_lens must be int32 [N]")
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != N:
         raise ValueError("page_table must be int32 [N, max_pages]")
-    if k_cache.dim() != 4 or v_cache.dim() != 4 or k_cache.shape[:3] != v_cache.shape[:3] or k_cache.dtype != v_cache.dtype:
+    kind = k_cache.dtype
+    if k_cache.dim() != 4 or v_cache.dim() != 4 or k_cache.shape[:3] != v_cache.shape[:3] or v_cache.dtype != kind:
         raise ValueError("k_cache and v_cache must be [num_pages, Hk, page_size, d] of one dtype")
-    if k_cache.dtype not in _KV_CODES:
-        raise TypeError(f"unsupported cache dtype {k_cache.dtype}")
-    if k_cache.dtype == torch.float8_e4m3fn:
+    code = _KV_CODES.get(kind)
+    if code is None:
+        raise TypeError(f"unsupported cache dtype {kind}")
+    ke = ve = None
+    if code == KDA_KV_E4M3:
         for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
             if t is None:
                 raise ValueError(f"an e4m3 cache needs {name}")
             _dev(t, name)
             if t.dtype != torch.uint8 or t.shape != k_cache.shape[:3]:
                 raise ValueError(f"{name} must be uint8 [num_pages, Hk, page_size]")
+        ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
     elif k_exp is not None or v_exp is not None:
         raise ValueError("k_exp and v_exp are for e4m3 caches")
-    return KdaKvCache(k_cache.data_ptr(), v_cache.data_ptr(), None if k_exp is None else k_exp.data_ptr(),
-                      None if v_exp is None else v_exp.data_ptr(), page_table.data_ptr(), cache_lens.data_ptr(),
-                      k_cache.shape[0], k_cache.shape[2], page_table.shape[1], _KV_CODES[k_cache.dtype])
+    return KdaKvCache(k_cache.data_ptr(), v_cache.data_ptr(), ke, ve, page_table.data_ptr(), cache_lens.data_ptr(),
+                      k_cache.shape[0], k_cache.shape[2], page_table.shape[1], code)
+
+
+class _Here:
+    """A context that changes nothing."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _on(device):
+    """The device as the current one (entering torch.cuda.device costs more than asking)."""
+    return _HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _handle(stream, device) -> int:
+    """The stream to enqueue on, as its handle: the given one (of `device`), else the device's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return _stream(stream, device).value or 0
 
 
 def _alloc_on(stream):
     """New tensors of a call come from the pool of the stream that the call runs on."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    return _HERE if stream is None else torch.cuda.stream(stream)
 
 
 def kda_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, *,
@@ -128,8 +157,8 @@ def kda_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: 
         raise ValueError("inconsistent q/k/v shapes or dtypes")
     out_dtype = q.dtype if out_dtype is None else out_dtype
     device = q.device
-    with torch.cuda.device(device):
-        s = _stream(stream, device)
+    with _on(device):
+        s = _handle(stream, device)
         with _alloc_on(stream):
             o = _out(o, (T, H, d_v), out_dtype, device)
         _one_device(device, k, v, cu_seqlens, o)
@@ -162,9 +191,9 @@ def kda_kv_write(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, cac
     if k_cache.shape[1] != Hk or k_cache.shape[3] != d_k or v_cache.shape[3] != d_v:
         raise ValueError("k_cache and v_cache must have the heads and channels of k and v")
     _one_device(k.device, v, cu_seqlens, cache_lens, page_table, k_cache, v_cache, k_exp, v_exp)
-    with torch.cuda.device(k.device):
+    with _on(k.device):
         st = lib.kda_kv_write(k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), N, T, Hk, d_k, d_v, sk, sv,
-                              _code(k.dtype), ctypes.byref(cache), _stream(stream, k.device))
+                              _code(k.dtype), ctypes.byref(cache), _handle(stream, k.device))
     if st != KDA_OK:
         raise KDAError(st, "kda_kv_write")
 
@@ -183,8 +212,8 @@ def kda_kv_read(T: int, cu_seqlens: torch.Tensor, cache_lens: torch.Tensor, page
     cache = _cache(N, cache_lens, page_table, k_cache, v_cache, k_exp, v_exp)
     Hk, d_k, d_v = k_cache.shape[1], k_cache.shape[3], v_cache.shape[3]
     device = k_cache.device
-    with torch.cuda.device(device):
-        s = _stream(stream, device)
+    with _on(device):
+        s = _handle(stream, device)
         with _alloc_on(stream):
             k = _out(k, (T, Hk, d_k), out_dtype, device)
             v = _out(v, (T, Hk, d_v), out_dtype, device)
@@ -229,8 +258,8 @@ def kda_attn_cache_fwd(q: torch.Tensor, cu_seqlens: torch.Tensor, cache_lens: to
             raise ValueError("tree_mask must be int64 [T]")
     out_dtype = q.dtype if out_dtype is None else out_dtype
     device = q.device
-    with torch.cuda.device(device):
-        s = _stream(stream, device)
+    with _on(device):
+        s = _handle(stream, device)
         with _alloc_on(stream):
             o = _out(o, (T, H, d_v), out_dtype, device)
             if workspace is None:

@@ -22,30 +22,40 @@
 namespace kda {
 namespace {
 
-// Sequence n's place on the line.
+// Sequence n's place on the line. One unit of the line is a step of a (sequence, kv head,
+// row tile), or all of its steps where the line is not cut inside them (AttnArgs::whole).
 struct Seq {
     int start, count;  // its new tokens
     int ctx, end;      // tokens before them (may be below 0), cached tokens within the page table
     int tiles, steps;  // row tiles; steps per row tile
-    __device__ __forceinline__ int64_t units(int Hk) const { return static_cast<int64_t>(Hk) * tiles * steps; }
+    int per;           // units per row tile
+    __device__ __forceinline__ int64_t units(int Hk) const { return static_cast<int64_t>(Hk) * tiles * per; }
 };
 
-template <int R, int STEP> __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int n) {
+// from the sequence's rows and cached length
+template <int R, int STEP> __device__ __forceinline__ Seq seq_from(const AttnArgs &a, int start, int count, int len) {
     Seq s;
-    seq_rows(a.cu, n, a.T, s.start, s.count);
-    const int len = max(ld_meta(a.lens, n), 0);
+    s.start = start;
+    s.count = count;
+    len = max(len, 0);
     s.ctx = len - s.count;
     s.end = min(len, a.max_pages << a.page_shift);
     s.tiles = static_cast<int>((static_cast<int64_t>(s.count) * a.G + R - 1) / R);
     s.steps = max((s.end + STEP - 1) / STEP, 1);  // at least one, which writes the rows
+    s.per = a.whole ? 1 : s.steps;
     return s;
+}
+template <int R, int STEP> __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int n) {
+    int start, count;
+    seq_rows(a.cu, n, a.T, start, count);
+    return seq_from<R, STEP>(a, start, count, ld_meta(a.lens, n));
 }
 
 // A workgroup takes at least kMinSteps steps where the line is short, so that a
 // short cache is not cut into pieces that cost more to join than to read.
 constexpr int kMinSteps = 2;
-__device__ __forceinline__ int64_t line_workgroups(int64_t U, int W) {
-    const int64_t w = (U + kMinSteps - 1) / kMinSteps;
+__device__ __forceinline__ int64_t line_workgroups(const AttnArgs &a, int64_t U) {
+    const int64_t W = a.W, w = a.whole ? U : (U + kMinSteps - 1) / kMinSteps;
     return w < W ? max(w, static_cast<int64_t>(1)) : W;
 }
 __device__ __forceinline__ int64_t line_begin(int64_t w, int64_t U, int64_t W) { return w * U / W; }
@@ -65,60 +75,71 @@ __device__ __forceinline__ int64_t wave_scan(int64_t x, int lane) {
 __host__ __device__ inline size_t part_floats(int R, int V) { return static_cast<size_t>(R) * (V + 2); }
 __host__ __device__ inline size_t prefix_bytes(int N) { return (static_cast<size_t>(N) + 1) * 8 + 255 & ~static_cast<size_t>(255); }
 
-// Total of the line, and the sequence that holds unit u with the units before it. Workgroup-uniform.
-// Every thread of the workgroup calls it. prefix: written if not nullptr.
+// The line, as a wave sees it: 64 sequences at a time, one to a lane. Up to 64 sequences stay
+// in the lanes, so that the sequences of a workgroup cost no further loads.
 template <int R, int STEP> struct Line {
     int64_t total;
-    __device__ __forceinline__ void scan(const AttnArgs &a, int tid, int64_t (&sh)[kWaves], int64_t *prefix) {
-        const int lane = tid & 63, w = tid >> 6;
-        int64_t base = 0;
-        for (int n0 = 0; n0 < a.N; n0 += 64 * kWaves) {
-            const int n = n0 + tid;
-            const int64_t mine = n < a.N ? seq_of<R, STEP>(a, min(n, a.N - 1)).units(a.Hk) : 0;
-            const int64_t inc = wave_scan(mine, lane);
-            if (lane == 63) sh[w] = inc;
-            __syncthreads();
-            int64_t before = base, all = 0;
-#pragma unroll
-            for (int u = 0; u < kWaves; ++u) {
-                if (u < w) before += sh[u];
-                all += sh[u];
-            }
-            if (prefix && n < a.N) prefix[n] = before + inc - mine;
-            base += all;
-            __syncthreads();
+    int start, count, len;  // of sequence base + lane
+    int64_t before, mine;   // units before it, its own
+    int base;
+
+    __device__ __forceinline__ void load(const AttnArgs &a, int n0, int64_t units_before, int lane) {
+        base = n0;
+        const int n = n0 + lane;
+        start = count = len = 0;
+        mine = 0;
+        if (n < a.N) {
+            start = clampi(a.cu[n], 0, a.T);
+            count = clampi(a.cu[n + 1], start, a.T) - start;
+            len = a.lens[n];
+            mine = seq_from<R, STEP>(a, start, count, len).units(a.Hk);
         }
-        total = base;
-        if (prefix && tid == 0) prefix[a.N] = base;
+        before = wave_scan(mine, lane) - mine + units_before;
     }
-    // the sequence that holds unit u < total, and the line before it
-    __device__ __forceinline__ void find(const AttnArgs &a, int64_t u, int tid, int64_t (&sh)[kWaves], int &n_of,
-                                         int64_t &before_of, int &sh_n, int64_t &sh_before) const {
-        const int lane = tid & 63, w = tid >> 6;
-        int64_t base = 0;
-        for (int n0 = 0; n0 < a.N; n0 += 64 * kWaves) {
-            const int n = n0 + tid;
-            const int64_t mine = n < a.N ? seq_of<R, STEP>(a, min(n, a.N - 1)).units(a.Hk) : 0;
-            const int64_t inc = wave_scan(mine, lane);
-            if (lane == 63) sh[w] = inc;
-            __syncthreads();
-            int64_t before = base, all = 0;
-#pragma unroll
-            for (int x = 0; x < kWaves; ++x) {
-                if (x < w) before += sh[x];
-                all += sh[x];
-            }
-            before += inc - mine;
-            if (before <= u && u < before + mine) {
-                sh_n = n;
-                sh_before = before;
-            }
-            base += all;
-            __syncthreads();
-            if (u < base) break;
+    __device__ __forceinline__ int64_t end() const {  // units up to the last lane's
+        const int64_t x = before + mine;
+        return static_cast<int64_t>(__builtin_amdgcn_readlane(static_cast<int>(x >> 32), 63)) << 32 |
+               static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x & 0xFFFFFFFFll), 63));
+    }
+    // prefix: the units before each sequence, and in all; written if not nullptr
+    __device__ __forceinline__ void scan(const AttnArgs &a, int lane, int64_t *prefix) {
+        int64_t units = 0;
+        for (int n0 = 0; n0 < a.N; n0 += 64) {
+            load(a, n0, units, lane);
+            if (prefix && n0 + lane < a.N) prefix[n0 + lane] = before;
+            units = end();
         }
-        n_of = __builtin_amdgcn_readfirstlane(sh_n);
-        before_of = sh_before;
+        total = units;
+        if (prefix && lane == 0) prefix[a.N] = units;
+    }
+    // the sequence that holds unit u < total: `n`, and the units before it
+    __device__ __forceinline__ Seq find(const AttnArgs &a, int64_t u, int lane, int &n, int64_t &units_before) {
+        if (a.N > 64) {
+            int64_t units = 0;
+            for (int n0 = 0;; n0 += 64) {
+                load(a, n0, units, lane);
+                units = end();
+                if (u < units) break;
+            }
+        }
+        return take(a, __builtin_ctzll(__ballot(before <= u && u < before + mine)), n, units_before);
+    }
+    // the next sequence after n that has units: there is one
+    __device__ __forceinline__ Seq next(const AttnArgs &a, int lane, int &n, int64_t &units_before) {
+        for (;;) {
+            const int at = n - base + 1;
+            const uint64_t some = __ballot(mine > 0) & (at < 64 ? ~0ull << at : 0);
+            if (some) return take(a, __builtin_ctzll(some), n, units_before);
+            load(a, base + 64, end(), lane);
+            n = base - 1;
+        }
+    }
+    __device__ __forceinline__ Seq take(const AttnArgs &a, int at, int &n, int64_t &units_before) const {
+        n = base + at;
+        units_before = static_cast<int64_t>(__builtin_amdgcn_readlane(static_cast<int>(before >> 32), at)) << 32 |
+                       static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(before & 0xFFFFFFFFll), at));
+        return seq_from<R, STEP>(a, __builtin_amdgcn_readlane(start, at), __builtin_amdgcn_readlane(count, at),
+                                 __builtin_amdgcn_readlane(len, at));
     }
 };
 
@@ -174,36 +195,29 @@ __global__ __launch_bounds__(64 * kWaves) void attn_cache_kernel(AttnArgs a) {
     constexpr int R = S::R;
     __shared__ __align__(16) char lds[S::kLds];
     __shared__ float stat[2][kWaves][R];
-    __shared__ int64_t sh[kWaves];
-    __shared__ int sh_n;
-    __shared__ int64_t sh_before;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     char *lk = lds + w * (S::KB + S::VB), *lv = lk + S::KB;
 
     Line<R, kStep> line;
-    line.scan(a, tid, sh, blockIdx.x == 0 ? static_cast<int64_t *>(a.ws) : nullptr);
+    line.scan(a, lane, blockIdx.x == 0 && w == 0 && !a.whole ? static_cast<int64_t *>(a.ws) : nullptr);
     const int64_t U = line.total;
     if (U == 0) return;
-    const int64_t W = line_workgroups(U, a.W);
+    const int64_t W = line_workgroups(a, U);
     if (static_cast<int64_t>(blockIdx.x) >= W) return;
     int64_t u = line_begin(blockIdx.x, U, W);
     const int64_t u_end = line_begin(blockIdx.x + 1, U, W);
     if (u >= u_end) return;
     int n;
     int64_t before;
-    line.find(a, u, tid, sh, n, before, sh_n, sh_before);
-    Seq q = seq_of<R, kStep>(a, n);
+    Seq q = line.find(a, u, lane, n, before);
     bool first = true;
 
     S st;
     while (u < u_end) {
-        while (u >= before + q.units(a.Hk)) {  // the next sequence with work: there is one, u < U
-            before += q.units(a.Hk);
-            q = seq_of<R, kStep>(a, ++n);
-        }
+        if (u >= before + q.units(a.Hk)) q = line.next(a, lane, n, before);
         const int64_t in = u - before;
-        const int item = static_cast<int>(in / q.steps), t0 = static_cast<int>(in - static_cast<int64_t>(item) * q.steps);
-        const int t1 = static_cast<int>(min(static_cast<int64_t>(q.steps), t0 + (u_end - u)));
+        const int item = static_cast<int>(in / q.per), t0 = static_cast<int>(in - static_cast<int64_t>(item) * q.per);
+        const int t1 = a.whole ? q.steps : static_cast<int>(min(static_cast<int64_t>(q.steps), t0 + (u_end - u)));
         const int kvh = item / q.tiles, r0 = (item - kvh * q.tiles) * R;
         const int rows = static_cast<int>(min(static_cast<int64_t>(R), static_cast<int64_t>(q.count) * a.G - r0));
         const bool whole = t0 == 0 && t1 == q.steps;
@@ -261,9 +275,14 @@ __global__ __launch_bounds__(64 * kWaves) void attn_cache_kernel(AttnArgs a) {
             });
         }
         first = false;
-        u += t1 - t0;
+        u += a.whole ? 1 : t1 - t0;
     }
 }
+
+// Up to this many tokens a (sequence, kv head, row tile) is one unit of the line, and there is
+// nothing to join: one step more or less costs about a microsecond, joining about five (its
+// launch and its reads).
+constexpr int kWhole = 4 * kStep;
 
 // Joins the pieces of the (sequence, kv head, row tile)s that the line was cut inside: a
 // workgroup takes up to 16 rows of one. Groups of V / 4 lanes take a row each; where there are
@@ -286,7 +305,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
     const int rows = static_cast<int>(min(static_cast<int64_t>(kJoinRows), static_cast<int64_t>(q.count) * a.G - r0));
     if (rows <= 0) return;
     const int64_t *prefix = static_cast<const int64_t *>(a.ws);
-    const int64_t U = prefix[a.N], W = line_workgroups(U, a.W);
+    const int64_t U = prefix[a.N], W = line_workgroups(a, U);
     const int64_t s = prefix[n] + (static_cast<int64_t>(kvh) * q.tiles + tile) * q.steps, e = s + q.steps;
     const int64_t w0 = line_owner(s, U, W), w1 = line_owner(e - 1, U, W);
     if (w0 == w1) return;
@@ -400,37 +419,30 @@ __global__ __launch_bounds__(256, 2) void attn_cache_rows_kernel(AttnArgs a) {
     using X = Rows<K, V>;
     constexpr int R = T::R;
     __shared__ __align__(1024) char lds[T::kLds];
-    __shared__ int64_t sh[kWaves];
-    __shared__ int sh_n;
-    __shared__ int64_t sh_before;
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     Line<R, kTile> line;
-    line.scan(a, tid, sh, blockIdx.x == 0 ? static_cast<int64_t *>(a.ws) : nullptr);
+    line.scan(a, lane, blockIdx.x == 0 && w == 0 && !a.whole ? static_cast<int64_t *>(a.ws) : nullptr);
     const int64_t U = line.total;
     if (U == 0) return;
-    const int64_t W = line_workgroups(U, a.W);
+    const int64_t W = line_workgroups(a, U);
     if (static_cast<int64_t>(blockIdx.x) >= W) return;
     int64_t u = line_begin(blockIdx.x, U, W);
     const int64_t u_end = line_begin(blockIdx.x + 1, U, W);
     if (u >= u_end) return;
     int n;
     int64_t before;
-    line.find(a, u, tid, sh, n, before, sh_n, sh_before);
-    Seq q = seq_of<R, kTile>(a, n);
+    Seq q = line.find(a, u, lane, n, before);
     bool first = true;
     const uint32_t base = lds_address(lds);
     const float c = fabsf(a.c);
 
     X st;
     while (u < u_end) {
-        while (u >= before + q.units(a.Hk)) {  // the next sequence with work: there is one, u < U
-            before += q.units(a.Hk);
-            q = seq_of<R, kTile>(a, ++n);
-        }
+        if (u >= before + q.units(a.Hk)) q = line.next(a, lane, n, before);
         const int64_t in = u - before;
-        const int item = static_cast<int>(in / q.steps), t0 = static_cast<int>(in - static_cast<int64_t>(item) * q.steps);
-        const int t1 = static_cast<int>(min(static_cast<int64_t>(q.steps), t0 + (u_end - u)));
+        const int item = static_cast<int>(in / q.per), t0 = static_cast<int>(in - static_cast<int64_t>(item) * q.per);
+        const int t1 = a.whole ? q.steps : static_cast<int>(min(static_cast<int64_t>(q.steps), t0 + (u_end - u)));
         const int kvh = item / q.tiles, r0 = (item - kvh * q.tiles) * R;
         const int rows = static_cast<int>(min(static_cast<int64_t>(R), static_cast<int64_t>(q.count) * a.G - r0));
         const bool whole = t0 == 0 && t1 == q.steps;
@@ -525,7 +537,7 @@ __global__ __launch_bounds__(256, 2) void attn_cache_rows_kernel(AttnArgs a) {
             }
         }
         first = false;
-        u += t1 - t0;
+        u += a.whole ? 1 : t1 - t0;
     }
 }
 
@@ -538,8 +550,7 @@ int tile_rows(int64_t T, int64_t N, int64_t G, bool f32) {
 
 template <int V, int R, int STEP> hipError_t launch_join(const AttnArgs &a, hipStream_t st) {
     const hipError_t e = hipGetLastError();
-    // one step per (sequence, kv head, row tile) at most: the line is never cut inside one
-    if (e != hipSuccess || (a.max_pages << a.page_shift) <= STEP) return e;
+    if (e != hipSuccess || a.whole) return e;
     const int64_t slots = static_cast<int64_t>(a.T) * a.G / R + a.N;
     hipLaunchKernelGGL((attn_join_kernel<V, R, STEP>), dim3(static_cast<unsigned>(slots * a.Hk * (R / kJoinRows))),
                        dim3(kJoinThreads), 0, st, a);
@@ -573,6 +584,7 @@ size_t attn_cache_workspace(int32_t N, int32_t T, int32_t H, int32_t Hk, int32_t
 hipError_t launch_attn_cache(const AttnArgs &args, hipStream_t st) {
     AttnArgs a = args;
     a.W = attn_cache_workgroups();
+    a.whole = (a.max_pages << a.page_shift) <= kWhole;
     if (a.K == 128) return a.V == 128 ? launch_dims<128, 128>(a, st) : launch_dims<128, 64>(a, st);
     return a.V == 128 ? launch_dims<64, 128>(a, st) : launch_dims<64, 64>(a, st);
 }

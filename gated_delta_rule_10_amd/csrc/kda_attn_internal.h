@@ -31,6 +31,7 @@ struct AttnArgs {
     kda_dtype_t in_dtype, out_dtype;
     kda_kv_dtype_t kv_dtype;
     int32_t W;                   // workgroups that share the call's work (cache only)
+    int32_t whole;               // cache only: no (sequence, kv head, row tile) is shared among workgroups
 };
 
 struct KvArgs {

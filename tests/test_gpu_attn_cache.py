@@ -93,6 +93,16 @@ def test_many_sequences():
     run(11, new, [(37 * n) % 90 for n in range(600)], 2, 1, 64, 64, 16, "bf16", "e4m3")
 
 
+@pytest.mark.parametrize("new", [1, 5])
+def test_many_sequences_and_a_long_one(new):
+    """The work is shared out over 64 sequences at a time, here with pieces that start behind sequences
+    without new tokens, and with a whole run of 64 that has none."""
+    count = [0 if 70 <= n < 140 else new if n % 3 else 0 for n in range(200)]
+    ctx = [(53 * n) % 300 if n != 150 else 3000 for n in range(200)]
+    run(26, count, ctx, 6, 1, 64, 64, 16, "bf16", "e4m3")
+    run(27, count, ctx, 6, 2, 64, 64, 16, "bf16", "bf16")
+
+
 def test_page_table_far_longer_than_the_sequences():
     run(12, [1, 1], [20, 150], 4, 2, 64, 64, 16, "bf16", "bf16", max_pages=5000)
 
