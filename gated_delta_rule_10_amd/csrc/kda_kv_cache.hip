@@ -2,8 +2,9 @@
 // rounding to e4m3 where the cache holds codes, and reading them back
 // (kda_kv_read). Both move each byte once; they are bound by memory.
 //
-// A (token, kv head) row of d elements is handled by d / 8 lanes (8 elements
-// each), keys and values in the same launch.
+// A workgroup takes 64 (token, kv head) rows of keys and of values, d / 8 lanes
+// (8 elements each) to a row. One lane per row finds its place in the cache
+// (sequence, page, offset) for all of them, while the first loads are on their way.
 //
 // e4m3: with a = max |x| of the row's finite elements = f 2^p (1/2 <= f < 1),
 // the least e with a <= 448 2^e = (7/8) 2^(9 + e) is p - 9 if f <= 7/8, else
@@ -15,33 +16,24 @@
 namespace kda {
 namespace {
 
-// Where new token t of the call lies: its page's first row (of Hk * page rows) and offset,
-// or false if it has no place.
-struct Place { int64_t page; int off; };
-__device__ __forceinline__ bool place_of(const KvArgs &a, int t, Place &p) {
+// Where new token t of the call lies: the row of its kv head h in [pages, Hk, page], kNowhere if
+// it has no place, kOutside if it is in no sequence.
+constexpr int64_t kNowhere = -1, kOutside = -2;
+__device__ __forceinline__ int64_t place_of(const KvArgs &a, int t, int h) {
     const int n = seq_of_token(a.cu, a.N, t);
     const int start = clampi(a.cu[n], 0, a.T), end = clampi(a.cu[n + 1], start, a.T);
-    if (t < start || t >= end) return false;
+    if (t < start || t >= end) return kOutside;
     const int64_t pos = static_cast<int64_t>(a.lens[n]) - (end - t);
-    if (pos < 0 || (pos >> a.page_shift) >= a.max_pages) return false;
+    if (pos < 0 || (pos >> a.page_shift) >= a.max_pages) return kNowhere;
     const int id = a.table[static_cast<int64_t>(n) * a.max_pages + (pos >> a.page_shift)];
-    if (id < 0 || id >= a.num_pages) return false;
-    p.page = id;
-    p.off = static_cast<int>(pos & ((1 << a.page_shift) - 1));
-    return true;
-}
-// whether t belongs to a sequence at all
-__device__ __forceinline__ bool in_batch(const KvArgs &a, int t) {
-    const int n = seq_of_token(a.cu, a.N, t);
-    const int start = clampi(a.cu[n], 0, a.T), end = clampi(a.cu[n + 1], start, a.T);
-    return t >= start && t < end;
+    if (id < 0 || id >= a.num_pages) return kNowhere;
+    return ((static_cast<int64_t>(id) * a.Hk + h) << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
 }
 
 template <typename T> struct alignas(16) Eight { T x[8]; };
 
 template <int D, typename T, kda_kv_dtype_t KV>
-__device__ __forceinline__ void write_row(const T *src, void *cache, uint8_t *exps, int64_t row, int c) {
-    const Eight<T> in = *reinterpret_cast<const Eight<T> *>(src + 8 * c);
+__device__ __forceinline__ void write_row(const Eight<T> &in, void *cache, uint8_t *exps, int64_t row, int c) {
     if constexpr (KV != KDA_KV_E4M3) {
         *reinterpret_cast<Eight<T> *>(static_cast<T *>(cache) + row * D + 8 * c) = in;
     } else {
@@ -107,40 +99,67 @@ __device__ __forceinline__ void read_row(T *dst, const void *cache, const uint8_
     }
 }
 
-constexpr int kThreads = 256;
-__host__ __device__ inline unsigned key_blocks(int64_t rows, int d) {
-    return static_cast<unsigned>((rows * (d / 8) + kThreads - 1) / kThreads);
-}
+constexpr int kThreads = 256, kRows = 64;
 
 template <int K, int V, typename T, kda_kv_dtype_t KV, bool WRITE>
 __global__ __launch_bounds__(kThreads) void kv_kernel(KvArgs a) {
-    constexpr int LK = K / 8, LV = V / 8;  // lanes of a (token, head) row
-    // the first key_blocks workgroups take the keys, the others the values
-    const int64_t rows = static_cast<int64_t>(a.T) * a.Hk;
-    const unsigned kb = key_blocks(rows, K);
-    const bool isv = blockIdx.x >= kb;
-    const int64_t at = static_cast<int64_t>(isv ? blockIdx.x - kb : blockIdx.x) * kThreads + threadIdx.x;
-    const int64_t row = isv ? at / LV : at / LK;
-    const int c = static_cast<int>(isv ? at % LV : at % LK);
-    if (row >= rows) return;
-    const int t = static_cast<int>(row / a.Hk), h = static_cast<int>(row - static_cast<int64_t>(t) * a.Hk);
-    Place p{0, 0};
-    const bool there = place_of(a, t, p);
-    const int64_t crow = ((p.page * a.Hk + h) << a.page_shift) + p.off;
-    if constexpr (WRITE) {
-        if (!there) return;
-        if (!isv) write_row<K, T, KV>(static_cast<const T *>(a.k) + t * a.ks + h * K, a.kc, a.kexp, crow, c);
-        else write_row<V, T, KV>(static_cast<const T *>(a.v) + t * a.vs + h * V, a.vc, a.vexp, crow, c);
-    } else {
-        if (!there && !in_batch(a, t)) return;
-        if (!isv) read_row<K, T, KV>(static_cast<T *>(a.k) + t * a.ks + h * K, a.kc, a.kexp, crow, there, c);
-        else read_row<V, T, KV>(static_cast<T *>(a.v) + t * a.vs + h * V, a.vc, a.vexp, crow, there, c);
+    constexpr int LK = K / 8, LV = V / 8;  // lanes of a row
+    constexpr int IK = kRows * LK / kThreads, IV = kRows * LV / kThreads;
+    __shared__ int64_t place[kRows];
+    const int tid = threadIdx.x;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows, left = static_cast<int64_t>(a.T) * a.Hk - r0;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(kRows), left));
+    const int t0 = static_cast<int>(r0 / a.Hk), h0 = static_cast<int>(r0 - static_cast<int64_t>(t0) * a.Hk);
+    // row r of the workgroup: token t0 + x / Hk, head x % Hk, x = h0 + r
+    auto at = [&](int r, int64_t stride, int d) {
+        const int x = h0 + r, t = x / a.Hk;
+        return static_cast<int64_t>(t0 + t) * stride + (x - t * a.Hk) * d;
+    };
+    Eight<T> k[IK], v[IV];
+    if (WRITE) {
+#pragma unroll
+        for (int i = 0; i < IK; ++i) {
+            const int r = i * (kThreads / LK) + tid / LK;
+            if (r < rows) k[i] = *reinterpret_cast<const Eight<T> *>(static_cast<const T *>(a.k) + at(r, a.ks, K) + 8 * (tid % LK));
+        }
+#pragma unroll
+        for (int i = 0; i < IV; ++i) {
+            const int r = i * (kThreads / LV) + tid / LV;
+            if (r < rows) v[i] = *reinterpret_cast<const Eight<T> *>(static_cast<const T *>(a.v) + at(r, a.vs, V) + 8 * (tid % LV));
+        }
+    }
+    if (tid < rows) {
+        const int x = h0 + tid, t = x / a.Hk;
+        place[tid] = place_of(a, t0 + t, x - t * a.Hk);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < IK; ++i) {
+        const int r = i * (kThreads / LK) + tid / LK, c = tid % LK;
+        if (r >= rows) continue;
+        const int64_t p = place[r];
+        if (WRITE) {
+            if (p >= 0) write_row<K, T, KV>(k[i], a.kc, a.kexp, p, c);
+        } else if (p != kOutside) {
+            read_row<K, T, KV>(static_cast<T *>(a.k) + at(r, a.ks, K), a.kc, a.kexp, p, p >= 0, c);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < IV; ++i) {
+        const int r = i * (kThreads / LV) + tid / LV, c = tid % LV;
+        if (r >= rows) continue;
+        const int64_t p = place[r];
+        if (WRITE) {
+            if (p >= 0) write_row<V, T, KV>(v[i], a.vc, a.vexp, p, c);
+        } else if (p != kOutside) {
+            read_row<V, T, KV>(static_cast<T *>(a.v) + at(r, a.vs, V), a.vc, a.vexp, p, p >= 0, c);
+        }
     }
 }
 
 template <int K, int V, bool WRITE> hipError_t launch_dims(const KvArgs &a, hipStream_t st) {
     const int64_t rows = static_cast<int64_t>(a.T) * a.Hk;
-    const dim3 grid(key_blocks(rows, K) + key_blocks(rows, V)), block(kThreads);
+    const dim3 grid(static_cast<unsigned>((rows + kRows - 1) / kRows)), block(kThreads);
     if (a.kv_dtype == KDA_KV_F32)
         hipLaunchKernelGGL((kv_kernel<K, V, float, KDA_KV_F32, WRITE>), grid, block, 0, st, a);
     else if (a.kv_dtype == KDA_KV_BF16 && a.dtype == KDA_BF16)
