@@ -19,6 +19,9 @@
 // joins them in the order of the line, so results do not depend on timing.
 #include "kda_attn_stream.h"
 
+#ifndef KDA_PER
+#define KDA_PER 2
+#endif
 namespace kda {
 namespace {
 
@@ -189,8 +192,11 @@ struct Pages {
     }
 };
 
+// workgroups to a compute unit, as registers and LDS allow
+template <typename TC> constexpr int kPerCu = sizeof(TC) == 4 ? 1 : sizeof(TC) == 2 ? 2 : KDA_PER;
+
 template <int K, int V, int RT, typename TC>
-__global__ __launch_bounds__(64 * kWaves) void attn_cache_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * kWaves, kPerCu<TC>) void attn_cache_kernel(AttnArgs a) {
     using S = Stream<K, V, RT, TC>;
     constexpr int R = S::R;
     __shared__ __align__(16) char lds[S::kLds];
@@ -230,33 +236,35 @@ __global__ __launch_bounds__(64 * kWaves) void attn_cache_kernel(AttnArgs a) {
         st.load_q(a, q.start, kvh, r0, rows, lane);
         Pages pages;
         pages.begin(a, n, t0 * kStep, lane);
-        bool here[2] = {false, false}, soon[2] = {false, false};
-        auto load = [&](int t, bool (&there)[2]) {
-            const int p0 = t * kStep + w * kStepWave;
+        // this wave's steps: those with a token that some row sees
+        const int te = min(t1, (last - w * kStepWave + kStep - 1) / kStep);
+        auto load = [&](int t, typename S::Ahead &n) {
             pages.reach(a, t * kStep, lane);
             int64_t row[2];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                row[b] = pages.row(a, kvh, p0 + 16 * b);
-                there[b] = pages.exists(a, p0 + 16 * b);
+                const int pos = t * kStep + w * kStepWave + 16 * b;
+                row[b] = pages.row(a, kvh, pos);
+                n.here[b] = pages.exists(a, pos);
             }
-            st.load_cache(a, row, lane);
+            S::load_cache(n, a, row, lane);
         };
-        if (t0 * kStep + w * kStepWave < last) load(t0, here);
-        for (int t = t0; t < t1; ++t) {
+        // Loads past the last step read that step again, so that every step has as many behind it.
+        auto step = [&](int t, typename S::Ahead &n) {
             const int p0 = t * kStep + w * kStepWave;
-            if (p0 >= last) break;  // wave-uniform; later steps lie further on
-            const bool masked = p0 + kStepWave > open || !here[0] || !here[1];
-            const uint32_t kx[2] = {st.ke[0], st.ke[1]}, vx[2] = {st.ve[0], st.ve[1]};
+            const bool masked = p0 + kStepWave > open || !n.here[0] || !n.here[1];
+            const uint32_t kx[2] = {n.ke[0], n.ke[1]}, vx[2] = {n.ve[0], n.ve[1]};
             uint32_t sees[RT];
-            if (masked) st.visible(sees, a, q.start, r0, rows, p0, q.ctx, q.end, here, lane);
-            const bool odd = st.stage(lk, lv, masked, p0, q.end, here, lane);
-            if (t + 1 < t1 && p0 + kStep < last) load(t + 1, soon);
+            if (masked) st.visible(sees, a, q.start, r0, rows, p0, q.ctx, q.end, n.here, lane);
+            const bool odd = S::stage(n, lk, lv, masked, p0, q.end, lane);
+            load(min(t + 1, te - 1), n);
             __builtin_amdgcn_wave_barrier();
             st.step(lk, lv, a.c, masked, sees, odd, kx, vx, lane);
             __builtin_amdgcn_wave_barrier();
-            here[0] = soon[0];
-            here[1] = soon[1];
+        };
+        if (t0 < te) {
+            load(t0, st.next);
+            for (int t = t0; t < te; ++t) step(t, st.next);
         }
         __syncthreads();  // the join takes the waves' LDS
         if (whole) {
@@ -297,7 +305,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
     constexpr int PARTS = R / kJoinRows;
     const int part_of = blockIdx.x % PARTS, rest = blockIdx.x / PARTS, kvh = rest % a.Hk;
     const int64_t slot = rest / a.Hk;
-    const int n = seq_of_slot(a.cu, a.N, a.T, a.G, R, slot);
+    const int n = seq_of_slot(a.cu, a.N, a.T, a.G, R, slot, tid & 63);
     const Seq q = seq_of<R, STEP>(a, n);
     const int64_t tile = slot - static_cast<int64_t>(q.start) * a.G / R - n;
     if (tile < 0 || tile >= q.tiles) return;
@@ -508,14 +516,7 @@ __global__ __launch_bounds__(256, 2) void attn_cache_rows_kernel(AttnArgs a) {
         }
         for (; t < te; ++t, there = t < te ? turn(t) : 0) {
             if (!some) continue;
-            uint32_t sees = 0;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int pos = t * kTile + X::token(i, lane), b = pos - q.ctx;
-                bool see = b < 0 || (a.mask ? b < 64 && ((bits >> (b & 63)) & 1u) : b <= tok);
-                see = see && pos < q.end && ((there >> (i >> 3)) & 1u);
-                sees |= static_cast<uint32_t>(see) << i;
-            }
+            const uint32_t sees = X::of_lane(seen_tokens(a.mask != nullptr, bits, t * kTile, q.ctx, q.ctx + tok, q.end, there), lane);
             const char *lk = tile(t), *lv = lk + X::KB;
             st.scores(lk, lane);
             st.template softmax<true>(c, sees);
@@ -574,7 +575,7 @@ template <int K, int V> hipError_t launch_dims(const AttnArgs &a, hipStream_t st
 
 }  // namespace
 
-int32_t attn_cache_workgroups() { return 2 * compute_units(); }
+int32_t attn_cache_workgroups() { return KDA_PER * compute_units(); }
 
 size_t attn_cache_workspace(int32_t N, int32_t T, int32_t H, int32_t Hk, int32_t V, kda_dtype_t in_dtype) {
     const int R = tile_rows(T, N, H / Hk, in_dtype == KDA_F32);

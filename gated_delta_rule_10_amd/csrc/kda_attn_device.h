@@ -105,23 +105,47 @@ template <> __device__ __forceinline__ bool not_finite<e4m3_t>(uint32_t x) {
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
 
+// the n lowest bits (none for n <= 0, all 64 from 64 on)
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
+// Which of the 64 tokens from position p0 on a row sees, as bits: all before position `ctx`, and
+// new token b = position - ctx if bit b of `bits` is set or, without a mask, up to `own`;
+// none from position `end` on, and none of a group of 16 tokens whose bit in `here` is not set.
+__device__ __forceinline__ uint64_t seen_tokens(bool mask, uint64_t bits, int p0, int ctx, int own, int end, uint32_t here) {
+    const int b = p0 - ctx;  // of the first token
+    uint64_t w = low_bits(own - p0 + 1);
+    if (mask) w = b >= 64 ? 0 : b >= 0 ? bits >> b : b <= -64 ? ~0ull : bits << -b | low_bits(-b);
+    const uint64_t groups = (here & 1 ? 0xFFFFull : 0) | (here & 2 ? 0xFFFFull << 16 : 0) | (here & 4 ? 0xFFFFull << 32 : 0) |
+                            (here & 8 ? 0xFFFFull << 48 : 0);
+    return w & low_bits(end - p0) & groups;
+}
+
 // Rows [start, start + count) of sequence n, inside [0, T] whatever cu holds.
 __device__ __forceinline__ void seq_rows(const int32_t *cu, int n, int T, int &start, int &count) {
     start = clampi(ld_meta(cu, n), 0, T);
     count = clampi(ld_meta(cu, n + 1), start, T) - start;
 }
 
+// The last n in [0, N) with key(n) <= s, for keys that do not fall (0 if there is none; in [0, N)
+// whatever the keys). A wave looks at 64 of them at a time: one load for up to 64 sequences, and
+// none for one. All lanes take part and get the same answer.
+template <typename Key> __device__ __forceinline__ int wave_last_upto(int N, int64_t s, int lane, Key key) {
+    int lo = 0, len = N;
+    while (len > 1) {
+        const int step = (len + 63) / 64, at = lane * step;
+        const bool upto = at < len && key(lo + at) <= s;
+        const int i = max(__popcll(__ballot(upto)) - 1, 0) * step;
+        lo += i;
+        len = min(step, len - i);
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
 // Slot s of the slots that tiles of R rows take: a sequence with G rows per
 // token owns the slots from floor(G cu[n] / R) + n on, at least as many as its
-// ceil(G L / R) tiles, so a slot finds its sequence by binary search alone.
-__device__ __forceinline__ int seq_of_slot(const int32_t *cu, int N, int T, int G, int R, int64_t s) {
-    int lo = 0, hi = N - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (static_cast<int64_t>(clampi(ld_meta(cu, mid), 0, T)) * G / R + mid <= s) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
+// ceil(G L / R) tiles, so a slot finds its sequence from cu alone.
+__device__ __forceinline__ int seq_of_slot(const int32_t *cu, int N, int T, int G, int R, int64_t s, int lane) {
+    return wave_last_upto(N, s, lane, [&](int n) { return static_cast<int64_t>(clampi(cu[n], 0, T)) * G / R + n; });
 }
 
 // Sequence of token t < cu[N]: the last n with cu[n] <= t.

@@ -20,7 +20,7 @@ __global__ __launch_bounds__(64 * kWaves) void attn_prompt_kernel(AttnArgs a, in
 
     const int kvh = blockIdx.x % a.Hk;
     const int64_t slot = slots - 1 - static_cast<int>(blockIdx.x / a.Hk);  // the longest first
-    const int n = seq_of_slot(a.cu, a.N, a.T, a.G, R, slot);
+    const int n = seq_of_slot(a.cu, a.N, a.T, a.G, R, slot, lane);
     int start, count;
     seq_rows(a.cu, n, a.T, start, count);
     const int64_t first = (slot - static_cast<int64_t>(start) * a.G / R - n) * R;
@@ -32,15 +32,15 @@ __global__ __launch_bounds__(64 * kWaves) void attn_prompt_kernel(AttnArgs a, in
     S st;
     st.reset();
     st.load_q(a, start, kvh, r0, rows, lane);
-    const bool here[2] = {true, true};
     const uint32_t none[2] = {0, 0};
-    if (w * kStepWave < last) st.load_packed(a, start, kvh, w * kStepWave, lane);
+    auto &ahead = st.next;
+    if (w * kStepWave < last) S::load_packed(ahead, a, start, kvh, w * kStepWave, lane);
     for (int p0 = w * kStepWave; p0 < last; p0 += kStep) {
         const bool masked = p0 + kStepWave > open;
         uint32_t sees[RT];
-        if (masked) st.visible(sees, a, start, r0, rows, p0, 0, count, here, lane);
-        const bool odd = st.stage(lk, lv, masked, p0, count, here, lane);
-        if (p0 + kStep < last) st.load_packed(a, start, kvh, p0 + kStep, lane);
+        if (masked) st.visible(sees, a, start, r0, rows, p0, 0, count, ahead.here, lane);
+        const bool odd = S::stage(ahead, lk, lv, masked, p0, count, lane);
+        if (p0 + kStep < last) S::load_packed(ahead, a, start, kvh, p0 + kStep, lane);
         __builtin_amdgcn_wave_barrier();
         st.step(lk, lv, a.c, masked, sees, odd, none, none, lane);
         __builtin_amdgcn_wave_barrier();
@@ -91,14 +91,6 @@ __global__ __launch_bounds__(64 * kWaves) void attn_prompt_kernel(AttnArgs a, in
         }
     };
 
-// the lane's tokens of a tile up to `top` (which may be below 0 or past the tile), as bits
-__device__ __forceinline__ uint32_t seen_upto(int top, int lane) {
-    uint32_t v = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v |= static_cast<uint32_t>(Rows<64, 64>::token(i, lane) <= top) << i;
-    return v;
-}
-
 template <int K, int V, int NW>
 __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a, int slots) {
     using P = Rows<K, V>;
@@ -108,7 +100,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
 
     const int kvh = blockIdx.x % a.Hk;
     const int64_t slot = slots - 1 - static_cast<int>(blockIdx.x / a.Hk);  // the longest first
-    const int n = seq_of_slot(a.cu, a.N, a.T, a.G, R, slot);
+    const int n = seq_of_slot(a.cu, a.N, a.T, a.G, R, slot, lane);
     int start, count;
     seq_rows(a.cu, n, a.T, start, count);
     const int64_t first = (slot - static_cast<int64_t>(start) * a.G / R - n) * R;
@@ -198,7 +190,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
             copy_v(j + 1);
         }
         if (sees(j)) {
-            seen = seen_upto(own - j * kTile, lane);
+            seen = P::of_lane(low_bits(own - j * kTile + 1), lane);
             st.template softmax<true>(c, seen);
         }
         swap(ahead);

@@ -114,9 +114,14 @@ template <int K, int V> struct Rows {
         else if (n == 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
 
-    // token of the tile that bit (register) 16 b + i of the lane is
-    static __device__ __forceinline__ int token(int bit, int lane) {
-        return 32 * (bit >> 4) + 8 * ((bit & 15) >> 2) + 4 * (lane >> 5) + (bit & 3);
+    // of a row's bits for the 64 tokens, those of the lane's registers: bit 16 b + i of the result
+    // is token 32 b + 8 (i / 4) + 4 (l / 32) + i % 4
+    static __device__ __forceinline__ uint32_t of_lane(uint64_t w, int lane) {
+        w >>= 4 * (lane >> 5);
+        uint32_t v = 0;
+#pragma unroll
+        for (int n = 0; n < 8; ++n) v |= (static_cast<uint32_t>(w >> (8 * n)) & 15u) << (4 * n);
+        return v;
     }
 
     // 2^(c s - m) in bf16, the running maximum and sum (c >= 0: q carries the scale's sign);

@@ -55,8 +55,12 @@ template <int K, int V, int RT, typename TC> struct Stream {
     Frag q[RT][KT];
     f32x4 o[VT][RT];
     float m[RT], l[RT];  // per row l % 16 of each 16-row block; l is this lane's share
-    u32x4 kr[NK], vr[NV];
-    uint32_t ke[2], ve[2];
+    // keys, values and exponents on their way, of the next step
+    struct Ahead {
+        u32x4 kr[NK], vr[NV];
+        uint32_t ke[2], ve[2];
+        bool here[2];  // whether the pages of the two groups of 16 tokens exist
+    } next;
 
     __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -85,7 +89,7 @@ template <int K, int V, int RT, typename TC> struct Stream {
     // ---- sources: chunk x of a wave's 32 tokens
     // cache: row[b] is the cache row of the first of tokens 16 b .. 16 b + 15 (a page ends at a multiple of
     // 16, so the 16 rows lie behind one another)
-    __device__ __forceinline__ void load_cache(const AttnArgs &a, const int64_t (&row)[2], int lane) {
+    static __device__ __forceinline__ void load_cache(Ahead &n, const AttnArgs &a, const int64_t (&row)[2], int lane) {
         const char *k[2], *v[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -95,60 +99,61 @@ template <int K, int V, int RT, typename TC> struct Stream {
         const uint32_t at = 16 * lane;
 #pragma unroll
         for (int x = 0; x < NK; ++x)
-            kr[x] = *reinterpret_cast<const u32x4 *>(k[2 * x / NK] + at + (x % (NK / 2)) * 1024);
+            n.kr[x] = *reinterpret_cast<const u32x4 *>(k[2 * x / NK] + at + (x % (NK / 2)) * 1024);
 #pragma unroll
         for (int x = 0; x < NV; ++x)
-            vr[x] = *reinterpret_cast<const u32x4 *>(v[2 * x / NV] + at + (x % (NV / 2)) * 1024);
+            n.vr[x] = *reinterpret_cast<const u32x4 *>(v[2 * x / NV] + at + (x % (NV / 2)) * 1024);
         if (kCodes) {
             const uint32_t g = 4 * (lane >> 4);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                ke[b] = *reinterpret_cast<const uint32_t *>(a.kexp + row[b] + g);
-                ve[b] = *reinterpret_cast<const uint32_t *>(a.vexp + row[b] + g);
+                n.ke[b] = *reinterpret_cast<const uint32_t *>(a.kexp + row[b] + g);
+                n.ve[b] = *reinterpret_cast<const uint32_t *>(a.vexp + row[b] + g);
             }
         }
     }
     // packed tokens of the call: a position past the last token reads the last one and is masked
-    __device__ __forceinline__ void load_packed(const AttnArgs &a, int start, int kvh, int p0, int lane) {
+    static __device__ __forceinline__ void load_packed(Ahead &n, const AttnArgs &a, int start, int kvh, int p0, int lane) {
+        n.here[0] = n.here[1] = true;
 #pragma unroll
         for (int x = 0; x < NK; ++x) {
             const int e = x * 64 + lane, t = e / CK, c = e % CK;
             const int64_t row = min(start + p0 + t, a.T - 1);
-            kr[x] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(
+            n.kr[x] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(
                         static_cast<const TC *>(a.k) + row * a.ks + kvh * K) + 16 * c);
         }
 #pragma unroll
         for (int x = 0; x < NV; ++x) {
             const int e = x * 64 + lane, t = e / CV, c = e % CV;
             const int64_t row = min(start + p0 + t, a.T - 1);
-            vr[x] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(
+            n.vr[x] = *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(
                         static_cast<const TC *>(a.v) + row * a.vs + kvh * V) + 16 * c);
         }
     }
 
-    // Registers to this wave's LDS. `masked`: tokens that nobody may see (here[b] false,
+    // Registers to this wave's LDS. `masked`: tokens that nobody may see (their page is missing,
     // or position >= end) get zero values, and the result says whether any of the others
     // holds an infinity or NaN.
-    __device__ __forceinline__ bool stage(char *lk, char *lv, bool masked, int p0, int end, const bool (&here)[2], int lane) {
+    static __device__ __forceinline__ bool stage(Ahead &n, char *lk, char *lv, bool masked, int p0, int end, int lane) {
         bool odd = false;
         if (masked) {
 #pragma unroll
             for (int x = 0; x < NV; ++x) {
                 const int t = (x * 64 + lane) / CV;
-                if (p0 + t >= end || !(t < 16 ? here[0] : here[1])) vr[x] = (u32x4){0, 0, 0, 0};
+                if (p0 + t >= end || !(t < 16 ? n.here[0] : n.here[1])) n.vr[x] = (u32x4){0, 0, 0, 0};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) odd |= not_finite<TC>(vr[x][j]);
+                for (int j = 0; j < 4; ++j) odd |= not_finite<TC>(n.vr[x][j]);
             }
         }
 #pragma unroll
         for (int x = 0; x < NK; ++x) {
             const int e = x * 64 + lane, t = e / CK, c = e % CK;
-            *reinterpret_cast<u32x4 *>(lk + t * (K * ES) + 16 * (c ^ swz_k(t))) = kr[x];
+            *reinterpret_cast<u32x4 *>(lk + t * (K * ES) + 16 * (c ^ swz_k(t))) = n.kr[x];
         }
 #pragma unroll
         for (int x = 0; x < NV; ++x) {
             const int e = x * 64 + lane, t = e / CV, c = e % CV;
-            *reinterpret_cast<u32x4 *>(lv + t * (V * ES) + 16 * (c ^ swz_v(t))) = vr[x];
+            *reinterpret_cast<u32x4 *>(lv + t * (V * ES) + 16 * (c ^ swz_v(t))) = n.vr[x];
         }
         return masked && __any(odd);
     }
@@ -223,7 +228,7 @@ template <int K, int V, int RT, typename TC> struct Stream {
                 for (int i = 0; i < RT; ++i) s[b][i] = mma16(kf, q[i][ks], s[b][i]);
             }
         }
-        Frag p[RT];
+        Frag p[RT], rest[RT];
         float pf[RT][8];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
@@ -254,56 +259,58 @@ template <int K, int V, int RT, typename TC> struct Stream {
                 if (kCodes) pf[i][j] = scaled_by(pf[i][j], vx[j >> 2], j & 3);
             }
             p[i] = to_frag(pf[i], Frag{});
+            if constexpr (ES != 4) {
+                float r[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r[j] = pf[i][j] - static_cast<float>(p[i][j]);
+                rest[i] = to_frag(r, Frag{});
+            }
         }
         if (!odd) {
 #pragma unroll
             for (int d = 0; d < VT; ++d) {
                 const Frag vf = v_frag(lv, d, lane);
 #pragma unroll
-                for (int i = 0; i < RT; ++i) o[d][i] = mma16(vf, p[i], o[d][i]);
+                for (int i = 0; i < RT; ++i) {
+                    if constexpr (ES != 4) o[d][i] = mma16(vf, rest[i], o[d][i]);
+                    o[d][i] = mma16(vf, p[i], o[d][i]);
+                }
             }
             return;
         }
         // An infinity or NaN among values that some row does not see: a zero weight would
         // not keep it out of a matrix product, so each token is added to the rows that see it.
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
 #pragma unroll 1
-            for (int g = 0; g < 4; ++g) {
-                const int t = 16 * (j >> 2) + 4 * g + (j & 3), src = 16 * g + (lane & 15);
+        for (int t = 0; t < kStepWave; ++t) {
+            const int j = 4 * (t >> 4) + (t & 3), src = 4 * (t & 12) + (lane & 15);  // its register, its lanes
 #pragma unroll
-                for (int i = 0; i < RT; ++i) {
-                    const float w = __shfl(pf[i][j], src);
-                    const uint32_t see = __shfl(sees[i], src);
+            for (int i = 0; i < RT; ++i) {
+                float w = 0.f;
 #pragma unroll
-                    for (int d = 0; d < VT; ++d) {
-                        const f32x4 x = v_row(lv, t, d, lane);
-                        if ((see >> j) & 1u) o[d][i] += x * w;
-                    }
+                for (int x = 0; x < 8; ++x)
+                    if (x == j) w = pf[i][x];
+                w = __shfl(w, src);
+                const bool see = (__shfl(sees[i], src) >> j) & 1u;
+#pragma unroll
+                for (int d = 0; d < VT; ++d) {
+                    const f32x4 x = v_row(lv, t, d, lane);
+                    if (see) o[d][i] += x * w;
                 }
             }
         }
     }
 
-    // Which tokens the lane's rows see in a masked step: positions before `ctx`, and new
-    // token b = position - ctx if bit b of the row's mask is set or, without a mask, b <= own.
-    // Positions from `end` on, and pages that are not there, are seen by none.
+    // Which tokens the lane's rows see in a masked step (seen_tokens)
     __device__ __forceinline__ void visible(uint32_t (&sees)[RT], const AttnArgs &a, int start, int r0, int rows, int p0,
                                             int ctx, int end, const bool (&here)[2], int lane) const {
-        const int g = lane >> 4;
+        const int g = 4 * (lane >> 4);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             const int tok = (r0 + min(16 * i + (lane & 15), rows - 1)) / a.G;
             const uint64_t bits = a.mask ? a.mask[start + tok] : 0;
-            uint32_t v = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int pos = p0 + 16 * (j >> 2) + 4 * g + (j & 3), b = pos - ctx;
-                bool see = b < 0 || (a.mask ? b < 64 && ((bits >> (b & 63)) & 1u) : b <= tok);
-                see = see && pos < end && here[j >> 2];
-                v |= static_cast<uint32_t>(see) << j;
-            }
-            sees[i] = v;
+            const uint32_t w = static_cast<uint32_t>(
+                seen_tokens(a.mask != nullptr, bits, p0, ctx, ctx + tok, end, (here[0] ? 1 : 0) | (here[1] ? 2 : 0)));
+            sees[i] = ((w >> g) & 15u) | ((w >> (16 + g)) & 15u) << 4;
         }
     }
 

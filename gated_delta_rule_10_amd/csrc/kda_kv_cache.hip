@@ -17,13 +17,29 @@ namespace kda {
 namespace {
 
 // Where new token t of the call lies: the row of its kv head h in [pages, Hk, page], kNowhere if
-// it has no place, kOutside if it is in no sequence.
+// it has no place, kOutside if it is in no sequence. Every lane of a wave calls it, with tokens
+// that do not fall from lane to lane, `t0` the first one's. The sequences from t0's on are read
+// by one load, a lane each; only a token behind 64 of them is searched for in memory.
 constexpr int64_t kNowhere = -1, kOutside = -2;
-__device__ __forceinline__ int64_t place_of(const KvArgs &a, int t, int h) {
-    const int n = seq_of_token(a.cu, a.N, t);
-    const int start = clampi(a.cu[n], 0, a.T), end = clampi(a.cu[n + 1], start, a.T);
+__device__ __forceinline__ int64_t place_of(const KvArgs &a, int t0, int t, int h, int lane) {
+    const int n0 = wave_last_upto(a.N, t0, lane, [&](int n) { return static_cast<int64_t>(a.cu[n]); });
+    const int m = min(n0 + lane, a.N - 1);
+    const int wstart = a.cu[m], wend = a.cu[m + 1], wlen = a.lens[m];
+    int n = 0;  // of the window: the last whose start is not above t
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) n += __shfl(wstart, n + d) <= t && n0 + n + d < a.N ? d : 0;
+    int start = __shfl(wstart, n), end = __shfl(wend, n), len = __shfl(wlen, n);
+    n += n0;
+    if (n - n0 == 63 && t >= end) {
+        n = seq_of_token(a.cu, a.N, t);
+        start = a.cu[n];
+        end = a.cu[n + 1];
+        len = a.lens[n];
+    }
+    start = clampi(start, 0, a.T);
+    end = clampi(end, start, a.T);
     if (t < start || t >= end) return kOutside;
-    const int64_t pos = static_cast<int64_t>(a.lens[n]) - (end - t);
+    const int64_t pos = static_cast<int64_t>(len) - (end - t);
     if (pos < 0 || (pos >> a.page_shift) >= a.max_pages) return kNowhere;
     const int id = a.table[static_cast<int64_t>(n) * a.max_pages + (pos >> a.page_shift)];
     if (id < 0 || id >= a.num_pages) return kNowhere;
@@ -128,9 +144,9 @@ __global__ __launch_bounds__(kThreads) void kv_kernel(KvArgs a) {
             if (r < rows) v[i] = *reinterpret_cast<const Eight<T> *>(static_cast<const T *>(a.v) + at(r, a.vs, V) + 8 * (tid % LV));
         }
     }
-    if (tid < rows) {
-        const int x = h0 + tid, t = x / a.Hk;
-        place[tid] = place_of(a, t0 + t, x - t * a.Hk);
+    if (tid < kRows) {  // the first wave
+        const int x = h0 + min(tid, rows - 1), t = x / a.Hk;
+        place[tid] = place_of(a, t0, t0 + t, x - t * a.Hk, tid);
     }
     __syncthreads();
 #pragma unroll
