@@ -17,7 +17,8 @@ def __getattr__(name):
     # the bindings import torch; load them only when one of their names is used
     if name in _ATTN:
         from . import attn
-        return getattr(attn, name)
+        globals()[name] = f = getattr(attn, name)
+        return f
     if name in __all__:
         from . import kda
         return getattr(kda, name)

@@ -70,43 +70,48 @@ def _rows(t: torch.Tensor, name: str) -> int:
     return st if T > 1 else h * d
 
 
+def _dense(device, **tensors) -> None:
+    """Every tensor given (None skipped) contiguous and on `device`, a GPU: the call runs there."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device != device or not t.is_contiguous():
+            _dev(t, name)
+            _one_device(device, t)
+
+
 def _offsets(cu_seqlens: torch.Tensor) -> int:
     """N of a cu_seqlens tensor."""
-    _dev(cu_seqlens, "cu_seqlens")
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
         raise ValueError("cu_seqlens must be int32 [N + 1]")
     return cu_seqlens.shape[0] - 1
 
 
-def _cache(N: int, cache_lens, page_table, k_cache, v_cache, k_exp, v_exp) -> KdaKvCache:
+def _cache(device, N: int, cache_lens, page_table, k_cache, v_cache, k_exp, v_exp) -> KdaKvCache:
     """The call's cache, after checking its tensors against each other."""
-    _dev(cache_lens, "cache_lens")
-    _dev(page_table, "page_table")
-    _dev(k_cache, "k_cache")
-    _dev(v_cache, "v_cache")
+    _dense(device, cache_lens=cache_lens, page_table=page_table, k_cache=k_cache, v_cache=v_cache, k_exp=k_exp, v_exp=v_exp)
     if cache_lens.dtype != torch.int32 or cache_lens.shape != (N,):
         raise ValueError("cache_lens must be int32 [N]")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != N:
+    rows = page_table.shape
+    if page_table.dtype != torch.int32 or len(rows) != 2 or rows[0] != N:
         raise ValueError("page_table must be int32 [N, max_pages]")
-    kind = k_cache.dtype
-    if k_cache.dim() != 4 or v_cache.dim() != 4 or k_cache.shape[:3] != v_cache.shape[:3] or v_cache.dtype != kind:
+    kind, shape, vshape = k_cache.dtype, k_cache.shape, v_cache.shape
+    if len(shape) != 4 or len(vshape) != 4 or shape[:3] != vshape[:3] or v_cache.dtype != kind:
         raise ValueError("k_cache and v_cache must be [num_pages, Hk, page_size, d] of one dtype")
     code = _KV_CODES.get(kind)
     if code is None:
         raise TypeError(f"unsupported cache dtype {kind}")
     ke = ve = None
     if code == KDA_KV_E4M3:
-        for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
-            if t is None:
-                raise ValueError(f"an e4m3 cache needs {name}")
-            _dev(t, name)
-            if t.dtype != torch.uint8 or t.shape != k_cache.shape[:3]:
-                raise ValueError(f"{name} must be uint8 [num_pages, Hk, page_size]")
+        if k_exp is None or v_exp is None:
+            raise ValueError("an e4m3 cache needs k_exp and v_exp")
+        if k_exp.dtype != torch.uint8 or v_exp.dtype != torch.uint8 or not k_exp.shape == v_exp.shape == shape[:3]:
+            raise ValueError("k_exp and v_exp must be uint8 [num_pages, Hk, page_size]")
         ke, ve = k_exp.data_ptr(), v_exp.data_ptr()
     elif k_exp is not None or v_exp is not None:
         raise ValueError("k_exp and v_exp are for e4m3 caches")
     return KdaKvCache(k_cache.data_ptr(), v_cache.data_ptr(), ke, ve, page_table.data_ptr(), cache_lens.data_ptr(),
-                      k_cache.shape[0], k_cache.shape[2], page_table.shape[1], code)
+                      shape[0], shape[2], rows[1], code)
 
 
 class _Here:
@@ -161,7 +166,8 @@ def kda_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: 
         s = _handle(stream, device)
         with _alloc_on(stream):
             o = _out(o, (T, H, d_v), out_dtype, device)
-        _one_device(device, k, v, cu_seqlens, o)
+        _dense(device, cu_seqlens=cu_seqlens, o=o)
+        _one_device(device, k, v)
         st = lib.kda_attn_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), N, T, H, Hk, d_k, d_v,
                               sq, sk, sv, _code(q.dtype), _code(out_dtype),
                               d_k ** -0.5 if scale is None else float(scale), o.data_ptr(), s)
@@ -187,13 +193,15 @@ def kda_kv_write(k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, cac
     d_v = v.shape[2]
     if v.shape[:2] != (T, Hk) or k.dtype != v.dtype:
         raise ValueError("inconsistent k/v shapes or dtypes")
-    cache = _cache(N, cache_lens, page_table, k_cache, v_cache, k_exp, v_exp)
+    device = k.device
+    _dense(device, cu_seqlens=cu_seqlens)
+    _one_device(device, v)
+    cache = _cache(device, N, cache_lens, page_table, k_cache, v_cache, k_exp, v_exp)
     if k_cache.shape[1] != Hk or k_cache.shape[3] != d_k or v_cache.shape[3] != d_v:
         raise ValueError("k_cache and v_cache must have the heads and channels of k and v")
-    _one_device(k.device, v, cu_seqlens, cache_lens, page_table, k_cache, v_cache, k_exp, v_exp)
-    with _on(k.device):
+    with _on(device):
         st = lib.kda_kv_write(k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), N, T, Hk, d_k, d_v, sk, sv,
-                              _code(k.dtype), ctypes.byref(cache), _handle(stream, k.device))
+                              _code(k.dtype), ctypes.byref(cache), _handle(stream, device))
     if st != KDA_OK:
         raise KDAError(st, "kda_kv_write")
 
@@ -209,15 +217,16 @@ def kda_kv_read(T: int, cu_seqlens: torch.Tensor, cache_lens: torch.Tensor, page
     """
     lib = load_library()
     N = _offsets(cu_seqlens)
-    cache = _cache(N, cache_lens, page_table, k_cache, v_cache, k_exp, v_exp)
-    Hk, d_k, d_v = k_cache.shape[1], k_cache.shape[3], v_cache.shape[3]
     device = k_cache.device
+    _dense(device, cu_seqlens=cu_seqlens)
+    cache = _cache(device, N, cache_lens, page_table, k_cache, v_cache, k_exp, v_exp)
+    Hk, d_k, d_v = k_cache.shape[1], k_cache.shape[3], v_cache.shape[3]
     with _on(device):
         s = _handle(stream, device)
         with _alloc_on(stream):
             k = _out(k, (T, Hk, d_k), out_dtype, device)
             v = _out(v, (T, Hk, d_v), out_dtype, device)
-        _one_device(device, cu_seqlens, cache_lens, page_table, v_cache, k_exp, v_exp, k, v)
+        _dense(device, k=k, v=v)
         st = lib.kda_kv_read(k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), N, T, Hk, d_k, d_v, _code(out_dtype),
                              ctypes.byref(cache), s)
     if st != KDA_OK:
@@ -248,16 +257,15 @@ def kda_attn_cache_fwd(q: torch.Tensor, cu_seqlens: torch.Tensor, cache_lens: to
     sq = _rows(q, "q")
     N = _offsets(cu_seqlens)
     T, H, d_k = q.shape
-    cache = _cache(N, cache_lens, page_table, k_cache, v_cache, k_exp, v_exp)
+    device = q.device
+    _dense(device, cu_seqlens=cu_seqlens, tree_mask=tree_mask)
+    cache = _cache(device, N, cache_lens, page_table, k_cache, v_cache, k_exp, v_exp)
     Hk, d_v = k_cache.shape[1], v_cache.shape[3]
     if k_cache.shape[3] != d_k:
         raise ValueError("q and k_cache must have the same channels")
-    if tree_mask is not None:
-        _dev(tree_mask, "tree_mask")
-        if tree_mask.dtype != torch.int64 or tuple(tree_mask.shape) != (T,):
-            raise ValueError("tree_mask must be int64 [T]")
+    if tree_mask is not None and (tree_mask.dtype != torch.int64 or tree_mask.shape != (T,)):
+        raise ValueError("tree_mask must be int64 [T]")
     out_dtype = q.dtype if out_dtype is None else out_dtype
-    device = q.device
     with _on(device):
         s = _handle(stream, device)
         with _alloc_on(stream):
@@ -265,8 +273,7 @@ def kda_attn_cache_fwd(q: torch.Tensor, cu_seqlens: torch.Tensor, cache_lens: to
             if workspace is None:
                 need = int(lib.kda_attn_cache_fwd_workspace_size(N, T, H, Hk, d_k, d_v, _code(q.dtype)))
                 workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        _dev(workspace, "workspace")
-        _one_device(device, cu_seqlens, cache_lens, page_table, k_cache, v_cache, k_exp, v_exp, tree_mask, o, workspace)
+        _dense(device, o=o, workspace=workspace)
         st = lib.kda_attn_cache_fwd(q.data_ptr(), cu_seqlens.data_ptr(), N, T, H, Hk, d_k, d_v, sq, _code(q.dtype),
                                     _code(out_dtype), d_k ** -0.5 if scale is None else float(scale),
                                     ctypes.byref(cache), _ptr(tree_mask), o.data_ptr(), workspace.data_ptr(),

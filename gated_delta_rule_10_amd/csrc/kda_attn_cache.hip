@@ -295,7 +295,7 @@ constexpr int kWhole = 4 * kStep;
 // Joins the pieces of the (sequence, kv head, row tile)s that the line was cut inside: a
 // workgroup takes up to 16 rows of one. Groups of V / 4 lanes take a row each; where there are
 // more groups than rows, several share a row's pieces and are added in the end.
-constexpr int kJoinThreads = 256, kJoinRows = 16;
+constexpr int kJoinThreads = 512, kJoinRows = 16;
 template <int V, int R, int STEP>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
     constexpr int LPR = V / 4, GR = kJoinThreads / LPR;  // lanes of a row, groups

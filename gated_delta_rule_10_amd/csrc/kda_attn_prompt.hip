@@ -99,12 +99,14 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     const int kvh = blockIdx.x % a.Hk;
-    const int64_t slot = slots - 1 - static_cast<int>(blockIdx.x / a.Hk);  // the longest first
+    // The longest first, sequence by sequence: the tiles at work at a time then share their keys and
+    // values in L2 (taking the longest tiles of all sequences first was slower: 421 against 400 us
+    // for 16 prompts of 200 to 4000 tokens).
+    const int64_t slot = slots - 1 - static_cast<int>(blockIdx.x / a.Hk);
     const int n = seq_of_slot(a.cu, a.N, a.T, a.G, R, slot, lane);
     int start, count;
     seq_rows(a.cu, n, a.T, start, count);
-    const int64_t first = (slot - static_cast<int64_t>(start) * a.G / R - n) * R;
-    const int64_t all = static_cast<int64_t>(count) * a.G;
+    const int64_t first = (slot - static_cast<int64_t>(start) * a.G / R - n) * R, all = static_cast<int64_t>(count) * a.G;
     if (first < 0 || first >= all) return;
     const int last = static_cast<int>((min(first + R, all) - 1) / a.G);  // last token of the tile
 
