@@ -19,9 +19,6 @@
 // joins them in the order of the line, so results do not depend on timing.
 #include "kda_attn_stream.h"
 
-#ifndef KDA_PER
-#define KDA_PER 2
-#endif
 namespace kda {
 namespace {
 
@@ -193,10 +190,10 @@ struct Pages {
 };
 
 // workgroups to a compute unit, as registers and LDS allow
-template <typename TC> constexpr int kPerCu = sizeof(TC) == 4 ? 1 : sizeof(TC) == 2 ? 2 : KDA_PER;
+constexpr int kPerCu = 2;
 
 template <int K, int V, int RT, typename TC>
-__global__ __launch_bounds__(64 * kWaves, kPerCu<TC>) void attn_cache_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * kWaves, kPerCu) void attn_cache_kernel(AttnArgs a) {
     using S = Stream<K, V, RT, TC>;
     constexpr int R = S::R;
     __shared__ __align__(16) char lds[S::kLds];
@@ -204,7 +201,7 @@ __global__ __launch_bounds__(64 * kWaves, kPerCu<TC>) void attn_cache_kernel(Att
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     char *lk = lds + w * (S::KB + S::VB), *lv = lk + S::KB;
 
-    Line<R, kStep> line;
+    Line<R, S::kStep> line;
     line.scan(a, lane, blockIdx.x == 0 && w == 0 && !a.whole ? static_cast<int64_t *>(a.ws) : nullptr);
     const int64_t U = line.total;
     if (U == 0) return;
@@ -235,15 +232,15 @@ __global__ __launch_bounds__(64 * kWaves, kPerCu<TC>) void attn_cache_kernel(Att
         st.reset();
         st.load_q(a, q.start, kvh, r0, rows, lane);
         Pages pages;
-        pages.begin(a, n, t0 * kStep, lane);
+        pages.begin(a, n, t0 * S::kStep, lane);
         // this wave's steps: those with a token that some row sees
-        const int te = min(t1, (last - w * kStepWave + kStep - 1) / kStep);
+        const int te = min(t1, (last - w * S::kStepWave + S::kStep - 1) / S::kStep);
         auto load = [&](int t, typename S::Ahead &n) {
-            pages.reach(a, t * kStep, lane);
-            int64_t row[2];
+            pages.reach(a, t * S::kStep, lane);
+            int64_t row[S::NB];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const int pos = t * kStep + w * kStepWave + 16 * b;
+            for (int b = 0; b < S::NB; ++b) {
+                const int pos = t * S::kStep + w * S::kStepWave + 16 * b;
                 row[b] = pages.row(a, kvh, pos);
                 n.here[b] = pages.exists(a, pos);
             }
@@ -251,9 +248,14 @@ __global__ __launch_bounds__(64 * kWaves, kPerCu<TC>) void attn_cache_kernel(Att
         };
         // Loads past the last step read that step again, so that every step has as many behind it.
         auto step = [&](int t, typename S::Ahead &n) {
-            const int p0 = t * kStep + w * kStepWave;
-            const bool masked = p0 + kStepWave > open || !n.here[0] || !n.here[1];
-            const uint32_t kx[2] = {n.ke[0], n.ke[1]}, vx[2] = {n.ve[0], n.ve[1]};
+            const int p0 = t * S::kStep + w * S::kStepWave;
+            const bool masked = p0 + S::kStepWave > open || !n.here[0] || !n.here[S::NB - 1];
+            uint32_t kx[S::NB], vx[S::NB];  // this step's: the next one's are about to be loaded
+#pragma unroll
+            for (int b = 0; b < S::NB; ++b) {
+                kx[b] = n.ke[b];
+                vx[b] = n.ve[b];
+            }
             uint32_t sees[RT];
             if (masked) st.visible(sees, a, q.start, r0, rows, p0, q.ctx, q.end, n.here, lane);
             const bool odd = S::stage(n, lk, lv, masked, p0, q.end, lane);
@@ -290,7 +292,7 @@ __global__ __launch_bounds__(64 * kWaves, kPerCu<TC>) void attn_cache_kernel(Att
 // Up to this many tokens a (sequence, kv head, row tile) is one unit of the line, and there is
 // nothing to join: one step more or less costs about a microsecond, joining about five (its
 // launch and its reads).
-constexpr int kWhole = 4 * kStep;
+constexpr int kWhole = 512;
 
 // Joins the pieces of the (sequence, kv head, row tile)s that the line was cut inside: a
 // workgroup takes up to 16 rows of one. Groups of V / 4 lanes take a row each; where there are
@@ -542,12 +544,9 @@ __global__ __launch_bounds__(256, 2) void attn_cache_rows_kernel(AttnArgs a) {
     }
 }
 
-// Rows of a tile: 16 where the mean rows of a (sequence, kv head) fit them, else 128
-// (32 for fp32).
-int tile_rows(int64_t T, int64_t N, int64_t G, bool f32) {
-    const int64_t rows = (T + N - 1) / N * G;
-    return rows <= 16 ? 16 : f32 ? 32 : 128;
-}
+// Rows of a tile: 16 where the mean rows of a (sequence, kv head) fit them, else 128. fp32 is
+// bound by its products from 16 rows on, so larger tiles would save nothing.
+int tile_rows(int64_t T, int64_t N, int64_t G, bool f32) { return f32 || (T + N - 1) / N * G <= 16 ? 16 : 128; }
 
 template <int V, int R, int STEP> hipError_t launch_join(const AttnArgs &a, hipStream_t st) {
     const hipError_t e = hipGetLastError();
@@ -557,9 +556,9 @@ template <int V, int R, int STEP> hipError_t launch_join(const AttnArgs &a, hipS
                        dim3(kJoinThreads), 0, st, a);
     return hipGetLastError();
 }
-template <int K, int V, int RT, typename TC> hipError_t launch_stream(const AttnArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL((attn_cache_kernel<K, V, RT, TC>), dim3(a.W), dim3(64 * kWaves), 0, st, a);
-    return launch_join<V, 16 * RT, kStep>(a, st);
+template <int K, int V, typename TC> hipError_t launch_stream(const AttnArgs &a, hipStream_t st) {
+    hipLaunchKernelGGL((attn_cache_kernel<K, V, 1, TC>), dim3(a.W), dim3(64 * kWaves), 0, st, a);
+    return launch_join<V, 16, Stream<K, V, 1, TC>::kStep>(a, st);
 }
 template <int K, int V, typename TC> hipError_t launch_rows(const AttnArgs &a, hipStream_t st) {
     hipLaunchKernelGGL((attn_cache_rows_kernel<K, V, TC>), dim3(a.W), dim3(256), 0, st, a);
@@ -568,14 +567,14 @@ template <int K, int V, typename TC> hipError_t launch_rows(const AttnArgs &a, h
 
 template <int K, int V> hipError_t launch_dims(const AttnArgs &a, hipStream_t st) {
     const bool one = tile_rows(a.T, a.N, a.G, a.in_dtype == KDA_F32) == 16;
-    if (a.kv_dtype == KDA_KV_F32) return one ? launch_stream<K, V, 1, float>(a, st) : launch_stream<K, V, 2, float>(a, st);
-    if (a.kv_dtype == KDA_KV_BF16) return one ? launch_stream<K, V, 1, bf16_t>(a, st) : launch_rows<K, V, bf16_t>(a, st);
-    return one ? launch_stream<K, V, 1, e4m3_t>(a, st) : launch_rows<K, V, e4m3_t>(a, st);
+    if (a.kv_dtype == KDA_KV_F32) return launch_stream<K, V, float>(a, st);
+    if (a.kv_dtype == KDA_KV_BF16) return one ? launch_stream<K, V, bf16_t>(a, st) : launch_rows<K, V, bf16_t>(a, st);
+    return one ? launch_stream<K, V, e4m3_t>(a, st) : launch_rows<K, V, e4m3_t>(a, st);
 }
 
 }  // namespace
 
-int32_t attn_cache_workgroups() { return KDA_PER * compute_units(); }
+int32_t attn_cache_workgroups() { return kPerCu * compute_units(); }
 
 size_t attn_cache_workspace(int32_t N, int32_t T, int32_t H, int32_t Hk, int32_t V, kda_dtype_t in_dtype) {
     const int R = tile_rows(T, N, H / Hk, in_dtype == KDA_F32);

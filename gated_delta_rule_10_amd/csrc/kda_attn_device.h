@@ -47,6 +47,12 @@ __device__ __forceinline__ f32x8 load_frag(const float *p) {
     return (f32x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
 }
 
+__device__ __forceinline__ f32x4 mma16(f32x4 a, f32x4 b, f32x4 c) {  // 16 products, fp32
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+    return c;
+}
+
 // two fp32 to bf16, nearest even (the gfx950 conversion keeps NaN)
 __device__ __forceinline__ bf16x2 pack_bf16(float x, float y) {
     typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -56,9 +62,7 @@ __device__ __forceinline__ bf16x8 to_frag(const float *x, bf16x8) {
     const bf16x2 a = pack_bf16(x[0], x[1]), b = pack_bf16(x[2], x[3]), c = pack_bf16(x[4], x[5]), d = pack_bf16(x[6], x[7]);
     return (bf16x8){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
-__device__ __forceinline__ f32x8 to_frag(const float *x, f32x8) {
-    return (f32x8){x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
-}
+__device__ __forceinline__ f32x4 to_frag(const float *x, f32x4) { return (f32x4){x[0], x[1], x[2], x[3]}; }
 
 // eight e4m3 codes times a power of two as bf16, exactly
 __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t lo, uint32_t hi, float scale) {

@@ -7,7 +7,7 @@
 // key and value read serves all of them.
 //
 // Work of a workgroup: four waves; a step gives each wave 32 consecutive
-// tokens. Each wave keeps its own m, sum and output over its tokens (no barrier
+// tokens (fp32: 16, so that two workgroups fit a compute unit's LDS). Each wave keeps its own m, sum and output over its tokens (no barrier
 // while streaming) and the four are joined at the end. A wave holds the next
 // step's keys and values in registers while it works on the current ones, which
 // lie in its own part of LDS.
@@ -20,13 +20,13 @@
 // LDS reads give without any movement of P.
 #pragma once
 
+#include <type_traits>
+
 #include "kda_attn_rows.h"
 
 namespace kda {
 
 constexpr int kWaves = 4;
-constexpr int kStepWave = 32;                  // tokens per wave and step
-constexpr int kStep = kWaves * kStepWave;      // tokens per workgroup and step
 
 template <int K, int V, int RT, typename TC> struct Stream {
     using Frag = typename mma_of<TC>::frag;
@@ -34,6 +34,11 @@ template <int K, int V, int RT, typename TC> struct Stream {
     static constexpr int R = 16 * RT;
     static constexpr int ES = sizeof(TC);
     static constexpr bool kCodes = sizeof(TC) == 1;
+    static constexpr int NB = ES == 4 ? 1 : 2;             // groups of 16 tokens per wave and step
+    static constexpr int kStepWave = 16 * NB;              // tokens per wave and step
+    static constexpr int kStep = kWaves * kStepWave;       // tokens per workgroup and step
+    static constexpr int NT = 4 * NB;                      // of them, tokens in a lane's registers
+    using PFrag = typename std::conditional<ES == 4, f32x4, bf16x8>::type;  // weights, values: NT tokens
     static constexpr int CK = K * ES / 16, CV = V * ES / 16;  // 16-byte chunks per row
     static constexpr int NK = kStepWave * CK / 64, NV = kStepWave * CV / 64;  // chunks per lane and step
     static constexpr int KT = K / 32, VT = V / 16;
@@ -58,8 +63,8 @@ template <int K, int V, int RT, typename TC> struct Stream {
     // keys, values and exponents on their way, of the next step
     struct Ahead {
         u32x4 kr[NK], vr[NV];
-        uint32_t ke[2], ve[2];
-        bool here[2];  // whether the pages of the two groups of 16 tokens exist
+        uint32_t ke[NB], ve[NB];
+        bool here[NB];  // whether the pages of the groups of 16 tokens exist
     } next;
 
     __device__ __forceinline__ void reset() {
@@ -89,24 +94,24 @@ template <int K, int V, int RT, typename TC> struct Stream {
     // ---- sources: chunk x of a wave's 32 tokens
     // cache: row[b] is the cache row of the first of tokens 16 b .. 16 b + 15 (a page ends at a multiple of
     // 16, so the 16 rows lie behind one another)
-    static __device__ __forceinline__ void load_cache(Ahead &n, const AttnArgs &a, const int64_t (&row)[2], int lane) {
-        const char *k[2], *v[2];
+    static __device__ __forceinline__ void load_cache(Ahead &n, const AttnArgs &a, const int64_t (&row)[NB], int lane) {
+        const char *k[NB], *v[NB];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < NB; ++b) {
             k[b] = static_cast<const char *>(a.k) + row[b] * (K * ES);
             v[b] = static_cast<const char *>(a.v) + row[b] * (V * ES);
         }
         const uint32_t at = 16 * lane;
 #pragma unroll
         for (int x = 0; x < NK; ++x)
-            n.kr[x] = *reinterpret_cast<const u32x4 *>(k[2 * x / NK] + at + (x % (NK / 2)) * 1024);
+            n.kr[x] = *reinterpret_cast<const u32x4 *>(k[NB * x / NK] + at + (x % (NK / NB)) * 1024);
 #pragma unroll
         for (int x = 0; x < NV; ++x)
-            n.vr[x] = *reinterpret_cast<const u32x4 *>(v[2 * x / NV] + at + (x % (NV / 2)) * 1024);
+            n.vr[x] = *reinterpret_cast<const u32x4 *>(v[NB * x / NV] + at + (x % (NV / NB)) * 1024);
         if (kCodes) {
             const uint32_t g = 4 * (lane >> 4);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < NB; ++b) {
                 n.ke[b] = *reinterpret_cast<const uint32_t *>(a.kexp + row[b] + g);
                 n.ve[b] = *reinterpret_cast<const uint32_t *>(a.vexp + row[b] + g);
             }
@@ -114,7 +119,8 @@ template <int K, int V, int RT, typename TC> struct Stream {
     }
     // packed tokens of the call: a position past the last token reads the last one and is masked
     static __device__ __forceinline__ void load_packed(Ahead &n, const AttnArgs &a, int start, int kvh, int p0, int lane) {
-        n.here[0] = n.here[1] = true;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) n.here[b] = true;
 #pragma unroll
         for (int x = 0; x < NK; ++x) {
             const int e = x * 64 + lane, t = e / CK, c = e % CK;
@@ -140,7 +146,7 @@ template <int K, int V, int RT, typename TC> struct Stream {
 #pragma unroll
             for (int x = 0; x < NV; ++x) {
                 const int t = (x * 64 + lane) / CV;
-                if (p0 + t >= end || !(t < 16 ? n.here[0] : n.here[1])) n.vr[x] = (u32x4){0, 0, 0, 0};
+                if (p0 + t >= end || !n.here[NB == 1 || t < 16 ? 0 : NB - 1]) n.vr[x] = (u32x4){0, 0, 0, 0};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) odd |= not_finite<TC>(n.vr[x][j]);
             }
@@ -172,8 +178,8 @@ template <int K, int V, int RT, typename TC> struct Stream {
             return (f32x8){x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
         }
     }
-    // V^T: channel 16 d + l % 16, tokens 4 g + 0..3 and 16 + 4 g + 0..3
-    __device__ __forceinline__ Frag v_frag(const char *lv, int d, int lane) const {
+    // V^T: channel 16 d + l % 16, tokens 4 g + 0..3 and (bf16 products) 16 + 4 g + 0..3
+    __device__ __forceinline__ PFrag v_frag(const char *lv, int d, int lane) const {
         const int i = lane & 15, g = lane >> 4;
         if constexpr (ES == 2) {
             typedef __attribute__((address_space(3))) i16x4 lds4;
@@ -190,10 +196,10 @@ template <int K, int V, int RT, typename TC> struct Stream {
             const i32x2 w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds2 *)p);
             return codes_to_bf16(w[0], w[1], 1.f);
         } else {
-            f32x8 x;
+            f32x4 x;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int t = (j & 3) + 4 * g + (j >> 2) * 16, ch = 16 * d + i;
+            for (int j = 0; j < 4; ++j) {
+                const int t = j + 4 * g, ch = 16 * d + i;
                 x[j] = *reinterpret_cast<const float *>(lv + t * (V * 4) + 16 * ((ch >> 2) ^ swz_v(t)) + 4 * (ch & 3));
             }
             return x;
@@ -215,10 +221,10 @@ template <int K, int V, int RT, typename TC> struct Stream {
     // One step over the 32 staged tokens. sees[i] bit (4 b + j): row l % 16 of block i sees
     // token 16 b + 4 g + j (read only when masked). e: exponents of these tokens.
     __device__ __forceinline__ void step(const char *lk, const char *lv, float c, bool masked, const uint32_t (&sees)[RT],
-                                         bool odd, const uint32_t (&kx)[2], const uint32_t (&vx)[2], int lane) {
-        f32x4 s[2][RT];
+                                         bool odd, const uint32_t (&kx)[NB], const uint32_t (&vx)[NB], int lane) {
+        f32x4 s[NB][RT];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < NB; ++b) {
 #pragma unroll
             for (int i = 0; i < RT; ++i) s[b][i] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -228,18 +234,20 @@ template <int K, int V, int RT, typename TC> struct Stream {
                 for (int i = 0; i < RT; ++i) s[b][i] = mma16(kf, q[i][ks], s[b][i]);
             }
         }
-        Frag p[RT], rest[RT];
-        float pf[RT][8];
+        PFrag p[RT], rest[RT];
+        float pf[RT][NT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-            float x[8];
+            float x[NT];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < NT; ++j) {
                 x[j] = s[j >> 2][i][j & 3] * c;
                 if (kCodes) x[j] = scaled_by(x[j], kx[j >> 2], j & 3);
                 if (masked) x[j] = (sees[i] >> j) & 1u ? x[j] : -INFINITY;
             }
-            float t = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+            float t = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+#pragma unroll
+            for (int j = 4; j < NT; j += 4) t = fmaxf(t, fmaxf(fmaxf(x[j], x[j + 1]), fmaxf(x[j + 2], x[j + 3])));
             t = swap32_max(swap16_max(t));
             // The reference m only has to keep 2^(s - m) in range, so it moves when the
             // step's maximum passes it by more than 2^8, not at every step.
@@ -253,23 +261,23 @@ template <int K, int V, int RT, typename TC> struct Stream {
             }
             const float ref = m[i] == -INFINITY ? 0.f : m[i];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < NT; ++j) {
                 pf[i][j] = __builtin_amdgcn_exp2f(x[j] - ref);
                 l[i] += pf[i][j];
                 if (kCodes) pf[i][j] = scaled_by(pf[i][j], vx[j >> 2], j & 3);
             }
-            p[i] = to_frag(pf[i], Frag{});
+            p[i] = to_frag(pf[i], PFrag{});
             if constexpr (ES != 4) {
                 float r[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) r[j] = pf[i][j] - static_cast<float>(p[i][j]);
-                rest[i] = to_frag(r, Frag{});
+                rest[i] = to_frag(r, PFrag{});
             }
         }
         if (!odd) {
 #pragma unroll
             for (int d = 0; d < VT; ++d) {
-                const Frag vf = v_frag(lv, d, lane);
+                const PFrag vf = v_frag(lv, d, lane);
 #pragma unroll
                 for (int i = 0; i < RT; ++i) {
                     if constexpr (ES != 4) o[d][i] = mma16(vf, rest[i], o[d][i]);
@@ -287,7 +295,7 @@ template <int K, int V, int RT, typename TC> struct Stream {
             for (int i = 0; i < RT; ++i) {
                 float w = 0.f;
 #pragma unroll
-                for (int x = 0; x < 8; ++x)
+                for (int x = 0; x < NT; ++x)
                     if (x == j) w = pf[i][x];
                 w = __shfl(w, src);
                 const bool see = (__shfl(sees[i], src) >> j) & 1u;
@@ -302,15 +310,16 @@ template <int K, int V, int RT, typename TC> struct Stream {
 
     // Which tokens the lane's rows see in a masked step (seen_tokens)
     __device__ __forceinline__ void visible(uint32_t (&sees)[RT], const AttnArgs &a, int start, int r0, int rows, int p0,
-                                            int ctx, int end, const bool (&here)[2], int lane) const {
+                                            int ctx, int end, const bool (&here)[NB], int lane) const {
         const int g = 4 * (lane >> 4);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             const int tok = (r0 + min(16 * i + (lane & 15), rows - 1)) / a.G;
             const uint64_t bits = a.mask ? a.mask[start + tok] : 0;
             const uint32_t w = static_cast<uint32_t>(
-                seen_tokens(a.mask != nullptr, bits, p0, ctx, ctx + tok, end, (here[0] ? 1 : 0) | (here[1] ? 2 : 0)));
-            sees[i] = ((w >> g) & 15u) | ((w >> (16 + g)) & 15u) << 4;
+                seen_tokens(a.mask != nullptr, bits, p0, ctx, ctx + tok, end, (here[0] ? 1 : 0) | (here[NB - 1] ? 2 : 0)));
+            sees[i] = (w >> g) & 15u;
+            if (NB == 2) sees[i] |= ((w >> (16 + g)) & 15u) << 4;
         }
     }
 
