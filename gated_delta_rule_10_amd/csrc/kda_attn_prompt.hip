@@ -135,7 +135,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
     // The two waves of a SIMD take turns: one is in its products (the values of the tile before,
     // the scores of this one) while the other is in its softmax, and every barrier swaps them.
     // Copies for a tile are issued two turns before its first use, which is when the last reader
-    // of that buffer has gone. The first J tiles are seen whole by every row of the workgroup.
+    // of that buffer has gone; those of tile 0's values and tile 1's keys at the start. The first
+    // J tiles are seen whole by every row of the workgroup.
     const int J = (static_cast<int>(first / a.G) + 1) / kTile, tiles = last / kTile + 1;
     const bool ahead = w < NW / 2;
     auto copy_k = [&](int j) { if (j < tiles) kc.tile(base + lk(j), w, lane); };
@@ -147,19 +148,20 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
     auto sees = [&](int j) { return some && j * kTile <= tok1; };  // the wave has work in tile j
     copy_k(0);
     st.load_q(static_cast<const bf16_t *>(a.q) + static_cast<int64_t>(start + own) * a.qs + h * K, a.c < 0.f, lane);
-    swap(true);
-    if (!ahead) {
-        copy_k(1);
-        copy_v(0);
-        swap(false);
-    }
+    copy_v(0);
+    copy_k(1);
+    // tile 0's keys; a call of one tile has no copies of tile 1 behind them
+    if (tiles > 1) wait_copies<Copier<P, V, false, NW>::N + Copier<P, K, true, NW>::N>();
+    else wait_copies<Copier<P, V, false, NW>::N>();
+    phase_barrier();
+    if (!ahead) swap(false);
     // The wave in its products issues first where they are the longer turn (two heads of 64
     // channels have half the products for the same softmax): 7.27 against 7.41 ms for 32768
     // tokens at 128 channels, and 191 against 188 us for 4 x 4096 at 64.
     constexpr bool kProductsFirst = K + V > 128;
     int j = 0;
     for (; j < J; ++j) {
-        if (ahead) {
+        if (ahead && j > 0) {
             copy_k(j + 1);
             copy_v(j);
         }
@@ -183,7 +185,7 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
     }
     uint32_t seen = ~0u;  // of tile j - 1
     for (; j < tiles; ++j) {
-        if (ahead) {
+        if (ahead && j > 0) {
             copy_k(j + 1);
             copy_v(j);
         }

@@ -67,10 +67,11 @@ template <int K, int V> struct Rows {
     __device__ __forceinline__ void load_q(const bf16_t *row, bool negative, int lane) {
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) q[ks] = load_frag(row + 16 * ks + 8 * (lane >> 5));
-        const uint32_t sign = negative ? 0x80008000u : 0u;
+        if (negative) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-            q[ks] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, q[ks]) ^ (u32x4){sign, sign, sign, sign});
+            for (int ks = 0; ks < KS; ++ks)
+                q[ks] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, q[ks]) ^ (u32x4){0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u});
+        }
     }
     __device__ __forceinline__ void reset() {
         m = -INFINITY;
@@ -205,15 +206,19 @@ template <int K, int V> struct Rows {
             const uint32_t mine = (sees >> (8 * x)) & 255u;  // bits 8 x .. 8 x + 7 are the lane's of these 16 tokens
             if (!__any(mine != 0)) continue;                 // no row of the wave sees any of them
             bf16x8 vf[DB];
-            uint32_t odd = 0;
 #pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                vf[d] = v_frag(lv, x, d, lane);
-                const u32x4 u = __builtin_bit_cast(u32x4, vf[d]);
+            for (int d = 0; d < DB; ++d) vf[d] = v_frag(lv, x, d, lane);
+            bool strange = false;
+            if (__any(mine != 255u)) {
+                uint32_t odd = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) odd |= (u[i] & 0x7F807F80u) + 0x00800080u;  // an exponent of ones carries
+                for (int d = 0; d < DB; ++d) {
+                    const u32x4 u = __builtin_bit_cast(u32x4, vf[d]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) odd |= (u[i] & 0x7F807F80u) + 0x00800080u;  // an exponent of ones carries
+                }
+                strange = __any((odd & 0x80008000u) != 0);
             }
-            const bool strange = __any(mine != 255u) && __any((odd & 0x80008000u) != 0);
             if (strange) {
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
