@@ -42,7 +42,12 @@
  *    nothing (not written, read as zeros, seen by no row).
  *  - Arithmetic: fp32 scores, softmax statistics and accumulation. With bf16
  *    inputs the weights w_j are rounded to bf16 (by at most 2^-8 of each) before
- *    the product with v. Results do not depend on timing: no atomics.
+ *    the product with v; over a cache with up to 16 rows (mean new tokens of a
+ *    sequence times H / Hk) they keep 16 bits. E4M3 codes are multiplied as
+ *    exact bf16 numbers, but below bf16's least normal one (2^-126) and above
+ *    its largest (infinity). Results do not depend on timing: no atomics.
+ *  - cu_seqlens, lens, page_table and tree_mask must not change while a call
+ *    that reads them runs.
  */
 #ifndef KDA_ATTN_H_
 #define KDA_ATTN_H_
@@ -88,7 +93,7 @@ typedef struct {
  *   q  [T_total, H, d_k]   k  [T_total, Hk, d_k]   v  [T_total, Hk, d_v]   in_dtype
  *   o  [T_total, H, d_v]   out_dtype output (dense)
  *
- * Sizes: N >= 1, H >= 1, 0 <= T_total < 2^31 - 1024, 128 T_total H <= 2^40, 16 N H < 2^31.
+ * Sizes: N >= 1, H >= 1, T_total >= 0, T_total H < 2^31 - 1024, 16 N H < 2^31.
  * dtype pairs: (F32, F32), (BF16, BF16), (BF16, F32).
  * `scale` is finite (1 / sqrt(d_k) is customary).
  */
@@ -105,8 +110,9 @@ kda_status_t kda_attn_fwd(const void *q, const void *k, const void *v, const int
  * F32 and BF16 caches hold k and v as given. An E4M3 cache holds, per token
  * and head, the least e >= -127 with max |x| <= 448 * 2^e over the row's finite
  * elements, and x * 2^-e rounded to the nearest code (ties to even): exact but
- * for that one rounding. An infinity or NaN becomes a NaN. A page that is
- * written must belong to one position of one sequence of the call.
+ * for that one rounding. An infinity or NaN becomes a NaN. Pages may be shared
+ * by sequences, but a place that the call writes must be one position of one
+ * sequence.
  */
 kda_status_t kda_kv_write(const void *k, const void *v, const int32_t *cu_seqlens, int32_t N, int32_t T_total,
                           int32_t Hk, int32_t d_k, int32_t d_v, int64_t k_stride, int64_t v_stride,
@@ -137,7 +143,7 @@ kda_status_t kda_kv_read(void *k, void *v, const int32_t *cu_seqlens, int32_t N,
  *   q  [T_total, H, d_k]  in_dtype    o  [T_total, H, d_v]  out_dtype output (dense)
  *
  * dtype pairs as for kda_attn_fwd; F32 inputs with an F32 cache, BF16 inputs
- * with a BF16 or E4M3 one. Sizes as for kda_attn_fwd, T_total H < 2^31, N max_pages < 2^31,
+ * with a BF16 or E4M3 one. Sizes as for kda_attn_fwd, N max_pages < 2^31,
  * max_pages page_size < 2^31 - 1024.
  * workspace: kda_attn_cache_fwd_workspace_size bytes of device scratch. Calls
  * that may overlap must not share one.

@@ -67,6 +67,29 @@ def test_several_tokens(dt, kv, new):
 
 
 @pytest.mark.parametrize("dt,kv", KINDS)
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (128, 64), (64, 128)])
+@pytest.mark.parametrize("page", [16, 64, 256])
+def test_several_tokens_dims_and_pages(dt, kv, dk, dv, page):
+    """More than 16 rows for a kv head: 9 and 20 tokens for 3 query heads each; the second has none before it."""
+    run(28, [9, 0, 20], [150, 7, 0], 6, 2, dk, dv, page, dt, kv)
+
+
+@pytest.mark.parametrize("dt,kv", KINDS)
+def test_more_rows_than_a_tile(dt, kv):
+    """64 drafted tokens for 9 query heads: 576 rows; and 300 tokens in a row."""
+    new = [64]
+    run(29, new, [100], 9, 1, 64, 64, 32, dt, kv, masks=ac.tree_masks(new, 29))
+    run(30, [300], [77], 2, 2, 64, 64, 32, dt, kv)
+
+
+@pytest.mark.parametrize("dt,kv", KINDS)
+def test_several_tokens_over_a_long_cache(dt, kv):
+    """Rows of several tokens whose cache is split over workgroups, with a mask."""
+    new = [12, 5, 33]
+    run(31, new, [2500, 40, 900], 4, 1, 64, 64, 64, dt, kv, masks=ac.tree_masks(new, 31))
+
+
+@pytest.mark.parametrize("dt,kv", KINDS)
 @pytest.mark.parametrize("new", [[1], [2, 9], [24, 3], [63], [64, 64], [5, 0, 31]])
 def test_trees(dt, kv, new):
     run(6, new, [50, 3, 0][:len(new)], 8, 2, 64, 128, 16, dt, kv, masks=ac.tree_masks(new, 6))
@@ -124,15 +147,16 @@ def test_mask_bits_of_tokens_that_are_not_there():
 
 @pytest.mark.parametrize("dt,kv", KINDS)
 @pytest.mark.parametrize("which", ["k", "v"])
-def test_tokens_not_seen_have_no_influence(dt, kv, which):
+@pytest.mark.parametrize("H", [4, 20])
+def test_tokens_not_seen_have_no_influence(dt, kv, which, H):
     """A drafted token that holds NaN: rows that do not see it are right, rows that do are NaN. What no
-    sequence holds is NaN throughout (ac.Cache fills it so)."""
+    sequence holds is NaN throughout (ac.Cache fills it so). 10 and 50 rows for a kv head."""
     new, ctx = [5], [45]
     masks = [0b00001, 0b00011, 0b00101, 0b01001, 0b10001]  # token 2 is seen by itself alone
     c = filled(15, [50], 2, 64, 64, 16, kv)
-    q = ac.normal(15, 5, 4, 64).to(DT[dt]).cuda()
+    q = ac.normal(15, 5, H, 64).to(DT[dt]).cuda()
     ref, lim = ac.cache_reference(q, c, new, masks, 0.125, dt == "bf16", dt == "bf16")
-    page, off = c.place(0, [47])
+    page, off = c.place(0, [ctx[0] + 2])
     getattr(c, which).view(torch.uint8)[int(page[0]), :, int(off[0])] = 0xFF
     got = call(q, new, c, masks, 0.125, dt)
     keep = [0, 1, 3, 4]
@@ -184,8 +208,9 @@ def test_q_of_a_wider_row():
     ac.check("o", call(q, [1, 2], c, None, 0.125, "bf16"), ref, lim)
 
 
-def test_offsets_past_32_bits():
-    """A cache of more than 2^32 bytes whose used pages lie at its end."""
+@pytest.mark.parametrize("L", [1, 9])
+def test_offsets_past_32_bits(L):
+    """A cache of more than 2^32 bytes whose used pages lie at its end, for single and several tokens."""
     pages, page, Hk, d = 2 ** 18 + 40, 64, 1, 128
     k = torch.zeros((pages, Hk, page, d), dtype=torch.bfloat16, device="cuda")
     assert k.numel() * 2 > 2 ** 32
@@ -194,9 +219,9 @@ def test_offsets_past_32_bits():
     base = pages - c.k.shape[0]
     k[base:], v[base:] = c.k, c.v
     table = torch.where(c.table >= 0, c.table + base, c.table)
-    q = ac.normal(19, 1, 4, d).bfloat16().cuda()
-    got = attn.kda_attn_cache_fwd(q, ac.offsets([1]), c.lens, table, k, v, scale=0.09)
-    ref, lim = ac.cache_reference(q, c, [1], None, 0.09, True, True)
+    q = ac.normal(19, L, 4, d).bfloat16().cuda()
+    got = attn.kda_attn_cache_fwd(q, ac.offsets([L]), c.lens, table, k, v, scale=0.09)
+    ref, lim = ac.cache_reference(q, c, [L], None, 0.09, True, True)
     ac.check("o", got, ref, lim)
     new = ac.normal(20, 1, Hk, d).bfloat16().cuda()
     attn.kda_kv_write(new, new, ac.offsets([1]), c.lens, table, k, v)
@@ -275,6 +300,41 @@ def test_captured_and_replayed():
         c.host_lens = [int(x) for x in lens.cpu()]
         ref, lim = ac.cache_reference(q, c, [1] * N, None, d ** -0.5, True, True)
         ac.check(f"replay {step}", got, ref, lim)
+
+
+def test_captured_tree_over_a_split_cache():
+    """Drafted tokens over a cache that is split over workgroups, in two graphs with workspaces of their own,
+    replayed in turn with eager calls of other inputs between them."""
+    new, H, Hk, d = [6, 11], 8, 2, 64
+    c = filled(32, [1500, 700], Hk, d, d, 64, "e4m3")
+    T, masks = sum(new), [ac.mask_tensor(ac.tree_masks(new, s)) for s in (1, 2)]
+    cu = ac.offsets(new)
+    n = attn.kda_attn_cache_fwd_workspace_size(2, T, H, Hk, d, d, torch.bfloat16)
+    q = [torch.zeros((T, H, d), dtype=torch.bfloat16, device="cuda") for _ in masks]
+    o = [torch.zeros_like(x) for x in q]
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in masks]
+
+    def layer(i, out, work):
+        attn.kda_attn_cache_fwd(q[i], cu, *c.args(), **c.exps(), tree_mask=masks[i], o=out, workspace=work)
+
+    graphs = []
+    for i in range(2):
+        layer(i, o[i], ws[i])
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            layer(i, o[i], ws[i])
+    for step in range(4):
+        for i in range(2):
+            q[i].copy_(ac.normal(2000 + 10 * step + i, T, H, d))
+        graphs[0].replay()
+        graphs[1].replay()
+        got = [x.clone() for x in o]
+        for i in range(2):
+            eager = torch.empty_like(o[i])
+            layer(i, eager, torch.empty_like(ws[i]))
+            torch.cuda.synchronize()
+            assert torch.equal(got[i], eager), f"replay {step} of graph {i}"
 
 
 def test_prompt_then_decode_equals_one_prompt():

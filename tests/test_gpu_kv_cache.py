@@ -158,6 +158,51 @@ def test_one_token_for_many_sequences():
     assert same(rk.double().cpu(), wanted(k, "e4m3")) and same(rv.double().cpu(), wanted(v, "e4m3"))
 
 
+@pytest.mark.parametrize("lens", [[0] * 100 + [3] + [0] * 90 + [200, 0, 1], [1, 0] * 80, [130]])
+def test_sequences_without_tokens_between_others(lens):
+    """The place of a token is found whatever number of empty sequences lies before it."""
+    c = ac.Cache([x + 5 for x in lens], 3, 64, 64, 16, "bf16")
+    T = sum(lens)
+    k, v = ac.normal(8, T, 3, 64).bfloat16().cuda(), ac.normal(9, T, 3, 64).bfloat16().cuda()
+    cu = ac.offsets(lens)
+    attn.kda_kv_write(k, v, cu, *c.args())
+    rk, rv = attn.kda_kv_read(T, cu, *c.args())
+    assert torch.equal(rk, k) and torch.equal(rv, v)
+    at = 0
+    for n, L in enumerate(lens):
+        held = c.values(n, L + 5)
+        assert torch.equal(held[0][5:], k[at:at + L].double().cpu()) and torch.equal(held[1][5:], v[at:at + L].double().cpu())
+        at += L
+
+
+def test_another_stream_and_capture():
+    c, e = (ac.Cache([9, 40], 2, 64, 64, 16, "e4m3") for _ in "ce")
+    k, v = ac.normal(10, 12, 2, 64).bfloat16().cuda(), ac.normal(11, 12, 2, 64).bfloat16().cuda()
+    cu = ac.offsets([2, 10])
+    attn.kda_kv_write(k, v, cu, *c.args(), **c.exps())
+    want = attn.kda_kv_read(12, cu, *c.args(), **c.exps())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    attn.kda_kv_write(k, v, cu, *e.args(), **e.exps(), stream=s)
+    got = attn.kda_kv_read(12, cu, *e.args(), **e.exps(), stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    out = [torch.zeros_like(x) for x in want]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        attn.kda_kv_write(k, v, cu, *e.args(), **e.exps())
+        attn.kda_kv_read(12, cu, *e.args(), **e.exps(), k=out[0], v=out[1])
+    for step in range(3):
+        k.copy_(ac.normal(20 + step, *k.shape))
+        graph.replay()
+        got = out[0].clone()
+        attn.kda_kv_write(k, v, cu, *c.args(), **c.exps())
+        want = attn.kda_kv_read(12, cu, *c.args(), **c.exps())
+        torch.cuda.synchronize()
+        assert torch.equal(got, want[0]) and torch.equal(out[1], want[1])
+
+
 def test_refused_on_the_gpu():
     c = ac.Cache([4], 1, 64, 64, 16, "e4m3")
     k = torch.zeros((4, 1, 64), dtype=torch.bfloat16, device="cuda")
