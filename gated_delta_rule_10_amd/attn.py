@@ -51,7 +51,7 @@ def load_library() -> ctypes.CDLL:
                                        P, P, P, sz, P]
     for f in (lib.kda_attn_fwd, lib.kda_kv_write, lib.kda_kv_read, lib.kda_attn_cache_fwd):
         f.restype = ctypes.c_int
-    lib.kda_attn_cache_fwd_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.c_int]
+    lib.kda_attn_cache_fwd_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32, i32, ctypes.c_int]
     lib.kda_attn_cache_fwd_workspace_size.restype = sz
     _lib = lib
     return lib
@@ -234,9 +234,10 @@ def kda_kv_read(T: int, cu_seqlens: torch.Tensor, cache_lens: torch.Tensor, page
     return k, v
 
 
-def kda_attn_cache_fwd_workspace_size(N: int, T: int, H: int, Hk: int, d_k: int, d_v: int,
+def kda_attn_cache_fwd_workspace_size(N: int, T: int, H: int, Hk: int, d_k: int, d_v: int, max_tokens: int,
                                       in_dtype: torch.dtype) -> int:
-    return int(load_library().kda_attn_cache_fwd_workspace_size(N, T, H, Hk, d_k, d_v, _code(in_dtype)))
+    """Bytes on the current device; max_tokens: what the page table reaches, max_pages * page_size."""
+    return int(load_library().kda_attn_cache_fwd_workspace_size(N, T, H, Hk, d_k, d_v, max_tokens, _code(in_dtype)))
 
 
 def kda_attn_cache_fwd(q: torch.Tensor, cu_seqlens: torch.Tensor, cache_lens: torch.Tensor, page_table: torch.Tensor,
@@ -271,13 +272,15 @@ def kda_attn_cache_fwd(q: torch.Tensor, cu_seqlens: torch.Tensor, cache_lens: to
         with _alloc_on(stream):
             o = _out(o, (T, H, d_v), out_dtype, device)
             if workspace is None:
-                need = int(lib.kda_attn_cache_fwd_workspace_size(N, T, H, Hk, d_k, d_v, _code(q.dtype)))
-                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+                need = lib.kda_attn_cache_fwd_workspace_size(N, T, H, Hk, d_k, d_v, cache.max_pages * cache.page_size,
+                                                             _code(q.dtype))
+                if need:
+                    workspace = torch.empty(need, dtype=torch.uint8, device=device)
         _dense(device, o=o, workspace=workspace)
         st = lib.kda_attn_cache_fwd(q.data_ptr(), cu_seqlens.data_ptr(), N, T, H, Hk, d_k, d_v, sq, _code(q.dtype),
                                     _code(out_dtype), d_k ** -0.5 if scale is None else float(scale),
-                                    ctypes.byref(cache), _ptr(tree_mask), o.data_ptr(), workspace.data_ptr(),
-                                    workspace.numel() * workspace.element_size(), s)
+                                    ctypes.byref(cache), _ptr(tree_mask), o.data_ptr(), _ptr(workspace),
+                                    0 if workspace is None else workspace.numel() * workspace.element_size(), s)
     if st != KDA_OK:
         raise KDAError(st, "kda_attn_cache_fwd")
     return o

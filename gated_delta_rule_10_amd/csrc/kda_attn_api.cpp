@@ -120,9 +120,10 @@ kda_status_t kda_kv_read(void *k, void *v, const int32_t *cu_seqlens, int32_t N,
 }
 
 size_t kda_attn_cache_fwd_workspace_size(int32_t N, int32_t T_total, int32_t H, int32_t Hk, int32_t d_k, int32_t d_v,
-                                         kda_dtype_t in_dtype) {
+                                         int32_t max_tokens, kda_dtype_t in_dtype) {
     if (!sizes_ok(N, T_total, H, Hk) || !head_dim_ok(d_k) || !head_dim_ok(d_v) || !dtype_valid(in_dtype)) return 0;
-    return kda::attn_cache_workspace(N, T_total, H, Hk, d_v, in_dtype);
+    if (T_total == 0 || max_tokens < 1) return 0;
+    return kda::attn_cache_workspace(N, T_total, H, Hk, d_v, max_tokens, in_dtype);
 }
 
 kda_status_t kda_attn_cache_fwd(const void *q, const int32_t *cu_seqlens, int32_t N, int32_t T_total, int32_t H,
@@ -140,7 +141,9 @@ kda_status_t kda_attn_cache_fwd(const void *q, const int32_t *cu_seqlens, int32_
         return KDA_ERR_UNSUPPORTED;
     if (!stride_ok(q_stride, H, d_k)) return KDA_ERR_INVALID_ARG;
     if (T_total == 0) return KDA_OK;
-    if (!workspace || workspace_bytes < kda::attn_cache_workspace(N, T_total, H, Hk, d_v, in_dtype)) return KDA_ERR_WORKSPACE;
+    const size_t need =
+        kda::attn_cache_workspace(N, T_total, H, Hk, d_v, cache->max_pages * cache->page_size, in_dtype);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     kda::AttnArgs a{};
     a.q = q; a.k = cache->k; a.v = cache->v; a.kexp = cache->k_exp; a.vexp = cache->v_exp; a.qs = q_stride;
     a.cu = cu_seqlens; a.lens = cache->lens; a.table = cache->page_table; a.mask = tree_mask; a.o = o; a.ws = workspace;

@@ -576,7 +576,8 @@ template <int K, int V> hipError_t launch_dims(const AttnArgs &a, hipStream_t st
 
 int32_t attn_cache_workgroups() { return kPerCu * compute_units(); }
 
-size_t attn_cache_workspace(int32_t N, int32_t T, int32_t H, int32_t Hk, int32_t V, kda_dtype_t in_dtype) {
+size_t attn_cache_workspace(int32_t N, int32_t T, int32_t H, int32_t Hk, int32_t V, int32_t max_tokens, kda_dtype_t in_dtype) {
+    if (max_tokens <= kWhole) return 0;
     const int R = tile_rows(T, N, H / Hk, in_dtype == KDA_F32);
     return prefix_bytes(N) + 2 * static_cast<size_t>(attn_cache_workgroups()) * part_floats(R, V) * sizeof(float);
 }

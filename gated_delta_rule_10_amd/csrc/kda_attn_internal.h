@@ -52,8 +52,9 @@ hipError_t launch_attn_cache(const AttnArgs &a, hipStream_t stream);
 hipError_t launch_kv_write(const KvArgs &a, hipStream_t stream);
 hipError_t launch_kv_read(const KvArgs &a, hipStream_t stream);
 
-// Workgroups and workspace bytes of the cache attention on the current device.
+// Workgroups and workspace bytes of the cache attention on the current device, for page tables
+// that reach max_tokens.
 int32_t attn_cache_workgroups();
-size_t attn_cache_workspace(int32_t N, int32_t T, int32_t H, int32_t Hk, int32_t V, kda_dtype_t in_dtype);
+size_t attn_cache_workspace(int32_t N, int32_t T, int32_t H, int32_t Hk, int32_t V, int32_t max_tokens, kda_dtype_t in_dtype);
 
 }  // namespace kda

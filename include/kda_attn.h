@@ -145,8 +145,8 @@ kda_status_t kda_kv_read(void *k, void *v, const int32_t *cu_seqlens, int32_t N,
  * dtype pairs as for kda_attn_fwd; F32 inputs with an F32 cache, BF16 inputs
  * with a BF16 or E4M3 one. Sizes as for kda_attn_fwd, N max_pages < 2^31,
  * max_pages page_size < 2^31 - 1024.
- * workspace: kda_attn_cache_fwd_workspace_size bytes of device scratch. Calls
- * that may overlap must not share one.
+ * workspace: kda_attn_cache_fwd_workspace_size bytes of device scratch, whatever
+ * they hold (NULL if that is 0). Calls that may overlap must not share one.
  */
 kda_status_t kda_attn_cache_fwd(const void *q, const int32_t *cu_seqlens, int32_t N, int32_t T_total, int32_t H,
                                 int32_t Hk, int32_t d_k, int32_t d_v, int64_t q_stride, kda_dtype_t in_dtype,
@@ -155,12 +155,14 @@ kda_status_t kda_attn_cache_fwd(const void *q, const int32_t *cu_seqlens, int32_
                                 hipStream_t stream);
 
 /*
- * Bytes of device workspace kda_attn_cache_fwd needs for these sizes on the
- * current device (0 for invalid sizes). It grows with N, and is otherwise
- * bounded by the device's compute units, not by the cached lengths.
+ * Bytes of device workspace kda_attn_cache_fwd needs on the current device for
+ * these sizes and page tables that reach max_tokens = max_pages * page_size
+ * cached tokens; 0 means the call may pass workspace = NULL (or the sizes are
+ * invalid). It grows with N, and is otherwise bounded by the device's compute
+ * units, not by the cached lengths.
  */
 size_t kda_attn_cache_fwd_workspace_size(int32_t N, int32_t T_total, int32_t H, int32_t Hk, int32_t d_k,
-                                         int32_t d_v, kda_dtype_t in_dtype);
+                                         int32_t d_v, int32_t max_tokens, kda_dtype_t in_dtype);
 
 #ifdef __cplusplus
 }

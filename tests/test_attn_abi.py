@@ -146,7 +146,8 @@ def test_kv_read_rejects(lib, over, status):
     (dict(q=None), INVALID), (dict(o=A + 2), INVALID), (dict(mask=A + 8), INVALID), (dict(H=3), INVALID),
     (dict(qs=1020), INVALID), (dict(scale=float("nan")), INVALID),
     (dict(c_dtype=attn.KDA_KV_F32), UNSUPPORTED), (dict(din=kda.KDA_F32, dout=kda.KDA_F32), UNSUPPORTED),
-    (dict(ws=None), kda.KDA_ERR_WORKSPACE), (dict(ws=A + 8), INVALID), (dict(wsb=1000), kda.KDA_ERR_WORKSPACE),
+    (dict(c_max_pages=40, ws=None), kda.KDA_ERR_WORKSPACE), (dict(ws=A + 8), INVALID),
+    (dict(c_max_pages=40, wsb=1000), kda.KDA_ERR_WORKSPACE),
 ])
 def test_attn_cache_fwd_rejects(lib, over, status):
     assert _cached(lib, **over) == status
@@ -154,11 +155,16 @@ def test_attn_cache_fwd_rejects(lib, over, status):
 
 def test_workspace_size(lib):
     ws = attn.kda_attn_cache_fwd_workspace_size
-    assert ws(1, 1, 8, 2, 128, 128, torch.bfloat16) > 0
-    assert ws(0, 1, 8, 2, 128, 128, torch.bfloat16) == 0
-    assert ws(1, 1, 8, 3, 128, 128, torch.bfloat16) == 0
-    assert ws(1, 1, 8, 2, 96, 128, torch.bfloat16) == 0
-    assert ws(5000, 5000, 8, 2, 128, 128, torch.bfloat16) > ws(1, 1, 8, 2, 128, 128, torch.bfloat16)
+    bf = torch.bfloat16
+    assert ws(1, 1, 8, 2, 128, 128, 4096, bf) > 0
+    assert ws(1, 1, 8, 2, 128, 128, 256, bf) == 0                       # a cache that is never split
+    assert ws(0, 1, 8, 2, 128, 128, 4096, bf) == 0
+    assert ws(1, 1, 8, 3, 128, 128, 4096, bf) == 0
+    assert ws(1, 1, 8, 2, 96, 128, 4096, bf) == 0
+    assert ws(1, 1, 8, 2, 128, 128, 0, bf) == 0
+    assert ws(5000, 5000, 8, 2, 128, 128, 4096, bf) > ws(1, 1, 8, 2, 128, 128, 4096, bf)
+    assert ws(1, 64, 8, 2, 128, 128, 2 ** 30, bf) == ws(1, 64, 8, 2, 128, 128, 4096, bf)  # not the lengths
+    assert _cached(lib, c_max_pages=4, c_page_size=256, ws=None, wsb=0) == kda.KDA_ERR_WORKSPACE
 
 
 def test_binding_refuses_host_tensors_and_wrong_layouts(lib):

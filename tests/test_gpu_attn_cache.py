@@ -110,6 +110,19 @@ def test_large_scores():
     run(10, [1, 3], [300, 40], 4, 2, 64, 64, 16, "f32", "f32", scale=-2.0)
 
 
+def test_magnitudes():
+    """Tokens whose keys and values differ by many orders of magnitude, each with its own scale."""
+    for L, ctx in ((1, 150), (9, 150)):
+        c = ac.Cache([ctx + L], 2, 64, 64, 16, "e4m3", seed=33)
+        k, v = ac.normal(33, ctx + L, 2, 64), ac.normal(34, ctx + L, 2, 64)
+        f = 10.0 ** (6 * torch.rand(ctx + L, 2, 1, generator=torch.Generator().manual_seed(1)) - 6)
+        g = 10.0 ** (50 * torch.rand(ctx + L, 2, 1, generator=torch.Generator().manual_seed(2)) - 30)
+        c.put(0, (k * f).bfloat16().float(), (v * g).bfloat16().float())
+        q = ac.normal(35, L, 8, 64).bfloat16().cuda()
+        ref, lim = ac.cache_reference(q, c, [L], None, 0.125, True, True)
+        ac.check(f"{L} new", call(q, [L], c, None, 0.125, "bf16"), ref, lim)
+
+
 def test_many_sequences():
     """More sequences than a workgroup looks over at once, some of them without new tokens."""
     new = [1, 0, 2, 1] * 150
@@ -231,7 +244,7 @@ def test_offsets_past_32_bits(L):
 
 def test_same_call_same_bits_whatever_the_workspace_held():
     q, c, a = run(21, [1, 1], [2500, 700], 8, 2, 64, 64, 64, "bf16", "e4m3")
-    n = attn.kda_attn_cache_fwd_workspace_size(2, 2, 8, 2, 64, 64, torch.bfloat16)
+    n = attn.kda_attn_cache_fwd_workspace_size(2, 2, 8, 2, 64, 64, c.table.shape[1] * 64, torch.bfloat16)
     for fill in (0, 0xFF, 0x7F):
         ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
         assert torch.equal(call(q, [1, 1], c, None, 64 ** -0.5, "bf16", workspace=ws), a)
@@ -240,7 +253,7 @@ def test_same_call_same_bits_whatever_the_workspace_held():
 def test_writes_nothing_outside():
     c = filled(22, [2600, 30], 2, 64, 128, 64, "bf16")
     q = ac.normal(22, 2, 4, 64).bfloat16().cuda()
-    n = attn.kda_attn_cache_fwd_workspace_size(2, 2, 4, 2, 64, 128, torch.bfloat16)
+    n = attn.kda_attn_cache_fwd_workspace_size(2, 2, 4, 2, 64, 128, c.table.shape[1] * 64, torch.bfloat16)
     bufs = []
 
     def guarded(nbytes):
@@ -274,7 +287,8 @@ def test_captured_and_replayed():
     cu = ac.offsets([1] * N)
     q, k, v = (torch.zeros((N, h, d), dtype=torch.bfloat16, device="cuda") for h in (H, Hk, Hk))
     o = torch.zeros_like(q)
-    ws = torch.empty(attn.kda_attn_cache_fwd_workspace_size(N, N, H, Hk, d, d, torch.bfloat16), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(attn.kda_attn_cache_fwd_workspace_size(N, N, H, Hk, d, d, c.table.shape[1] * page, torch.bfloat16) + 16,
+                     dtype=torch.uint8, device="cuda")
 
     def layer(out, work):
         attn.kda_kv_write(k, v, cu, lens, c.table, c.k, c.v, **c.exps())
@@ -309,7 +323,8 @@ def test_captured_tree_over_a_split_cache():
     c = filled(32, [1500, 700], Hk, d, d, 64, "e4m3")
     T, masks = sum(new), [ac.mask_tensor(ac.tree_masks(new, s)) for s in (1, 2)]
     cu = ac.offsets(new)
-    n = attn.kda_attn_cache_fwd_workspace_size(2, T, H, Hk, d, d, torch.bfloat16)
+    n = attn.kda_attn_cache_fwd_workspace_size(2, T, H, Hk, d, d, c.table.shape[1] * 64, torch.bfloat16)
+    assert n > 0
     q = [torch.zeros((T, H, d), dtype=torch.bfloat16, device="cuda") for _ in masks]
     o = [torch.zeros_like(x) for x in q]
     ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in masks]
@@ -372,7 +387,7 @@ def test_prompt_then_decode_equals_one_prompt():
 
 
 def test_refused_on_the_gpu():
-    c = filled(31, [20], 2, 64, 64, 16, "e4m3")
+    c = filled(31, [20], 2, 64, 64, 16, "e4m3", max_pages=40)
     q = torch.zeros((1, 4, 64), dtype=torch.bfloat16, device="cuda")
     cu = ac.offsets([1])
     with pytest.raises(ValueError):

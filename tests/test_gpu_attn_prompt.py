@@ -96,7 +96,6 @@ def test_tokens_not_seen_have_no_influence(dt, bad):
         got = attn.kda_attn_fwd(q, k, v, ac.offsets(lens), scale=0.09)
         torch.cuda.synchronize()
         # a token's value is added alone where a value near it is not finite: another order of the sum
-        _, lim = ac.prompt_reference(q, clean.new_zeros(k.shape), v.nan_to_num(0, 0, 0), lens, 0.09, dt == "bf16", dt == "bf16")
         ref, lim = ac.prompt_reference(q[:99], k[:99], v[:99], [99], 0.09, dt == "bf16", dt == "bf16")
         ac.check("rows before", got[:99], ref, lim)
         assert torch.equal(got[100:], clean[100:])
