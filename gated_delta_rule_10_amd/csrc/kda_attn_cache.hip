@@ -308,15 +308,16 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
     const int part_of = blockIdx.x % PARTS, rest = blockIdx.x / PARTS, kvh = rest % a.Hk;
     const int64_t slot = rest / a.Hk;
     const int n = seq_of_slot(a.cu, a.N, a.T, a.G, R, slot, tid & 63);
+    const int64_t *prefix = static_cast<const int64_t *>(a.ws);
+    const int64_t U = prefix[a.N], before = prefix[n];  // on their way with what seq_of reads
     const Seq q = seq_of<R, STEP>(a, n);
     const int64_t tile = slot - static_cast<int64_t>(q.start) * a.G / R - n;
     if (tile < 0 || tile >= q.tiles) return;
     const int64_t r0 = tile * R + part_of * kJoinRows;
     const int rows = static_cast<int>(min(static_cast<int64_t>(kJoinRows), static_cast<int64_t>(q.count) * a.G - r0));
     if (rows <= 0) return;
-    const int64_t *prefix = static_cast<const int64_t *>(a.ws);
-    const int64_t U = prefix[a.N], W = line_workgroups(a, U);
-    const int64_t s = prefix[n] + (static_cast<int64_t>(kvh) * q.tiles + tile) * q.steps, e = s + q.steps;
+    const int64_t W = line_workgroups(a, U);
+    const int64_t s = before + (static_cast<int64_t>(kvh) * q.tiles + tile) * q.steps, e = s + q.steps;
     const int64_t w0 = line_owner(s, U, W), w1 = line_owner(e - 1, U, W);
     if (w0 == w1) return;
     // piece i of the tile: of workgroup w0 + i, whose first piece it is unless w0 had other work before
@@ -337,7 +338,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
         for (int d = 1; d < LPR; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
         f32x4 x = {0.f, 0.f, 0.f, 0.f};
         float l = 0.f;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = sub; i < pieces; i += share) {
             const float *p = piece(i);
             const float mi = p[R * V + row], f = mi == -INFINITY ? 0.f : exp2f(mi - m);
