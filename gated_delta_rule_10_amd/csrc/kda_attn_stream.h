@@ -7,10 +7,12 @@
 // key and value read serves all of them.
 //
 // Work of a workgroup: four waves; a step gives each wave 32 consecutive
-// tokens (fp32: 16, so that two workgroups fit a compute unit's LDS). Each wave keeps its own m, sum and output over its tokens (no barrier
-// while streaming) and the four are joined at the end. A wave holds the next
-// step's keys and values in registers while it works on the current ones, which
-// lie in its own part of LDS.
+// tokens (fp32: 16, so that two workgroups fit a compute unit's LDS). Each wave
+// keeps its own m, sum and output over its tokens (no barrier while streaming)
+// and the four are joined at the end. A wave holds the next step's keys and
+// values in registers while it works on the current ones, which lie in its own
+// part of LDS. Two steps ahead, and three or four workgroups to a compute unit
+// with smaller steps, were slower for an e4m3 cache.
 //
 // Products (16 x 16 matrix instructions, 32-deep). S^T = K Q^T puts a row's
 // scores for tokens 16 b + 4 g + i (g = lane / 16) into registers of the lanes
