@@ -57,7 +57,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a,
 // ---- bf16
 //
 // NW waves of 32 rows each share tiles of 64 keys and values in LDS, copied there
-// directly from memory ahead of their use (two buffers each).
+// directly from memory ahead of their use (two buffers each). Where there are too few
+// rows for all compute units (halves()), a tile is 128 keys and values, its PARTS = 2
+// halves go to one half of the waves each, both with the same rows, and their maxima,
+// sums and outputs are joined in LDS in the end.
 //
 // What bounds it: at d = 128 the matrix cores (2 L^2 d H operations for L tokens)
 // under the card's power limit: 7.4 ms for one prompt of 32768, H = 32, Hk = 8 (1190
@@ -92,20 +95,22 @@ template <typename R, int D, bool KEYS, int NW> struct Copier {
         if (left >= kTile) {
 #pragma unroll
             for (int i = 0; i < N; ++i) copy_to_lds(dst + (i * NW + w) * 1024, next, off[i]);
-        } else {
+        } else {  // behind the tensor's end: its last row
+            const bf16_t *from = next + min(left - 1, 0) * stride;
 #pragma unroll
-            for (int i = 0; i < N; ++i) copy_to_lds(dst + (i * NW + w) * 1024, next, place(i, left - 1, w, lane));
+            for (int i = 0; i < N; ++i) copy_to_lds(dst + (i * NW + w) * 1024, from, place(i, max(left - 1, 0), w, lane));
         }
         next += kTile * stride;
         left -= kTile;
     }
 };
 
-template <int K, int V, int NW>
+template <int K, int V, int NW, int PARTS>
 __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a, int slots) {
     using P = Rows<K, V>;
-    constexpr int R = 32 * NW;
-    __shared__ __align__(1024) char lds[2 * (P::KB + P::VB)];
+    constexpr int R = 32 * NW / PARTS, kTurn = PARTS * kTile;  // rows; tokens of a tile
+    constexpr int KB = PARTS * P::KB, VB = PARTS * P::VB;
+    __shared__ __align__(1024) char lds[2 * (KB + VB)];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     const int kvh = blockIdx.x % a.Hk;
@@ -121,7 +126,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
     const int last = static_cast<int>((min(first + R, all) - 1) / a.G);  // last token of the tile
 
     // this wave's rows; rows past the sequence's repeat its last one and are not stored
-    const int64_t wr0 = first + 32 * w, wr1 = min(wr0 + 32, all);
+    const int part = PARTS == 1 ? 0 : w / (NW / PARTS), shift = part * kTile;  // its tokens of a tile
+    const int64_t wr0 = first + 32 * (w - part * (NW / PARTS)), wr1 = min(wr0 + 32, all);
     const bool some = wr0 < all;
     const int tok1 = static_cast<int>((max(wr1, static_cast<int64_t>(1)) - 1) / a.G);
     const int64_t row = min(wr0 + (lane & 31), all - 1);
@@ -133,8 +139,9 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
 
     const uint32_t base = lds_address(lds);
     // LDS: keys of even and odd tiles, values of even and odd tiles
-    auto lk = [&](int j) { return (j & 1) * P::KB; };
-    auto lv = [&](int j) { return 2 * P::KB + (j & 1) * P::VB; };
+    auto lk = [&](int j) { return (j & 1) * KB; };
+    auto lv = [&](int j) { return 2 * KB + (j & 1) * VB; };
+    const char *const own_k = lds + part * P::KB, *const own_v = lds + part * P::VB;
     Copier<P, K, true, NW> kc;
     Copier<P, V, false, NW> vc;
     kc.begin(static_cast<const bf16_t *>(a.k) + kvh * K, a.ks, start, a.T, w, lane);
@@ -144,22 +151,30 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
     // Copies for a tile are issued two turns before its first use, which is when the last reader
     // of that buffer has gone; those of tile 0's values and tile 1's keys at the start. The first
     // J tiles are seen whole by every row of the workgroup.
-    const int J = (static_cast<int>(first / a.G) + 1) / kTile, tiles = last / kTile + 1;
+    const int J = (static_cast<int>(first / a.G) + 1) / kTurn, tiles = last / kTurn + 1;
     const bool ahead = w < NW / 2;
-    auto copy_k = [&](int j) { if (j < tiles) kc.tile(base + lk(j), w, lane); };
-    auto copy_v = [&](int j) { if (j < tiles) vc.tile(base + lv(j), w, lane); };
+    auto copy_k = [&](int j) {
+        if (j >= tiles) return;
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) kc.tile(base + lk(j) + i * P::KB, w, lane);
+    };
+    auto copy_v = [&](int j) {
+        if (j >= tiles) return;
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i) vc.tile(base + lv(j) + i * P::VB, w, lane);
+    };
     auto swap = [&](bool wait) {
         if (wait) wait_copies();
         phase_barrier();
     };
-    auto sees = [&](int j) { return some && j * kTile <= tok1; };  // the wave has work in tile j
+    auto sees = [&](int j) { return some && j * kTurn + shift <= tok1; };  // the wave has work in tile j
     copy_k(0);
     st.load_q(static_cast<const bf16_t *>(a.q) + static_cast<int64_t>(start + own) * a.qs + h * K, a.c < 0.f, lane);
     copy_v(0);
     copy_k(1);
     // tile 0's keys; a call of one tile has no copies of tile 1 behind them
-    if (tiles > 1) wait_copies<Copier<P, V, false, NW>::N + Copier<P, K, true, NW>::N>();
-    else wait_copies<Copier<P, V, false, NW>::N>();
+    if (tiles > 1) wait_copies<PARTS * (Copier<P, V, false, NW>::N + Copier<P, K, true, NW>::N)>();
+    else wait_copies<PARTS * Copier<P, V, false, NW>::N>();
     phase_barrier();
     if (!ahead) swap(false);
     // The wave in its products issues first where they are the longer turn (two heads of 64
@@ -174,11 +189,11 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
         }
         if (kProductsFirst) __builtin_amdgcn_s_setprio(1);
         if (j > 0) {
-            st.values(lds + lv(j - 1), lane);
-            st.scores(lds + lk(j), lane);
+            st.values(own_v + lv(j - 1), lane);
+            st.scores(own_k + lk(j), lane);
             P::template interleave<true>();
         } else {
-            st.scores(lds + lk(0), lane);
+            st.scores(own_k + lk(0), lane);
             P::template interleave<false>();
         }
         if (kProductsFirst) __builtin_amdgcn_s_setprio(0);
@@ -196,29 +211,53 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
             copy_k(j + 1);
             copy_v(j);
         }
-        if (j > 0 && sees(j - 1)) st.values_masked(lds + lv(j - 1), seen, lane);
-        if (sees(j)) st.scores(lds + lk(j), lane);
+        if (j > 0 && sees(j - 1)) st.values_masked(own_v + lv(j - 1), seen, lane);
+        if (sees(j)) st.scores(own_k + lk(j), lane);
         swap(!ahead);
         if (!ahead) {
             copy_k(j + 2);
             copy_v(j + 1);
         }
         if (sees(j)) {
-            seen = P::of_lane(low_bits(own - j * kTile + 1), lane);
+            seen = P::of_lane(low_bits(own - j * kTurn - shift + 1), lane);
             st.template softmax<true>(c, seen);
         }
         swap(ahead);
     }
-    if (sees(j - 1)) st.values_masked(lds + lv(j - 1), seen, lane);
+    if (sees(j - 1)) st.values_masked(own_v + lv(j - 1), seen, lane);
     if (ahead) swap(false);
+    float l = swap32_sum(st.l);
+    if (PARTS == 2) {
+        // the later part's rows are added to the first's, in LDS: [V / 4][R] of four channels, then m and l
+        f32x4 *const ro = reinterpret_cast<f32x4 *>(lds);
+        float *const rm = reinterpret_cast<float *>(lds + R * V * 4), *const rl = rm + R;
+        const int at = (w & (NW / 2 - 1)) * 32 + (lane & 31);
+        phase_barrier();  // all are done with the tiles
+        if (part == 1) {
+            st.each(lane, [&](int ch, f32x4 x) { ro[(ch >> 2) * R + at] = x; });
+            if (lane < 32) {
+                rm[at] = st.m;
+                rl[at] = l;
+            }
+        }
+        phase_barrier();
+        if (part == 1) return;
+        const float m = fmaxf(st.m, rm[at]);
+        const float f = m == -INFINITY ? 1.f : exp2f(st.m - m), g = m == -INFINITY ? 1.f : exp2f(rm[at] - m);
+        l = l * f + rl[at] * g;
+        if (wr0 + (lane & 31) >= all) return;
+        st.each(lane, [&](int ch, f32x4 x) {
+            store_out(a, start, kvh, static_cast<int>(row), ch, x * f + ro[(ch >> 2) * R + at] * g, l);
+        });
+        return;
+    }
     if (wr0 + (lane & 31) >= all) return;
-    const float l = swap32_sum(st.l);
     st.each(lane, [&](int ch, f32x4 x) { store_out(a, start, kvh, static_cast<int>(row), ch, x, l); });
 }
 
-template <int K, int V, int NW> hipError_t launch_bf16(const AttnArgs &a, hipStream_t st) {
-    const int64_t slots = static_cast<int64_t>(a.T) * a.G / (32 * NW) + a.N;
-    hipLaunchKernelGGL((attn_prompt_bf16_kernel<K, V, NW>), dim3(static_cast<unsigned>(slots * a.Hk)), dim3(64 * NW), 0, st, a,
+template <int K, int V, int NW, int PARTS> hipError_t launch_bf16(const AttnArgs &a, hipStream_t st) {
+    const int64_t slots = static_cast<int64_t>(a.T) * a.G / (32 * NW / PARTS) + a.N;
+    hipLaunchKernelGGL((attn_prompt_bf16_kernel<K, V, NW, PARTS>), dim3(static_cast<unsigned>(slots * a.Hk)), dim3(64 * NW), 0, st, a,
                        static_cast<int>(slots));
     return hipGetLastError();
 }
@@ -231,9 +270,23 @@ hipError_t launch_f32(const AttnArgs &a, hipStream_t st) {
     return hipGetLastError();
 }
 
+// Whether tiles of 128 rows, whose keys two halves of the workgroup share, are faster than tiles
+// of 256 rows. They halve what a workgroup walks, which is what a call takes whose tiles all run
+// at once, but each row's share of the copies is twice as large. `tiles`: about how many there
+// are of 128 rows, some of them cut short by the sequences' ends. Up to 9/8 to a compute unit
+// they were faster throughout (whole against halves, us, H = 8, Hk = 2, d = 128: 1 x 1000 30 and
+// 22, 1 x 3500 81 and 53, 4 x 1100 35 and 27; H = 32, Hk = 8: 1 x 65 10.9 and 9.5, 1 x 1100 36
+// and 26); up to two they were if the walks are long (H = 32: 1 x 1500 46 and 38, 1 x 2000 58
+// and 51; H = 8: 1 x 8000 181 and 140; but 16 x 300 18 and 25); beyond, they were slower (H =
+// 32: 1 x 3500 109 and 123, 4 x 1100 66 and 81).
+bool halves(const AttnArgs &a) {
+    const int64_t units = compute_units(), tiles = (static_cast<int64_t>(a.T) * a.G / 64 + a.N) * a.Hk / 2;
+    return 8 * tiles <= 9 * units || (tiles <= 2 * units && a.T >= static_cast<int64_t>(1024) * a.N);
+}
+
 template <int K, int V> hipError_t launch_dims(const AttnArgs &a, hipStream_t st) {
     if (a.in_dtype == KDA_F32) return launch_f32<K, V, 1>(a, st);
-    return launch_bf16<K, V, 8>(a, st);
+    return halves(a) ? launch_bf16<K, V, 8, 2>(a, st) : launch_bf16<K, V, 8, 1>(a, st);
 }
 
 }  // namespace

@@ -167,3 +167,86 @@ def test_writes_nothing_outside(dt):
     attn.kda_attn_fwd(q, k, v, ac.offsets([100, 31]), o=o)
     assert (buf[:4096] == 0xA5).all() and (buf[-4096:] == 0xA5).all()
     assert torch.equal(o, attn.kda_attn_fwd(q, k, v, ac.offsets([100, 31])))
+
+
+# Calls with enough rows for all compute units take larger tiles of rows; the small calls above share a
+# tile's keys between two halves of a workgroup. Some of the heads are compared.
+FULL = 600  # tokens that fill the card at 128 heads
+
+
+def some_heads(q, k, v, cut=None):
+    H, G = q.shape[1], q.shape[1] // k.shape[1]
+    h = torch.tensor(sorted({0, 1, H // 2 + 1, H - 1}), device="cuda")
+    return tuple(x[:cut].contiguous() for x in (q[:, h], k[:, h // G], v[:, h // G])) + (h,)
+
+
+def run_some(q, k, v, lens, scale, out="bf16"):
+    got = attn.kda_attn_fwd(q, k, v, ac.offsets(lens), scale=scale, out_dtype=DT[out])
+    *ref, h = some_heads(q, k, v)
+    o, lim = ac.prompt_reference(*ref, lens, scale, True, out == "bf16")
+    ac.check(f"o bf16->{out} {lens}", got[:, h], o, lim)
+    return got
+
+
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (128, 64), (64, 128)])
+@pytest.mark.parametrize("H,Hk", [(128, 32), (128, 128), (129, 3)])
+def test_full_card(dk, dv, H, Hk):
+    lens = [65, 1, 0, 64, 63, 129, 17, FULL - 339]
+    assert sum(lens) == FULL
+    run_some(*make(21, FULL, H, Hk, dk, dv, "bf16"), lens, dk ** -0.5)
+
+
+def test_full_card_one_sequence_fp32_out():
+    run_some(*make(22, FULL, 128, 16, 128, 128, "bf16"), [FULL], 0.09, out="f32")
+
+
+@pytest.mark.parametrize("T", [1030, 1537, 2047])
+def test_few_long_sequences(T):
+    run_some(*make(23, T, 32, 8, 128, 128, "bf16"), [T], 0.09)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
+def test_full_card_scales(scale):
+    run_some(*make(24, FULL, 128, 16, 64, 64, "bf16"), [200, FULL - 200], scale)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_full_card_tokens_not_seen_have_no_influence(bad):
+    lens = [100, 60, FULL - 160]
+    q, k, v = make(25, FULL, 128, 32, 128, 128, "bf16")
+    clean = run_some(q, k, v, lens, 0.09)
+    for spoil in (lambda: k[99].fill_(bad), lambda: v[99].fill_(bad)):
+        spoil()
+        got = attn.kda_attn_fwd(q, k, v, ac.offsets(lens), scale=0.09)
+        torch.cuda.synchronize()
+        *ref, h = some_heads(q, k, v, 99)
+        o, lim = ac.prompt_reference(*ref, [99], 0.09, True, True)
+        ac.check("rows before", got[:99, h], o, lim)
+        assert torch.equal(got[100:], clean[100:])
+        assert not torch.isfinite(got[99]).any()
+
+
+@pytest.mark.parametrize("H,Hk", [(4, 2), (128, 32)])
+def test_parts_of_wider_rows_at_the_end_of_memory(H, Hk):
+    """k and v end with the tensor's last token: nothing behind it is read (strided rows, all lengths of a
+    last tile's beginning)."""
+    T = FULL + 128 if H == 128 else 300
+    x = ac.normal(26, T, H + 2 * Hk, 64).bfloat16().cuda()
+    for end in (T, T - 63, T - 65, T - 128):
+        y = x[:end]
+        run_some(y[:, :H], y[:, H:H + Hk], y[:, H + Hk:], [end // 3, end - end // 3], 0.125)
+
+
+def test_nan_meets_both_halves():
+    """A NaN in one half's keys reaches every row that sees it, and no other."""
+    q, k, v = make(27, 300, 4, 2, 128, 128, "bf16")
+    clean = run(q, k, v, [300], 0.09, "bf16")
+    for at in (10, 70, 130, 200):
+        k2 = k.clone()
+        k2[at] = float("nan")
+        got = attn.kda_attn_fwd(q, k2, v, ac.offsets([300]), scale=0.09)
+        torch.cuda.synchronize()
+        ref, lim = ac.prompt_reference(q[:at], k[:at], v[:at], [at], 0.09, True, True)
+        ac.check("rows before", got[:at], ref, lim)
+        assert torch.isnan(got[at:]).all()
+    assert torch.equal(attn.kda_attn_fwd(q, k, v, ac.offsets([300]), scale=0.09), clean)
