@@ -12,7 +12,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import kda
-from .kda import KDA_OK, KDAError, _code, _dev, _one_device, _out, _ptr, _stream
+from .kda import KDA_ERR_WORKSPACE, KDA_OK, KDAError, _code, _dev, _one_device, _out, _ptr, _stream
 
 KDA_KV_F32, KDA_KV_BF16, KDA_KV_E4M3 = range(3)
 _KV_CODES = {torch.float32: KDA_KV_F32, torch.bfloat16: KDA_KV_BF16, torch.float8_e4m3fn: KDA_KV_E4M3}
@@ -282,5 +282,8 @@ def kda_attn_cache_fwd(q: torch.Tensor, cu_seqlens: torch.Tensor, cache_lens: to
                                     ctypes.byref(cache), _ptr(tree_mask), o.data_ptr(), _ptr(workspace),
                                     0 if workspace is None else workspace.numel() * workspace.element_size(), s)
     if st != KDA_OK:
-        raise KDAError(st, "kda_attn_cache_fwd")
+        where = "kda_attn_cache_fwd"
+        if st == KDA_ERR_WORKSPACE:
+            where += " (kda_attn_cache_fwd_workspace_size)"
+        raise KDAError(st, where)
     return o

@@ -52,10 +52,6 @@ hipError_t finish(hipError_t e, hipStream_t stream) {
 
 }  // namespace
 
-namespace kda {
-hipError_t finish_call(hipError_t e, hipStream_t stream) { return finish(e, stream); }
-}  // namespace kda
-
 namespace {
 
 // Options: neutral values when `opt` is NULL; otherwise checked against the
@@ -177,8 +173,8 @@ const char *kda_status_string(kda_status_t s) {
     switch (s) {
     case KDA_OK: return "KDA_OK: success";
     case KDA_ERR_INVALID_ARG: return "KDA_ERR_INVALID_ARG: NULL or misaligned pointer, or size out of range";
-    case KDA_ERR_UNSUPPORTED: return "KDA_ERR_UNSUPPORTED: head dims must be 64 or 128, chunk size 64, dtype pair F32/F32, BF16/BF16 or BF16/F32, a cache type that goes with them";
-    case KDA_ERR_WORKSPACE: return "KDA_ERR_WORKSPACE: workspace smaller than the entry point's workspace size";
+    case KDA_ERR_UNSUPPORTED: return "KDA_ERR_UNSUPPORTED: head dims must be 64 or 128, chunk size 64, dtype pair F32/F32, BF16/BF16 or BF16/F32";
+    case KDA_ERR_WORKSPACE: return "KDA_ERR_WORKSPACE: workspace smaller than kda_chunk_fwd_workspace_size()";
     case KDA_ERR_HIP: return "KDA_ERR_HIP: kernel launch failed";
     }
     return "unknown kda_status_t";

@@ -3,8 +3,11 @@
 // for kda.h. Reads no device memory, allocates nothing and never synchronises.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
+#include <cstring>
 
 #include "kda_attn.h"
 #include "kda_attn_internal.h"
@@ -49,6 +52,18 @@ kda_status_t check_cache(const kda_kv_cache_t *c, int32_t N) {
     return KDA_OK;
 }
 
+// A call's end: its launch status and, with KDA_DEBUG_SYNC=1 (read once per process), that of
+// its work on `stream`.
+hipError_t finish(hipError_t e, hipStream_t stream) {
+    static const bool wait = [] {
+        const char *x = std::getenv("KDA_DEBUG_SYNC");
+        return x && std::strcmp(x, "1") == 0;
+    }();
+    if (e == hipSuccess && wait) e = hipStreamSynchronize(stream);
+    if (e == hipSuccess && wait) e = hipGetLastError();
+    return e;
+}
+
 // scale in the log2 domain has to be finite too
 constexpr double kLog2e = 1.4426950408889634;
 bool scale_ok(float s) { return std::isfinite(static_cast<float>(s * kLog2e)); }
@@ -79,10 +94,25 @@ kda_status_t kv_call(bool write, void *k, void *v, const int32_t *cu_seqlens, in
     a.page_shift = log2_of(cache->page_size); a.max_pages = cache->max_pages; a.num_pages = cache->num_pages;
     a.dtype = dtype; a.kv_dtype = cache->dtype;
     const hipError_t e = write ? kda::launch_kv_write(a, stream) : kda::launch_kv_read(a, stream);
-    return kda::finish_call(e, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+    return finish(e, stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
 }  // namespace
+
+namespace kda {
+
+// threads that race on a device's first query store the same value
+int compute_units() {
+    static std::atomic<int> known[64];
+    int dev = 0, n = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+    if ((n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 1) n = 256;
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+}  // namespace kda
 
 extern "C" {
 
@@ -102,7 +132,7 @@ kda_status_t kda_attn_fwd(const void *q, const void *k, const void *v, const int
     a.cu = cu_seqlens; a.o = o; a.N = N; a.T = T_total; a.H = H; a.Hk = Hk; a.G = H / Hk; a.K = d_k; a.V = d_v;
     a.c = static_cast<float>(scale * kLog2e);
     a.in_dtype = in_dtype; a.out_dtype = out_dtype;
-    return kda::finish_call(kda::launch_attn_prompt(a, stream), stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+    return finish(kda::launch_attn_prompt(a, stream), stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
 kda_status_t kda_kv_write(const void *k, const void *v, const int32_t *cu_seqlens, int32_t N, int32_t T_total,
@@ -151,7 +181,7 @@ kda_status_t kda_attn_cache_fwd(const void *q, const int32_t *cu_seqlens, int32_
     a.page_shift = log2_of(cache->page_size); a.max_pages = cache->max_pages; a.num_pages = cache->num_pages;
     a.c = static_cast<float>(scale * kLog2e);
     a.in_dtype = in_dtype; a.out_dtype = out_dtype; a.kv_dtype = cache->dtype;
-    return kda::finish_call(kda::launch_attn_cache(a, stream), stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+    return finish(kda::launch_attn_cache(a, stream), stream) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
 }
 
 }  // extern "C"

@@ -46,6 +46,9 @@ struct KvArgs {
     kda_kv_dtype_t kv_dtype;
 };
 
+// Compute units of the current device (cached per device).
+int compute_units();
+
 // Each launcher enqueues its kernel(s) on `stream` and returns the launch status.
 hipError_t launch_attn_prompt(const AttnArgs &a, hipStream_t stream);
 hipError_t launch_attn_cache(const AttnArgs &a, hipStream_t stream);

@@ -65,12 +65,6 @@ hipError_t launch_prefill_mfma(const PrefillArgs &a, hipStream_t stream);
 // o <- epilogue(o) in place, per (token, head) row (the fp32-path epilogue)
 hipError_t launch_epilogue(const PrefillArgs &a, hipStream_t stream);
 
-// Compute units of the current device (cached per device).
-int compute_units();
-
-// A call's end: its launch status and, with KDA_DEBUG_SYNC=1, that of its work on `stream`.
-hipError_t finish_call(hipError_t e, hipStream_t stream);
-
 // Workspace bytes of the matrix-core prefill (0 for d_k/d_v it cannot run).
 size_t prefill_mfma_workspace(int32_t N, int32_t T, int32_t H, int32_t K, int32_t V);
 // workspace of the fp32 vector-ALU path: one fp32 record per (chunk slot, head)

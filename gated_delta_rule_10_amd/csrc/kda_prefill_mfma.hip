@@ -1868,8 +1868,6 @@ void *noalloc_scratch() {
     return p;
 }
 
-int compute_units() { return cu_count(); }
-
 size_t prefill_mfma_workspace(int32_t N, int32_t T, int32_t H, int32_t K, int32_t V) {
     if (K == 128 && V == 128) return WsLayout<128, 128>(N, T, H).bytes;
     if (K == 128 && V == 64) return WsLayout<128, 64>(N, T, H).bytes;

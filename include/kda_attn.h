@@ -26,7 +26,10 @@
  * and never synchronises; all work is enqueued on `stream` and can be captured
  * in a HIP graph; arguments are checked on the host before anything is
  * enqueued. Status codes, types, kda_status_string and KDA_DEBUG_SYNC are
- * kda.h's.
+ * kda.h's; the texts name the limits of kda.h. Here KDA_ERR_UNSUPPORTED is also
+ * a page size or a pair of input and cache types that there is no kernel for,
+ * and KDA_ERR_WORKSPACE a workspace smaller than
+ * kda_attn_cache_fwd_workspace_size().
  *  - H is the number of query heads, Hk the number of key/value heads; H is a
  *    multiple of Hk, and query head h uses kv head h / (H / Hk).
  *  - d_k and d_v are 64 or 128, each on its own.
