@@ -34,6 +34,16 @@ bool sizes_ok(int32_t N, int32_t T, int32_t H, int32_t Hk) {
     return static_cast<int64_t>(N) * H * 16 <= INT32_MAX;  // grids, with one tile more per sequence and head
 }
 
+// A launch has to stay below 2^32 threads. Prompts: tiles of 256 rows and 512 threads (fp32: 16 and
+// 256), one more tile per sequence and kv head. Cache attention: the join's 512 threads per 16 rows
+// of tiles of up to 128. Cache writes and reads: 4 threads to a row, 64 rows to a workgroup.
+bool below(int64_t x, int bits) { return x < int64_t(1) << bits; }
+bool prompt_ok(int64_t N, int64_t T, int64_t H, int64_t Hk, kda_dtype_t in) {
+    return in == KDA_F32 ? below(T * H + 16 * N * Hk, 28) : below(T * H + 256 * N * Hk, 31);
+}
+bool cache_ok(int64_t N, int64_t T, int64_t H, int64_t Hk) { return below(T * H + 128 * N * Hk, 27); }
+bool kv_ok(int64_t T, int64_t Hk) { return below(T * Hk + 64, 30); }
+
 // The cache of a call over N sequences of Hk kv heads, without its type pair.
 kda_status_t check_cache(const kda_kv_cache_t *c, int32_t N) {
     if (!c || !kv_dtype_valid(c->dtype)) return KDA_ERR_INVALID_ARG;
@@ -77,7 +87,7 @@ int32_t log2_of(int32_t x) {
 kda_status_t kv_call(bool write, void *k, void *v, const int32_t *cu_seqlens, int32_t N, int32_t T_total, int32_t Hk,
                      int32_t d_k, int32_t d_v, int64_t k_stride, int64_t v_stride, kda_dtype_t dtype,
                      const kda_kv_cache_t *cache, hipStream_t stream) {
-    if (!sizes_ok(N, T_total, Hk, Hk) || !dtype_valid(dtype) || !given(cu_seqlens)) return KDA_ERR_INVALID_ARG;
+    if (!sizes_ok(N, T_total, Hk, Hk) || !kv_ok(T_total, Hk) || !dtype_valid(dtype) || !given(cu_seqlens)) return KDA_ERR_INVALID_ARG;
     const kda_status_t cs = check_cache(cache, N);
     if (cs != KDA_OK) return cs;
     if (T_total > 0 && (!given(k) || !given(v))) return KDA_ERR_INVALID_ARG;
@@ -121,6 +131,7 @@ kda_status_t kda_attn_fwd(const void *q, const void *k, const void *v, const int
                           int64_t k_stride, int64_t v_stride, kda_dtype_t in_dtype, kda_dtype_t out_dtype,
                           float scale, void *o, hipStream_t stream) {
     if (!sizes_ok(N, T_total, H, Hk) || !dtype_valid(in_dtype) || !dtype_valid(out_dtype)) return KDA_ERR_INVALID_ARG;
+    if (!prompt_ok(N, T_total, H, Hk, in_dtype)) return KDA_ERR_INVALID_ARG;
     if (!given(cu_seqlens) || !scale_ok(scale)) return KDA_ERR_INVALID_ARG;
     if (T_total > 0 && (!given(q) || !given(k) || !given(v) || !given(o))) return KDA_ERR_INVALID_ARG;
     if (!head_dim_ok(d_k) || !head_dim_ok(d_v) || !dtype_pair_ok(in_dtype, out_dtype)) return KDA_ERR_UNSUPPORTED;
@@ -151,7 +162,7 @@ kda_status_t kda_kv_read(void *k, void *v, const int32_t *cu_seqlens, int32_t N,
 
 size_t kda_attn_cache_fwd_workspace_size(int32_t N, int32_t T_total, int32_t H, int32_t Hk, int32_t d_k, int32_t d_v,
                                          int32_t max_tokens, kda_dtype_t in_dtype) {
-    if (!sizes_ok(N, T_total, H, Hk) || !head_dim_ok(d_k) || !head_dim_ok(d_v) || !dtype_valid(in_dtype)) return 0;
+    if (!sizes_ok(N, T_total, H, Hk) || !cache_ok(N, T_total, H, Hk) || !head_dim_ok(d_k) || !head_dim_ok(d_v) || !dtype_valid(in_dtype)) return 0;
     if (T_total == 0 || max_tokens < 1) return 0;
     return kda::attn_cache_workspace(N, T_total, H, Hk, d_v, max_tokens, in_dtype);
 }
@@ -162,6 +173,7 @@ kda_status_t kda_attn_cache_fwd(const void *q, const int32_t *cu_seqlens, int32_
                                 const uint64_t *tree_mask, void *o, void *workspace, size_t workspace_bytes,
                                 hipStream_t stream) {
     if (!sizes_ok(N, T_total, H, Hk) || !dtype_valid(in_dtype) || !dtype_valid(out_dtype)) return KDA_ERR_INVALID_ARG;
+    if (!cache_ok(N, T_total, H, Hk)) return KDA_ERR_INVALID_ARG;
     if (!given(cu_seqlens) || !scale_ok(scale)) return KDA_ERR_INVALID_ARG;
     const kda_status_t cs = check_cache(cache, N);
     if (cs != KDA_OK) return cs;

@@ -96,7 +96,9 @@ typedef struct {
  *   q  [T_total, H, d_k]   k  [T_total, Hk, d_k]   v  [T_total, Hk, d_v]   in_dtype
  *   o  [T_total, H, d_v]   out_dtype output (dense)
  *
- * Sizes: N >= 1, H >= 1, T_total >= 0, T_total H < 2^31 - 1024, 16 N H < 2^31.
+ * Sizes: N >= 1, H >= 1, T_total >= 0, 16 N H < 2^31, and, as a launch holds less
+ * than 2^32 threads, T_total H + 256 N Hk < 2^31 (F32 inputs: T_total H + 16 N Hk <
+ * 2^28); T_total H < 2^31 - 1024.
  * dtype pairs: (F32, F32), (BF16, BF16), (BF16, F32).
  * `scale` is finite (1 / sqrt(d_k) is customary).
  */
@@ -116,6 +118,8 @@ kda_status_t kda_attn_fwd(const void *q, const void *k, const void *v, const int
  * for that one rounding. An infinity or NaN becomes a NaN. Pages may be shared
  * by sequences, but a place that the call writes must be one position of one
  * sequence.
+ * Sizes, here and for kda_kv_read: N >= 1, Hk >= 1, T_total >= 0, 16 N Hk < 2^31,
+ * T_total Hk < 2^30 - 64.
  */
 kda_status_t kda_kv_write(const void *k, const void *v, const int32_t *cu_seqlens, int32_t N, int32_t T_total,
                           int32_t Hk, int32_t d_k, int32_t d_v, int64_t k_stride, int64_t v_stride,
@@ -146,8 +150,8 @@ kda_status_t kda_kv_read(void *k, void *v, const int32_t *cu_seqlens, int32_t N,
  *   q  [T_total, H, d_k]  in_dtype    o  [T_total, H, d_v]  out_dtype output (dense)
  *
  * dtype pairs as for kda_attn_fwd; F32 inputs with an F32 cache, BF16 inputs
- * with a BF16 or E4M3 one. Sizes as for kda_attn_fwd, N max_pages < 2^31,
- * max_pages page_size < 2^31 - 1024.
+ * with a BF16 or E4M3 one. Sizes: N >= 1, H >= 1, T_total >= 0, 16 N H < 2^31,
+ * T_total H + 128 N Hk < 2^27, N max_pages < 2^31, max_pages page_size < 2^31 - 1024.
  * workspace: kda_attn_cache_fwd_workspace_size bytes of device scratch, whatever
  * they hold (NULL if that is 0). Calls that may overlap must not share one.
  */

@@ -71,6 +71,8 @@ SIZES = [(dict(N=0), INVALID), (dict(T=-1), INVALID), (dict(T=2 ** 31 - 1024), I
     (dict(H=0), INVALID), (dict(Hk=0), INVALID), (dict(H=7), INVALID),               # 7 heads over 2 kv heads
     (dict(T=2 ** 28, H=8), INVALID),                                                 # T H past int32
     (dict(N=2 ** 27, H=8), INVALID),
+    (dict(N=2 ** 22, Hk=2), INVALID),                                                # launches of 2^32 threads
+    (dict(T=2 ** 25, din=kda.KDA_F32, dout=kda.KDA_F32), INVALID),
     (dict(qs=1016), INVALID), (dict(ks=255), INVALID), (dict(vs=260), INVALID),      # too short, not a multiple of 8
     (dict(din=7), INVALID), (dict(dout=7), INVALID),
     (dict(din=kda.KDA_F32, dout=kda.KDA_BF16), UNSUPPORTED),
@@ -137,6 +139,7 @@ def test_kv_write_rejects(lib, over, status):
 
 @pytest.mark.parametrize("over,status", SIZES + CACHES + [
     (dict(k=None), INVALID), (dict(v=A + 4), INVALID), (dict(c_dtype=attn.KDA_KV_F32), UNSUPPORTED),
+    (dict(T=2 ** 29 - 32), INVALID),                                                 # a launch of 2^32 threads
 ])
 def test_kv_read_rejects(lib, over, status):
     assert _kv(lib, lib.kda_kv_read, **over) == status
@@ -145,6 +148,7 @@ def test_kv_read_rejects(lib, over, status):
 @pytest.mark.parametrize("over,status", SIZES + CACHES + [
     (dict(q=None), INVALID), (dict(o=A + 2), INVALID), (dict(mask=A + 8), INVALID), (dict(H=3), INVALID),
     (dict(qs=1020), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(T=2 ** 24), INVALID), (dict(N=2 ** 19), INVALID),                          # launches of 2^32 threads
     (dict(c_dtype=attn.KDA_KV_F32), UNSUPPORTED), (dict(din=kda.KDA_F32, dout=kda.KDA_F32), UNSUPPORTED),
     (dict(c_max_pages=40, ws=None), kda.KDA_ERR_WORKSPACE), (dict(ws=A + 8), INVALID),
     (dict(c_max_pages=40, wsb=1000), kda.KDA_ERR_WORKSPACE),
