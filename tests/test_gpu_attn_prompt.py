@@ -250,3 +250,31 @@ def test_nan_meets_both_halves():
         ac.check("rows before", got[:at], ref, lim)
         assert torch.isnan(got[at:]).all()
     assert torch.equal(attn.kda_attn_fwd(q, k, v, ac.offsets([300]), scale=0.09), clean)
+
+
+@pytest.mark.parametrize("H,Hk,T", [(4, 2, 300), (128, 32, FULL)])
+def test_another_stream_and_capture(H, Hk, T):
+    """The same bits on another stream, and from a graph replayed between eager calls with other inputs."""
+    cu = ac.offsets([T // 3, T - T // 3])
+    sets = [make(31 + 3 * i, T, H, Hk, 128, 128, "bf16") for i in range(3)]
+    eager = [attn.kda_attn_fwd(*s, cu, scale=0.09) for s in sets]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    got = attn.kda_attn_fwd(*sets[0], cu, scale=0.09, stream=stream)
+    stream.synchronize()
+    assert torch.equal(got, eager[0])
+    held = tuple(x.clone() for x in sets[0])
+    with torch.cuda.stream(stream):
+        attn.kda_attn_fwd(*held, cu, scale=0.09)
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            out = attn.kda_attn_fwd(*held, cu, scale=0.09)
+        for i in (1, 2, 0, 1):
+            for to, x in zip(held, sets[i]):
+                to.copy_(x)
+            graph.replay()
+            stream.synchronize()
+            assert torch.equal(out, eager[i])
+            assert torch.equal(attn.kda_attn_fwd(*sets[i], cu, scale=0.09), eager[i])
+            stream.synchronize()
