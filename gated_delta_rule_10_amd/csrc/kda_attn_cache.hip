@@ -431,8 +431,13 @@ template <int K, int V, typename TC> struct Tiles {
             const u32x4 w = *reinterpret_cast<const u32x4 *>(raw + 16 * e);
             // the conversion takes a scale's exponent bits
             const float scale = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint8_t *>(exps + t)) << 23);
-            *reinterpret_cast<bf16x8 *>(to + t * (2 * D) + 16 * ((2 * c) ^ sw)) = codes_to_bf16(w[0], w[1], scale);
-            *reinterpret_cast<bf16x8 *>(to + t * (2 * D) + 16 * ((2 * c + 1) ^ sw)) = codes_to_bf16(w[2], w[3], scale);
+            // which of the two is written first: the chunks of eight lanes then lie in different banks
+            // (107 against 109 us for the trees above)
+            const int f = (D == 128 ? (c >> 2) ^ (KEYS ? 0 : t) : t) & 1;
+            const bf16x8 x = codes_to_bf16(f ? w[2] : w[0], f ? w[3] : w[1], scale);
+            const bf16x8 y = codes_to_bf16(f ? w[0] : w[2], f ? w[1] : w[3], scale);
+            *reinterpret_cast<bf16x8 *>(to + t * (2 * D) + 16 * ((2 * c + f) ^ sw)) = x;
+            *reinterpret_cast<bf16x8 *>(to + t * (2 * D) + 16 * ((2 * c + 1 - f) ^ sw)) = y;
         }
     }
 };
