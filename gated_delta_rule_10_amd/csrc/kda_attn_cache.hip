@@ -22,7 +22,7 @@
 // tokens, H = 32, Hk = 8, d = 128: a bf16 cache of 1.37 GB in 247 us (5.55 TB/s; a copy
 // reaches 4.9), an e4m3 one of 0.69 GB in 140 us (4.93 TB/s). One sequence of 524288
 // tokens: 2.15 GB in 367 us (5.85 TB/s), 8 us of them the join. 24 drafted tokens for
-// each of 16 sequences of 500 to 20000 tokens, e4m3: 105 us (2.45 TB/s, 450 TFLOP/s).
+// each of 16 sequences of 500 to 20000 tokens, e4m3: 106 us (2.43 TB/s, 450 TFLOP/s).
 #include "kda_attn_stream.h"
 
 namespace kda {
