@@ -31,12 +31,12 @@ __device__ __forceinline__ uint32_t lds_address(const char *p) {
     return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) char *)p));
 }
 
-// One instruction, where fmaxf of two would first make quiet NaNs of its operands. A NaN
-// operand is passed over, as by fmaxf.
+// The largest of three, a NaN passed over: one instruction, where fmaxf of two would first make
+// quiet NaNs of its operands. Not as inline assembly: it is the first to read the products'
+// results, and the compiler leaves the wait states that these need only before instructions that
+// it knows.
 __device__ __forceinline__ float max3(float x, float y, float z) {
-    float r;
-    __asm__("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(y), "v"(z));
-    return r;
+    return __builtin_elementwise_maximumnum(__builtin_elementwise_maximumnum(x, y), z);
 }
 
 // A workgroup barrier that nothing is moved across, without waiting for copies.
