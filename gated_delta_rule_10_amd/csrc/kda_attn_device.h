@@ -95,16 +95,15 @@ __device__ __forceinline__ float swap32_sum(float m) {
     return __uint_as_float(p[0]) + __uint_as_float(p[1]);
 }
 
-// A register of elements holds an infinity or a NaN (e4m3: a NaN).
-template <typename TC> __device__ __forceinline__ bool not_finite(uint32_t x);
-template <> __device__ __forceinline__ bool not_finite<float>(uint32_t x) { return (x & 0x7F800000u) == 0x7F800000u; }
-template <> __device__ __forceinline__ bool not_finite<bf16_t>(uint32_t x) {
-    return (x & 0x7F800000u) == 0x7F800000u || (x & 0x7F80u) == 0x7F80u;
-}
-template <> __device__ __forceinline__ bool not_finite<e4m3_t>(uint32_t x) {
+// Not 0 if a register of elements holds an infinity or a NaN (e4m3: a NaN).
+template <typename TC> __device__ __forceinline__ uint32_t not_finite(uint32_t x);
+// an exponent of ones carries into the sign's place, no other does
+template <> __device__ __forceinline__ uint32_t not_finite<float>(uint32_t x) { return ((x & 0x7F800000u) + 0x00800000u) & 0x80000000u; }
+template <> __device__ __forceinline__ uint32_t not_finite<bf16_t>(uint32_t x) { return ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
+template <> __device__ __forceinline__ uint32_t not_finite<e4m3_t>(uint32_t x) {
     // a byte whose low seven bits are all ones: no borrow from the byte above
     const uint32_t y = ~x & 0x7F7F7F7Fu;
-    return ((y - 0x01010101u) & 0x80808080u & ~y) != 0;
+    return (y - 0x01010101u) & 0x80808080u & ~y;
 }
 
 __device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }

@@ -78,3 +78,49 @@ def test_scores_whose_sums_cancel_late_in_prompts(sign, d, heads, kv_heads, T):
     g = h // (heads // kv_heads)
     ref, lim = ac.prompt_reference(q[:, h].contiguous(), k[:, g].contiguous(), v[:, g].contiguous(), [T], 1.0, True, True)
     ac.check(f"{sign} {d}", got[:, h], ref, lim)
+
+
+def check_values(name, got, ref, lim):
+    """ac.check, and every infinity and NaN in its place."""
+    g = got.double().cpu()
+    odd = ~torch.isfinite(ref)
+    assert torch.equal(torch.nan_to_num(g[odd], nan=1.0), torch.nan_to_num(ref[odd], nan=1.0)), f"{name}: other infinities or NaN"
+    ac.check(name, got, ref, lim)
+
+
+def infinities(v, at, other):
+    """Infinities of both signs in some channels of token `at` of v [T, heads, d], and of token `other`."""
+    inf = float("inf")
+    v[at, :, 3], v[at, :, 20], v[at, 0, 41:44] = inf, -inf, inf
+    v[other, :, 20], v[other, 1, 50] = inf, -inf      # channel 20: NaN for the rows that see both
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("heads", [4, 20])
+@pytest.mark.parametrize("ctx", [100, 1500])
+def test_infinite_values_that_a_row_sees(dt, heads, ctx):
+    """Infinities in v reach the rows that see them as infinities, early in the cache and among the new tokens,
+    with 4 and 20 rows for a kv head."""
+    bf, dtype = dt == "bf16", torch.bfloat16 if dt == "bf16" else torch.float32
+    q = ac.normal(50, 2, heads, 64).to(dtype).cuda()
+    for at, other in ((0, ctx + 1), (37, 5), (ctx // 2, ctx // 2 + 20), (ctx - 1, 2), (ctx + 1, 64)):
+        k, v = ac.normal(51, ctx + 2, 2, 64), ac.normal(52, ctx + 2, 2, 64)
+        infinities(v, at, other)
+        c = held(53, [ctx + 2], k, v, 64, dt)
+        ref, lim = ac.cache_reference(q, c, [2], None, 0.125, bf, bf)
+        check_values(f"{dt} {ctx} {at}", call(q, [2], c, None, 0.125, dt), ref, lim)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("heads,kv_heads,T", [(4, 2, 300), (128, 32, 600)])
+@pytest.mark.parametrize("at,other", [(0, 299), (130, 30), (200, 199)])
+def test_infinite_values_that_a_row_sees_in_prompts(dt, heads, kv_heads, T, at, other):
+    bf, dtype = dt == "bf16", torch.bfloat16 if dt == "bf16" else torch.float32
+    v = ac.normal(56, T, kv_heads, 64)
+    infinities(v, at, other)
+    q, k, v = (x.to(dtype).cuda() for x in (ac.normal(54, T, heads, 64), ac.normal(55, T, kv_heads, 64), v))
+    got = attn.kda_attn_fwd(q, k, v, ac.offsets([T]), scale=0.125)
+    h = torch.tensor([0, heads // kv_heads, heads - 1], device="cuda")
+    g = h // (heads // kv_heads)
+    ref, lim = ac.prompt_reference(q[:, h].contiguous(), k[:, g].contiguous(), v[:, g].contiguous(), [T], 0.125, bf, bf)
+    check_values(f"{dt} {at}", got[:, h], ref, lim)
