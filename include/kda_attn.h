@@ -49,6 +49,12 @@
  *    sequence times H / Hk) they keep 16 bits. E4M3 codes are multiplied as
  *    exact bf16 numbers, but below bf16's least normal one (2^-126) and above
  *    its largest (infinity). Results do not depend on timing: no atomics.
+ *  - Range: outputs are summed before they are divided, with weights of up to
+ *    2^8, so finite values of v have to stay below 2^120 / (tokens that a row
+ *    sees) in magnitude; larger ones may give infinities or NaN. Down to 2^-100
+ *    they keep the accuracy above; below it, the smallest weights are lost. An
+ *    infinity in v is one in the rows that see it, but may be NaN where its
+ *    weight is below 2^-126.
  *  - cu_seqlens, lens, page_table and tree_mask must not change while a call
  *    that reads them runs.
  */

@@ -124,3 +124,42 @@ def test_infinite_values_that_a_row_sees_in_prompts(dt, heads, kv_heads, T, at, 
     g = h // (heads // kv_heads)
     ref, lim = ac.prompt_reference(q[:, h].contiguous(), k[:, g].contiguous(), v[:, g].contiguous(), [T], 0.125, bf, bf)
     check_values(f"{dt} {at}", got[:, h], ref, lim)
+
+
+@pytest.mark.parametrize("dt,kv", [("bf16", "bf16"), ("bf16", "e4m3"), ("f32", "f32")])
+@pytest.mark.parametrize("heads", [4, 20])
+@pytest.mark.parametrize("ctx", [6, 300, 1700])
+@pytest.mark.parametrize("size", ["large", "small"])
+def test_values_at_the_ends_of_the_range(dt, kv, heads, ctx, size):
+    """Values of one sign just below 2^120 / tokens, and about 2^-100, under scores that rise slowly, so that
+    weights reach 2^8 of the reference that they are taken from."""
+    bf, T = dt == "bf16", ctx + 2
+    f = 2.0 ** 119 / T if size == "large" else 2.0 ** -100
+    k, v = 0.1 * ac.normal(60, T, 2, 64), f * (1 + 0.5 * torch.rand(T, 2, 64, generator=torch.Generator().manual_seed(60)))
+    k[:, :, 0] = 0.011 * torch.arange(T)[:, None]
+    q = 0.1 * ac.normal(61, 2, heads, 64)
+    q[:, :, 0] = 1
+    c = ac.Cache([T], 2, 64, 64, 64, kv, seed=62)
+    c.put(0, k, v)
+    q = q.to(torch.bfloat16 if bf else torch.float32).cuda()
+    ref, lim = ac.cache_reference(q, c, [2], None, 1.0, bf, bf)
+    assert torch.isfinite(ref).all()
+    ac.check(f"{size} {dt}/{kv} {heads} {ctx}", call(q, [2], c, None, 1.0, dt), ref, lim)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("heads,kv_heads,T", [(4, 2, 300), (128, 32, 600)])
+@pytest.mark.parametrize("size", ["large", "small"])
+def test_values_at_the_ends_of_the_range_in_prompts(dt, heads, kv_heads, T, size):
+    bf, dtype = dt == "bf16", torch.bfloat16 if dt == "bf16" else torch.float32
+    f = 2.0 ** 119 / T if size == "large" else 2.0 ** -100
+    k, v = 0.1 * ac.normal(63, T, kv_heads, 64), f * (1 + 0.5 * torch.rand(T, kv_heads, 64, generator=torch.Generator().manual_seed(63)))
+    k[:, :, 0] = 0.03 * torch.arange(T)[:, None]
+    q = 0.1 * ac.normal(64, T, heads, 64)
+    q[:, :, 0] = 1
+    q, k, v = (x.to(dtype).cuda() for x in (q, k, v))
+    got = attn.kda_attn_fwd(q, k, v, ac.offsets([T]), scale=1.0)
+    h = torch.tensor([0, heads - 1], device="cuda")
+    g = h // (heads // kv_heads)
+    ref, lim = ac.prompt_reference(q[:, h].contiguous(), k[:, g].contiguous(), v[:, g].contiguous(), [T], 1.0, bf, bf)
+    ac.check(f"{size} {dt}", got[:, h], ref, lim)
