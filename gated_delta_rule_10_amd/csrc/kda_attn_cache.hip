@@ -278,8 +278,8 @@ __global__ __launch_bounds__(64 * kWaves, kPerCu) void attn_cache_kernel(AttnArg
         }
         __syncthreads();  // the join takes the waves' LDS
         if (whole) {
-            st.join(lds, stat, w, lane, rows, [&](int row, int ch, float, f32x4 x, float l) {
-                store_out(a, q.start, kvh, r0 + row, ch, x, l);
+            st.join(lds, stat, w, lane, rows, [&](int row, int ch, float m, f32x4 x, float l) {
+                store_out(a, q.start, kvh, r0 + row, ch, m, x, l);
             });
         } else {
             float *part = reinterpret_cast<float *>(static_cast<char *>(a.ws) + prefix_bytes(a.N)) +
@@ -366,7 +366,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
             }
             __syncthreads();
         }
-        if (sub == 0 && rr < rows) store_out(a, q.start, kvh, static_cast<int>(r0) + rr, 4 * c, x, l);
+        if (sub == 0 && rr < rows) store_out(a, q.start, kvh, static_cast<int>(r0) + rr, 4 * c, m, x, l);
     }
 }
 
@@ -546,7 +546,7 @@ __global__ __launch_bounds__(256, 2) void attn_cache_rows_kernel(AttnArgs a) {
         if (32 * w + (lane & 31) < rows) {
             const float l = swap32_sum(st.l);
             if (whole) {
-                st.each(lane, [&](int ch, f32x4 x) { store_out(a, q.start, kvh, r, ch, x, l); });
+                st.each(lane, [&](int ch, f32x4 x) { store_out(a, q.start, kvh, r, ch, st.m, x, l); });
             } else {
                 float *part = reinterpret_cast<float *>(static_cast<char *>(a.ws) + prefix_bytes(a.N)) +
                               (2 * static_cast<size_t>(blockIdx.x) + (first ? 0 : 1)) * part_floats(R, V);

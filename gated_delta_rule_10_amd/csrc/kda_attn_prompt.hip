@@ -49,8 +49,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a,
         __builtin_amdgcn_wave_barrier();
     }
     __syncthreads();
-    st.join(lds, stat, w, lane, rows, [&](int row, int ch, float, f32x4 x, float l) {
-        store_out(a, start, kvh, r0 + row, ch, x, l);
+    st.join(lds, stat, w, lane, rows, [&](int row, int ch, float m, f32x4 x, float l) {
+        store_out(a, start, kvh, r0 + row, ch, m, x, l);
     });
 }
 
@@ -247,12 +247,12 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
         l = l * f + rl[at] * g;
         if (wr0 + (lane & 31) >= all) return;
         st.each(lane, [&](int ch, f32x4 x) {
-            store_out(a, start, kvh, static_cast<int>(row), ch, x * f + ro[(ch >> 2) * R + at] * g, l);
+            store_out(a, start, kvh, static_cast<int>(row), ch, m, x * f + ro[(ch >> 2) * R + at] * g, l);
         });
         return;
     }
     if (wr0 + (lane & 31) >= all) return;
-    st.each(lane, [&](int ch, f32x4 x) { store_out(a, start, kvh, static_cast<int>(row), ch, x, l); });
+    st.each(lane, [&](int ch, f32x4 x) { store_out(a, start, kvh, static_cast<int>(row), ch, st.m, x, l); });
 }
 
 template <int K, int V, int NW, int PARTS> hipError_t launch_bf16(const AttnArgs &a, hipStream_t st) {

@@ -48,6 +48,11 @@ __device__ __forceinline__ void phase_barrier() {
 
 constexpr int kTile = 64;  // tokens per tile
 
+// A row's running maximum is -infinity until the row has seen a token, and at least this from then
+// on, also if the scores are -infinity or NaN: a row that sees no token is 0, one whose scores are
+// all -infinity is 0 / 0.
+constexpr float kLowest = -3.402823466e38f;
+
 template <int K, int V> struct Rows {
     static constexpr int CK = K / 8, CV = V / 8;  // 16-byte chunks per row
     static constexpr int KB = kTile * K * 2, VB = kTile * V * 2;
@@ -128,10 +133,12 @@ template <int K, int V> struct Rows {
     // 2^(c s - m) in bf16, the running maximum and sum (c >= 0: q carries the scale's sign);
     // `sees`: a bit for each of the lane's 32 tokens that its row sees, used if MASKED
     template <bool MASKED> __device__ __forceinline__ void softmax(float c, uint32_t sees) {
+        // all ones where the lane's token i is seen
+        auto seen = [&](int i) { return static_cast<uint32_t>(static_cast<int32_t>(sees << (31 - i)) >> 31); };
         if (MASKED) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-                if (!((sees >> i) & 1u)) s[i >> 4][i & 15] = -INFINITY;
+                s[i >> 4][i & 15] = __uint_as_float((__float_as_uint(s[i >> 4][i & 15]) & seen(i)) | (0xFF800000u & ~seen(i)));
         }
         float t = max3(s[0][0], s[1][0], s[0][1]), u = max3(s[1][1], s[0][2], s[1][2]);
 #pragma unroll
@@ -140,8 +147,9 @@ template <int K, int V> struct Rows {
             u = max3(u, s[0][i + 1], s[1][i + 1]);
         }
         t = max3(t, s[0][15], s[1][15]);
-        t = swap32_max(fmaxf(t, u));
-        t = t == -INFINITY ? t : t * c;  // a scale of 0 leaves "nothing seen" as it is
+        t = fmaxf(fmaxf(t, u) * c, kLowest);
+        if (MASKED) t = sees ? t : -INFINITY;
+        t = swap32_max(t);
         // m only has to keep the powers in range: it moves when the tile passes it by more than 2^8
         if (__any(t > m + 8.f)) {
             const float mn = fmaxf(m, t);
@@ -157,9 +165,9 @@ template <int K, int V> struct Rows {
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                // with a scale of 0, -infinity would be 0 * infinity
-                const float x = MASKED && s[b][i] == -INFINITY ? -INFINITY : fmaf(s[b][i], c, -ref);
-                s[b][i] = __builtin_amdgcn_exp2f(x);
+                s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], c, -ref));
+                // not left to the exponential: with a scale of 0, -infinity is 0 * infinity
+                if (MASKED) s[b][i] = __uint_as_float(__float_as_uint(s[b][i]) & seen(16 * b + i));
                 sum[i & 1] += s[b][i];
             }
         l += sum[0] + sum[1];
@@ -265,14 +273,12 @@ template <int K, int V> struct Rows {
     }
 };
 
-// o of one row: channels ch .. ch + 3 of row r of a tile
-__device__ __forceinline__ void store_out(const AttnArgs &a, int start, int kvh, int r, int ch, f32x4 x, float l) {
+// o of one row: channels ch .. ch + 3 of row r of a tile, from its maximum, unnormalised outputs and sum
+__device__ __forceinline__ void store_out(const AttnArgs &a, int start, int kvh, int r, int ch, float m, f32x4 x, float l) {
     const int tok = r / a.G, h = kvh * a.G + (r - tok * a.G);
     const int64_t at = (static_cast<int64_t>(start + tok) * a.H + h) * a.V + ch;
-    // l is 0 only where nothing was seen
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if (l == 0.f) x = (f32x4){0.f, 0.f, 0.f, 0.f};
-    x *= inv;
+    const bool none = m == -INFINITY;  // the row saw no token: x and l are 0
+    x *= none ? 0.f : 1.f / l;
     if (a.out_dtype == KDA_BF16) {
         const bf16x2 lo = pack_bf16(x[0], x[1]), hi = pack_bf16(x[2], x[3]);
         *reinterpret_cast<bf16x4 *>(static_cast<bf16_t *>(a.o) + at) = (bf16x4){lo[0], lo[1], hi[0], hi[1]};

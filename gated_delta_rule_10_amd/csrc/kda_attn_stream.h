@@ -257,6 +257,8 @@ template <int K, int V, int RT, typename TC> struct Stream {
             float t = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
 #pragma unroll
             for (int j = 4; j < NT; j += 4) t = fmaxf(t, fmaxf(fmaxf(x[j], x[j + 1]), fmaxf(x[j + 2], x[j + 3])));
+            t = fmaxf(t, kLowest);
+            if (masked) t = sees[i] ? t : -INFINITY;
             t = swap32_max(swap16_max(t));
             // The reference m only has to keep 2^(s - m) in range, so it moves when the
             // step's maximum passes it by more than 2^8, not at every step.
@@ -332,8 +334,8 @@ template <int K, int V, int RT, typename TC> struct Stream {
         }
     }
 
-    // Join the four waves' results and hand out rows: put(row in tile, channel, sum m, float4 of
-    // unnormalised outputs, l). Every thread of the workgroup calls it.
+    // Join the four waves' results and hand out rows: put(row in tile, channel, maximum, float4
+    // of unnormalised outputs, sum). Every thread of the workgroup calls it.
     template <typename Put>
     __device__ __forceinline__ void join(char *lds, float (&stat)[2][kWaves][R], int w, int lane, int rows, Put put) {
         const int r = lane & 15, g = lane >> 4, tid = w * 64 + lane;

@@ -163,3 +163,71 @@ def test_values_at_the_ends_of_the_range_in_prompts(dt, heads, kv_heads, T, size
     g = h // (heads // kv_heads)
     ref, lim = ac.prompt_reference(q[:, h].contiguous(), k[:, g].contiguous(), v[:, g].contiguous(), [T], 1.0, bf, bf)
     ac.check(f"{size} {dt}", got[:, h], ref, lim)
+
+
+def infinite_keys(T, kv_heads, heads, seed, which):
+    """q, k, v where the tokens of `which` have a score of -infinity for all queries."""
+    q, k, v = (ac.normal(seed + i, n, h, 64) for i, (n, h) in enumerate(((T, heads), (T, kv_heads), (T, kv_heads))))
+    q[:, :, 0] = 1 + q[:, :, 0].abs()
+    k[which, :, 0] = -float("inf")
+    return q, k, v
+
+
+def expected(q, k, v, sees, scale, bf):
+    """A head's (o, bound): tokens with a score of -infinity weigh nothing; NaN where there is no other."""
+    q, k, v = q.cpu(), k.cpu(), v.cpu()
+    there = torch.isfinite(k).all(1)
+    o = ac.attend(q, torch.nan_to_num(k, neginf=0.0), v, sees & there, scale)
+    lim = ac.bound(*o, 64, bf, bf)
+    return torch.where((sees.any(1) & ~(sees & there).any(1))[:, None], torch.nan, o[0]), lim
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("heads", [4, 20])
+@pytest.mark.parametrize("ctx", [10, 100, 1500])
+def test_scores_of_minus_infinity(dt, heads, ctx):
+    """Some tokens weigh nothing; a row all of whose tokens do is NaN, one that sees no token is 0."""
+    bf, dtype, T = dt == "bf16", torch.bfloat16 if dt == "bf16" else torch.float32, ctx + 3
+    for name, which, ctx_, masks in (("some", slice(0, T - 5), ctx, None), ("all", slice(0, T), ctx, None),
+                                     ("the new ones", slice(ctx, T), ctx, None), ("no context", slice(0, 3), 0, [0, 2, 6])):
+        q, k, v = infinite_keys(ctx_ + 3, 2, heads, 70, which)
+        q = q[-3:].to(dtype).cuda()
+        c = held(73, [ctx_ + 3], k, v, 64, dt)
+        got = call(q, [3], c, masks, 0.125, dt)
+        kk, vv = c.values(0, ctx_ + 3)
+        sees = torch.ones(3, ctx_ + 3, dtype=torch.bool).tril(ctx_)
+        if masks:
+            sees = torch.tensor([[bool(m >> b & 1) for b in range(3)] for m in masks])
+        for h in range(heads):
+            g = h // (heads // 2)
+            check_values(f"{name} {dt} {ctx}", got[:, h], *expected(q[:, h], kk[:, g], vv[:, g], sees, 0.125, bf))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("heads,kv_heads,T", [(4, 2, 300), (128, 32, 600)])
+def test_scores_of_minus_infinity_in_prompts(dt, heads, kv_heads, T):
+    """The first 150 tokens: their rows are NaN, later ones as if they were not there."""
+    bf, dtype = dt == "bf16", torch.bfloat16 if dt == "bf16" else torch.float32
+    q, k, v = (x.to(dtype).cuda() for x in infinite_keys(T, kv_heads, heads, 74, slice(0, 150)))
+    got = attn.kda_attn_fwd(q, k, v, ac.offsets([T]), scale=0.125)
+    for h in (0, heads - 1):
+        g = h // (heads // kv_heads)
+        check_values(dt, got[:, h], *expected(q[:, h], k[:, g], v[:, g], torch.ones(T, T, dtype=torch.bool).tril(), 0.125, bf))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_infinite_scores_times_a_scale_of_zero(dt, sign):
+    """0 times infinity: NaN in the rows that see the token, whatever the form, and nowhere else."""
+    dtype = torch.bfloat16 if dt == "bf16" else torch.float32
+    for heads, kv_heads, T, at in ((4, 2, 300, 200), (128, 32, 600, 550)):
+        q, k, v = infinite_keys(T, kv_heads, heads, 77, slice(at, at + 1))
+        q, k, v = (x.to(dtype).cuda() for x in (q, sign * k, v))
+        got = attn.kda_attn_fwd(q, k, v, ac.offsets([T]), scale=0.0)
+        assert torch.isfinite(got[:at]).all() and got[at:].isnan().all()
+    for heads in (4, 20):
+        for ctx, at in ((100, 30), (100, 101), (1500, 40)):
+            q, k, v = infinite_keys(ctx + 3, 2, heads, 80, slice(at, at + 1))
+            got = call(q[-3:].to(dtype).cuda(), [3], held(83, [ctx + 3], sign * k, v, 64, dt), None, 0.0, dt)
+            sees = max(at - ctx, 0)
+            assert torch.isfinite(got[:sees]).all() and got[sees:].isnan().all()
