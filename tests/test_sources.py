@@ -32,3 +32,11 @@ def test_inline_assembly_computes_nothing(name):
     for ops, text in asm_statements(name):
         for op in ops:
             assert re.fullmatch(r"s_mov_b32|s_nop|s_waitcnt|s_barrier|global_load_lds_dword(x4)?", op), text
+
+
+@pytest.mark.parametrize("name", SOURCES)
+def test_inline_assembly_names_what_it_writes(name):
+    """M0 is written by the copies to LDS: as a clobber, so that nothing is held there across them."""
+    for ops, text in asm_statements(name):
+        if re.search(r"s_mov_b32 m0", text):
+            assert re.search(r'"m0"', text.split(":")[-1]), text
