@@ -137,12 +137,14 @@ template <int K, int V> struct Rows {
     // 2^(c s - m) in bf16, the running maximum and sum (c >= 0: q carries the scale's sign);
     // `sees`: a bit for each of the lane's 32 tokens that its row sees, used if MASKED
     template <bool MASKED> __device__ __forceinline__ void softmax(float c, uint32_t sees) {
-        // all ones where the lane's token i is seen
-        auto seen = [&](int i) { return static_cast<uint32_t>(static_cast<int32_t>(sees << (31 - i)) >> 31); };
         if (MASKED) {
+            // by a word of ones where the lane's token i is seen: 104.5 against 106.3 us for 24 drafted tokens
+            // of 16 sequences, e4m3, with conditions (words kept for the weights below as well: they spill)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                s[i >> 4][i & 15] = __uint_as_float((__float_as_uint(s[i >> 4][i & 15]) & seen(i)) | (0xFF800000u & ~seen(i)));
+            for (int i = 0; i < 32; ++i) {
+                const uint32_t seen = static_cast<uint32_t>(static_cast<int32_t>(sees << (31 - i)) >> 31);
+                s[i >> 4][i & 15] = __uint_as_float((__float_as_uint(s[i >> 4][i & 15]) & seen) | (0xFF800000u & ~seen));
+            }
         }
         float t = max3(s[0][0], s[1][0], s[0][1]), u = max3(s[1][1], s[0][2], s[1][2]);
 #pragma unroll
@@ -171,7 +173,7 @@ template <int K, int V> struct Rows {
             for (int i = 0; i < 16; ++i) {
                 s[b][i] = __builtin_amdgcn_exp2f(fmaf(s[b][i], c, -ref));
                 // not left to the exponential: with a scale of 0, -infinity is 0 * infinity
-                if (MASKED) s[b][i] = __uint_as_float(__float_as_uint(s[b][i]) & seen(16 * b + i));
+                if (MASKED && !((sees >> (16 * b + i)) & 1u)) s[b][i] = 0.f;
                 sum[i & 1] += s[b][i];
             }
         l += sum[0] + sum[1];
