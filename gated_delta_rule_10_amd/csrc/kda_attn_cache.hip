@@ -2,7 +2,8 @@
 //
 // The cache is what the call has to read, so it is read once: a workgroup
 // takes all rows of a (sequence, kv head), the new tokens times the query heads
-// of the group, in tiles of R rows, over a run of steps of 128 cached tokens.
+// of the group, in tiles of R rows, over a run of steps: 128 cached tokens, 64 of fp32, and 64
+// where the waves share them (below).
 //
 // Two kernels, by the rows that a (sequence, kv head) has on average:
 //  - up to 16 (single tokens, with the group's heads): the steps of a run are shared out
@@ -200,9 +201,9 @@ struct Pages {
 // workgroups to a compute unit, as registers and LDS allow
 constexpr int kPerCu = 2;
 
-template <int K, int V, int RT, typename TC>
+template <int K, int V, typename TC>
 __global__ __launch_bounds__(64 * kWaves, kPerCu) void attn_cache_kernel(AttnArgs a) {
-    using S = Stream<K, V, RT, TC>;
+    using S = Stream<K, V, TC>;
     constexpr int R = S::R;
     __shared__ __align__(16) char lds[S::kLds];
     __shared__ float stat[2][kWaves][R];
@@ -264,8 +265,8 @@ __global__ __launch_bounds__(64 * kWaves, kPerCu) void attn_cache_kernel(AttnArg
                 kx[b] = n.ke[b];
                 vx[b] = n.ve[b];
             }
-            uint32_t sees[RT];
-            if (masked) st.visible(sees, a, q.start, r0, rows, p0, q.ctx, q.end, n.here, lane);
+            uint32_t sees = 0;
+            if (masked) sees = st.visible(a, q.start, r0, rows, p0, q.ctx, q.end, n.here, lane);
             const bool odd = S::stage(n, lk, lv, masked, p0, q.end, lane);
             load(min(t + 1, te - 1), n);
             __builtin_amdgcn_wave_barrier();
@@ -580,8 +581,8 @@ template <int V, int R, int STEP> hipError_t launch_join(const AttnArgs &a, hipS
     return hipGetLastError();
 }
 template <int K, int V, typename TC> hipError_t launch_stream(const AttnArgs &a, hipStream_t st) {
-    hipLaunchKernelGGL((attn_cache_kernel<K, V, 1, TC>), dim3(a.W), dim3(64 * kWaves), 0, st, a);
-    return launch_join<V, 16, Stream<K, V, 1, TC>::kStep>(a, st);
+    hipLaunchKernelGGL((attn_cache_kernel<K, V, TC>), dim3(a.W), dim3(64 * kWaves), 0, st, a);
+    return launch_join<V, 16, Stream<K, V, TC>::kStep>(a, st);
 }
 template <int K, int V, typename TC> hipError_t launch_rows(const AttnArgs &a, hipStream_t st) {
     hipLaunchKernelGGL((attn_cache_rows_kernel<K, V, TC>), dim3(a.W), dim3(256), 0, st, a);

@@ -12,9 +12,9 @@
 namespace kda {
 namespace {
 
-template <int K, int V, int RT, typename TC>
+template <int K, int V>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a, int slots) {
-    using S = Stream<K, V, RT, TC>;
+    using S = Stream<K, V, float>;
     constexpr int R = S::R;
     __shared__ __align__(16) char lds[S::kLds];
     __shared__ float stat[2][kWaves][R];
@@ -40,8 +40,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a,
     if (w * S::kStepWave < last) S::load_packed(ahead, a, start, kvh, w * S::kStepWave, lane);
     for (int p0 = w * S::kStepWave; p0 < last; p0 += S::kStep) {
         const bool masked = p0 + S::kStepWave > open;
-        uint32_t sees[RT];
-        if (masked) st.visible(sees, a, start, r0, rows, p0, 0, count, ahead.here, lane);
+        uint32_t sees = 0;
+        if (masked) sees = st.visible(a, start, r0, rows, p0, 0, count, ahead.here, lane);
         const bool odd = S::stage(ahead, lk, lv, masked, p0, count, lane);
         if (p0 + S::kStep < last) S::load_packed(ahead, a, start, kvh, p0 + S::kStep, lane);
         __builtin_amdgcn_wave_barrier();
@@ -56,7 +56,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a,
 
 // ---- bf16
 //
-// NW waves of 32 rows each share tiles of 64 keys and values in LDS, copied there
+// NW = 8 waves of 32 rows each share tiles of 64 keys and values in LDS, copied there
 // directly from memory ahead of their use (two buffers each). Where there are too few
 // rows for all compute units (halves()), a tile is 128 keys and values, its PARTS = 2
 // halves go to one half of the waves each, both with the same rows, and their maxima,
@@ -69,9 +69,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a,
 // = 16 (718 TFLOP/s). Short prompts add what a workgroup cannot overlap, its start and its
 // store: 400 us for 16 prompts of 200 to 4000 tokens, H = 32 (880 TFLOP/s).
 
+constexpr int NW = 8;
+
 // Copies of the tiles of keys or values (D channels), in order: 64 rows from the next one on
 // to LDS at dst.
-template <typename R, int D, bool KEYS, int NW> struct Copier {
+template <typename R, int D, bool KEYS> struct Copier {
     static constexpr int C = D / 8, N = kTile * D * 2 / (1024 * NW);
     static_assert(N >= 1, "a tile is at least one copy per wave");
     const bf16_t *next;
@@ -105,7 +107,7 @@ template <typename R, int D, bool KEYS, int NW> struct Copier {
     }
 };
 
-template <int K, int V, int NW, int PARTS>
+template <int K, int V, int PARTS>
 __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a, int slots) {
     using P = Rows<K, V>;
     constexpr int R = 32 * NW / PARTS, kTurn = PARTS * kTile;  // rows; tokens of a tile
@@ -142,8 +144,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
     auto lk = [&](int j) { return (j & 1) * KB; };
     auto lv = [&](int j) { return 2 * KB + (j & 1) * VB; };
     const char *const own_k = lds + part * P::KB, *const own_v = lds + part * P::VB;
-    Copier<P, K, true, NW> kc;
-    Copier<P, V, false, NW> vc;
+    Copier<P, K, true> kc;
+    Copier<P, V, false> vc;
     kc.begin(static_cast<const bf16_t *>(a.k) + kvh * K, a.ks, start, a.T, w, lane);
     vc.begin(static_cast<const bf16_t *>(a.v) + kvh * V, a.vs, start, a.T, w, lane);
     // The two waves of a SIMD take turns: one is in its products (the values of the tile before,
@@ -173,8 +175,8 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
     copy_v(0);
     copy_k(1);
     // tile 0's keys; a call of one tile has no copies of tile 1 behind them
-    if (tiles > 1) wait_copies<PARTS * (Copier<P, V, false, NW>::N + Copier<P, K, true, NW>::N)>();
-    else wait_copies<PARTS * Copier<P, V, false, NW>::N>();
+    if (tiles > 1) wait_copies<PARTS * (Copier<P, V, false>::N + Copier<P, K, true>::N)>();
+    else wait_copies<PARTS * Copier<P, V, false>::N>();
     phase_barrier();
     if (!ahead) swap(false);
     // The wave in its products issues first where they are the longer turn (two heads of 64
@@ -255,17 +257,17 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_prompt_bf16_kernel(AttnArgs a
     st.each(lane, [&](int ch, f32x4 x) { store_out(a, start, kvh, static_cast<int>(row), ch, st.m, x, l); });
 }
 
-template <int K, int V, int NW, int PARTS> hipError_t launch_bf16(const AttnArgs &a, hipStream_t st) {
+template <int K, int V, int PARTS> hipError_t launch_bf16(const AttnArgs &a, hipStream_t st) {
     const int64_t slots = static_cast<int64_t>(a.T) * a.G / (32 * NW / PARTS) + a.N;
-    hipLaunchKernelGGL((attn_prompt_bf16_kernel<K, V, NW, PARTS>), dim3(static_cast<unsigned>(slots * a.Hk)), dim3(64 * NW), 0, st, a,
+    hipLaunchKernelGGL((attn_prompt_bf16_kernel<K, V, PARTS>), dim3(static_cast<unsigned>(slots * a.Hk)), dim3(64 * NW), 0, st, a,
                        static_cast<int>(slots));
     return hipGetLastError();
 }
 
-template <int K, int V, int RT>
+template <int K, int V>
 hipError_t launch_f32(const AttnArgs &a, hipStream_t st) {
-    const int64_t slots = static_cast<int64_t>(a.T) * a.G / (16 * RT) + a.N;
-    hipLaunchKernelGGL((attn_prompt_kernel<K, V, RT, float>), dim3(static_cast<unsigned>(slots * a.Hk)), dim3(64 * kWaves), 0, st,
+    const int64_t slots = static_cast<int64_t>(a.T) * a.G / Stream<K, V, float>::R + a.N;
+    hipLaunchKernelGGL((attn_prompt_kernel<K, V>), dim3(static_cast<unsigned>(slots * a.Hk)), dim3(64 * kWaves), 0, st,
                        a, static_cast<int>(slots));
     return hipGetLastError();
 }
@@ -285,8 +287,8 @@ bool halves(const AttnArgs &a) {
 }
 
 template <int K, int V> hipError_t launch_dims(const AttnArgs &a, hipStream_t st) {
-    if (a.in_dtype == KDA_F32) return launch_f32<K, V, 1>(a, st);
-    return halves(a) ? launch_bf16<K, V, 8, 2>(a, st) : launch_bf16<K, V, 8, 1>(a, st);
+    if (a.in_dtype == KDA_F32) return launch_f32<K, V>(a, st);
+    return halves(a) ? launch_bf16<K, V, 2>(a, st) : launch_bf16<K, V, 1>(a, st);
 }
 
 }  // namespace

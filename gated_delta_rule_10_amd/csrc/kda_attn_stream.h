@@ -1,4 +1,4 @@
-// Attention of a tile of R = 16 RT rows over a run of keys and values, streamed
+// Attention of a tile of R = 16 rows over a run of keys and values, streamed
 // once: o = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m), s_j = c q.k_j in the
 // log2 domain, with the running maximum m and sum kept per row in fp32.
 //
@@ -30,10 +30,10 @@ namespace kda {
 
 constexpr int kWaves = 4;
 
-template <int K, int V, int RT, typename TC> struct Stream {
+template <int K, int V, typename TC> struct Stream {
     using Frag = typename mma_of<TC>::frag;
     using Elem = typename mma_of<TC>::elem;  // of q
-    static constexpr int R = 16 * RT;
+    static constexpr int R = 16;
     static constexpr int ES = sizeof(TC);
     static constexpr bool kCodes = sizeof(TC) == 1;
     static constexpr int NB = ES == 4 ? 1 : 2;             // groups of 16 tokens per wave and step
@@ -46,7 +46,7 @@ template <int K, int V, int RT, typename TC> struct Stream {
     static constexpr int KT = K / 32, VT = V / 16;
     static constexpr int KB = kStepWave * K * ES, VB = kStepWave * V * ES;    // LDS bytes per wave
     static constexpr int kJoinRow = V + 4;                                    // floats per row of a join tile
-    static constexpr int kJoin = kWaves * 16 * kJoinRow * 4;
+    static constexpr int kJoin = kWaves * R * kJoinRow * 4;
     static constexpr int kRing = kWaves * (KB + VB);
     static constexpr int kLds = kRing > kJoin ? kRing : kJoin;
 
@@ -59,9 +59,9 @@ template <int K, int V, int RT, typename TC> struct Stream {
         return (4 * (t >> 2)) & (CV - 1);
     }
 
-    Frag q[RT][KT];
-    f32x4 o[VT][RT];
-    float m[RT], l[RT];  // per row l % 16 of each 16-row block; l is this lane's share
+    Frag q[KT];
+    f32x4 o[VT];
+    float m, l;  // of row l % 16; the sum is this lane's share
     // keys, values and exponents on their way, of the next step
     struct Ahead {
         u32x4 kr[NK], vr[NV];
@@ -70,30 +70,23 @@ template <int K, int V, int RT, typename TC> struct Stream {
     } next;
 
     __device__ __forceinline__ void reset() {
+        m = -INFINITY;
+        l = 0.f;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            m[i] = -INFINITY;
-            l[i] = 0.f;
-#pragma unroll
-            for (int d = 0; d < VT; ++d) o[d][i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-        }
+        for (int d = 0; d < VT; ++d) o[d] = (f32x4){0.f, 0.f, 0.f, 0.f};
     }
 
-    // Row tile rt of (sequence rows from `start`, kv head g): fragments of q.
+    // Rows from r0 on of (sequence rows from `start`, kv head kvh): fragments of q.
     // Rows past `rows` repeat the last one and are not stored.
     __device__ __forceinline__ void load_q(const AttnArgs &a, int start, int kvh, int r0, int rows, int lane) {
-        const int g = lane >> 4;
+        const int g = lane >> 4, r = r0 + min(lane & 15, rows - 1);
+        const int tok = r / a.G, h = kvh * a.G + (r - tok * a.G);
+        const Elem *p = static_cast<const Elem *>(a.q) + static_cast<int64_t>(start + tok) * a.qs + h * K + 8 * g;
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const int r = r0 + min(16 * i + (lane & 15), rows - 1);
-            const int tok = r / a.G, h = kvh * a.G + (r - tok * a.G);
-            const Elem *p = static_cast<const Elem *>(a.q) + static_cast<int64_t>(start + tok) * a.qs + h * K + 8 * g;
-#pragma unroll
-            for (int s = 0; s < KT; ++s) q[i][s] = load_frag(p + 32 * s);
-        }
+        for (int s = 0; s < KT; ++s) q[s] = load_frag(p + 32 * s);
     }
 
-    // ---- sources: chunk x of a wave's 32 tokens
+    // ---- sources: chunk x of a wave's kStepWave tokens
     // cache: row[b] is the cache row of the first of tokens 16 b .. 16 b + 15 (a page ends at a multiple of
     // 16, so the 16 rows lie behind one another)
     static __device__ __forceinline__ void load_cache(Ahead &n, const AttnArgs &a, const int64_t (&row)[NB], int lane) {
@@ -119,10 +112,10 @@ template <int K, int V, int RT, typename TC> struct Stream {
             }
         }
     }
-    // packed tokens of the call: a position past the last token reads the last one and is masked
+    // packed tokens of the call (fp32): a position past the last token reads the last one and is masked
     static __device__ __forceinline__ void load_packed(Ahead &n, const AttnArgs &a, int start, int kvh, int p0, int lane) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) n.here[b] = true;
+        static_assert(ES == 4, "bf16 prompts have their own kernel");
+        n.here[0] = true;
 #pragma unroll
         for (int x = 0; x < NK; ++x) {
             const int e = x * 64 + lane, t = e / CK, c = e % CK;
@@ -227,73 +220,60 @@ template <int K, int V, int RT, typename TC> struct Stream {
         return (f32x4){static_cast<float>(x[0]), static_cast<float>(x[1]), static_cast<float>(x[2]), static_cast<float>(x[3])};
     }
 
-    // One step over the 32 staged tokens. sees[i] bit (4 b + j): row l % 16 of block i sees
-    // token 16 b + 4 g + j (read only when masked). e: exponents of these tokens.
-    __device__ __forceinline__ void step(const char *lk, const char *lv, float c, bool masked, const uint32_t (&sees)[RT],
-                                         bool odd, const uint32_t (&kx)[NB], const uint32_t (&vx)[NB], int lane) {
-        f32x4 s[NB][RT];
+    // One step over the kStepWave staged tokens. sees bit (4 b + j): row l % 16 sees token 16 b + 4 g + j
+    // (read only when masked). kx, vx: exponents of these tokens.
+    __device__ __forceinline__ void step(const char *lk, const char *lv, float c, bool masked, uint32_t sees, bool odd, const uint32_t (&kx)[NB], const uint32_t (&vx)[NB], int lane) {
+        f32x4 s[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
+            s[b] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < RT; ++i) s[b][i] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int ks = 0; ks < KT; ++ks) {
-                const Frag kf = k_frag(lk, b, ks, lane);
-#pragma unroll
-                for (int i = 0; i < RT; ++i) s[b][i] = mma16(kf, q[i][ks], s[b][i]);
-            }
+            for (int ks = 0; ks < KT; ++ks) s[b] = mma16(k_frag(lk, b, ks, lane), q[ks], s[b]);
         }
-        PFrag p[RT], rest[RT];
-        float pf[RT][NT];
+        float x[NT], pf[NT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            float x[NT];
+        for (int j = 0; j < NT; ++j) {
+            x[j] = s[j >> 2][j & 3] * c;
+            if (kCodes) x[j] = scaled_by(x[j], kx[j >> 2], j & 3);
+            if (masked) x[j] = (sees >> j) & 1u ? x[j] : -INFINITY;
+        }
+        float t = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                x[j] = s[j >> 2][i][j & 3] * c;
-                if (kCodes) x[j] = scaled_by(x[j], kx[j >> 2], j & 3);
-                if (masked) x[j] = (sees[i] >> j) & 1u ? x[j] : -INFINITY;
-            }
-            float t = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        for (int j = 4; j < NT; j += 4) t = fmaxf(t, fmaxf(fmaxf(x[j], x[j + 1]), fmaxf(x[j + 2], x[j + 3])));
+        t = fmaxf(t, kLowest);
+        if (masked) t = sees ? t : -INFINITY;
+        t = swap32_max(swap16_max(t));
+        // The reference m only has to keep 2^(s - m) in range, so it moves when the
+        // step's maximum passes it by more than 2^8, not at every step.
+        if (__any(t > m + 8.f)) {
+            const float mn = fmaxf(m, t);
+            const float f = mn == -INFINITY ? 1.f : exp2f(m - mn);
+            m = mn;
+            l *= f;
 #pragma unroll
-            for (int j = 4; j < NT; j += 4) t = fmaxf(t, fmaxf(fmaxf(x[j], x[j + 1]), fmaxf(x[j + 2], x[j + 3])));
-            t = fmaxf(t, kLowest);
-            if (masked) t = sees[i] ? t : -INFINITY;
-            t = swap32_max(swap16_max(t));
-            // The reference m only has to keep 2^(s - m) in range, so it moves when the
-            // step's maximum passes it by more than 2^8, not at every step.
-            if (__any(t > m[i] + 8.f)) {
-                const float mn = fmaxf(m[i], t);
-                const float f = mn == -INFINITY ? 1.f : exp2f(m[i] - mn);
-                m[i] = mn;
-                l[i] *= f;
+            for (int d = 0; d < VT; ++d) o[d] *= f;
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
-                for (int d = 0; d < VT; ++d) o[d][i] *= f;
-            }
-            const float ref = m[i] == -INFINITY ? 0.f : m[i];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                pf[i][j] = __builtin_amdgcn_exp2f(x[j] - ref);
-                l[i] += pf[i][j];
-                if (kCodes) pf[i][j] = scaled_by(pf[i][j], vx[j >> 2], j & 3);
-            }
-            p[i] = to_frag(pf[i], PFrag{});
+        for (int j = 0; j < NT; ++j) {
+            pf[j] = __builtin_amdgcn_exp2f(x[j] - ref);
+            l += pf[j];
+            if (kCodes) pf[j] = scaled_by(pf[j], vx[j >> 2], j & 3);
+        }
+        const PFrag p = to_frag(pf, PFrag{});
+        if (!odd) {
+            PFrag rest;  // of the weights, what bf16 leaves
             if constexpr (ES != 4) {
                 float r[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) r[j] = pf[i][j] - static_cast<float>(p[i][j]);
-                rest[i] = to_frag(r, PFrag{});
+                for (int j = 0; j < 8; ++j) r[j] = pf[j] - static_cast<float>(p[j]);
+                rest = to_frag(r, PFrag{});
             }
-        }
-        if (!odd) {
 #pragma unroll
             for (int d = 0; d < VT; ++d) {
                 const PFrag vf = v_frag(lv, d, lane);
-#pragma unroll
-                for (int i = 0; i < RT; ++i) {
-                    if constexpr (ES != 4) o[d][i] = mma16(vf, rest[i], o[d][i]);
-                    o[d][i] = mma16(vf, p[i], o[d][i]);
-                }
+                if constexpr (ES != 4) o[d] = mma16(vf, rest, o[d]);
+                o[d] = mma16(vf, p, o[d]);
             }
             return;
         }
@@ -302,36 +282,29 @@ template <int K, int V, int RT, typename TC> struct Stream {
 #pragma unroll 1
         for (int t = 0; t < kStepWave; ++t) {
             const int j = 4 * (t >> 4) + (t & 3), src = 4 * (t & 12) + (lane & 15);  // its register, its lanes
+            float w = 0.f;
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                float w = 0.f;
+            for (int i = 0; i < NT; ++i)
+                if (i == j) w = pf[i];
+            w = __shfl(w, src);
+            const bool see = !masked || (__shfl(sees, src) >> j) & 1u;
 #pragma unroll
-                for (int x = 0; x < NT; ++x)
-                    if (x == j) w = pf[i][x];
-                w = __shfl(w, src);
-                const bool see = !masked || (__shfl(sees[i], src) >> j) & 1u;
-#pragma unroll
-                for (int d = 0; d < VT; ++d) {
-                    const f32x4 x = v_row(lv, t, d, lane);
-                    if (see) o[d][i] += x * w;
-                }
+            for (int d = 0; d < VT; ++d) {
+                const f32x4 y = v_row(lv, t, d, lane);
+                if (see) o[d] += y * w;
             }
         }
     }
 
-    // Which tokens the lane's rows see in a masked step (seen_tokens)
-    __device__ __forceinline__ void visible(uint32_t (&sees)[RT], const AttnArgs &a, int start, int r0, int rows, int p0,
-                                            int ctx, int end, const bool (&here)[NB], int lane) const {
-        const int g = 4 * (lane >> 4);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const int tok = (r0 + min(16 * i + (lane & 15), rows - 1)) / a.G;
-            const uint64_t bits = a.mask ? a.mask[start + tok] : 0;
-            const uint32_t w = static_cast<uint32_t>(
-                seen_tokens(a.mask != nullptr, bits, p0, ctx, ctx + tok, end, (here[0] ? 1 : 0) | (here[NB - 1] ? 2 : 0)));
-            sees[i] = (w >> g) & 15u;
-            if (NB == 2) sees[i] |= ((w >> (16 + g)) & 15u) << 4;
-        }
+    // Which tokens the lane's row sees in a masked step (seen_tokens), as step() takes them
+    __device__ __forceinline__ uint32_t visible(const AttnArgs &a, int start, int r0, int rows, int p0, int ctx, int end,
+                                                const bool (&here)[NB], int lane) const {
+        const int g = 4 * (lane >> 4), tok = (r0 + min(lane & 15, rows - 1)) / a.G;
+        const uint64_t bits = a.mask ? a.mask[start + tok] : 0;
+        const uint32_t w = static_cast<uint32_t>(
+            seen_tokens(a.mask != nullptr, bits, p0, ctx, ctx + tok, end, (here[0] ? 1 : 0) | (here[NB - 1] ? 2 : 0)));
+        const uint32_t sees = (w >> g) & 15u;
+        return NB == 2 ? sees | ((w >> (16 + g)) & 15u) << 4 : sees;
     }
 
     // Join the four waves' results and hand out rows: put(row in tile, channel, maximum, float4
@@ -339,49 +312,34 @@ template <int K, int V, int RT, typename TC> struct Stream {
     template <typename Put>
     __device__ __forceinline__ void join(char *lds, float (&stat)[2][kWaves][R], int w, int lane, int rows, Put put) {
         const int r = lane & 15, g = lane >> 4, tid = w * 64 + lane;
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            l[i] = swap32_sum(swap16_sum(l[i]));
-            if (g == 0) stat[0][w][16 * i + r] = m[i];
-        }
+        l = swap32_sum(swap16_sum(l));
+        if (g == 0) stat[0][w][r] = m;
         __syncthreads();
-        float f[RT];
+        float mm = stat[0][0][r];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            float mm = stat[0][0][16 * i + r];
-#pragma unroll
-            for (int u = 1; u < kWaves; ++u) mm = fmaxf(mm, stat[0][u][16 * i + r]);
-            f[i] = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mm);
-            // a wave that saw nothing of a row holds zeros for it; f keeps NaN and infinity as they are
-            if (g == 0) stat[1][w][16 * i + r] = l[i] * f[i];
-        }
+        for (int u = 1; u < kWaves; ++u) mm = fmaxf(mm, stat[0][u][r]);
+        // a wave that saw nothing of a row holds zeros for it
+        const float f = m == -INFINITY ? 0.f : exp2f(m - mm);
+        if (g == 0) stat[1][w][r] = l * f;
         float *tile = reinterpret_cast<float *>(lds);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            if (16 * i < rows) {
+        for (int d = 0; d < VT; ++d) *reinterpret_cast<f32x4 *>(tile + (w * R + r) * kJoinRow + 16 * d + 4 * g) = o[d] * f;
+        __syncthreads();
+        for (int e = tid; e < R * (V / 4); e += 64 * kWaves) {
+            const int row = e / (V / 4), ch = 4 * (e % (V / 4));
+            if (row < rows) {
+                f32x4 x = *reinterpret_cast<const f32x4 *>(tile + row * kJoinRow + ch);
+                float mj = stat[0][0][row], ll = stat[1][0][row];
 #pragma unroll
-                for (int d = 0; d < VT; ++d)
-                    *reinterpret_cast<f32x4 *>(tile + (w * 16 + r) * kJoinRow + 16 * d + 4 * g) = o[d][i] * f[i];
-            }
-            __syncthreads();
-            if (16 * i < rows) {
-                for (int e = tid; e < 16 * (V / 4); e += 64 * kWaves) {
-                    const int rr = e / (V / 4), ch = 4 * (e % (V / 4)), row = 16 * i + rr;
-                    if (row < rows) {
-                        f32x4 x = *reinterpret_cast<const f32x4 *>(tile + rr * kJoinRow + ch);
-                        float mm = stat[0][0][row], ll = stat[1][0][row];
-#pragma unroll
-                        for (int u = 1; u < kWaves; ++u) {
-                            x += *reinterpret_cast<const f32x4 *>(tile + (u * 16 + rr) * kJoinRow + ch);
-                            mm = fmaxf(mm, stat[0][u][row]);
-                            ll += stat[1][u][row];
-                        }
-                        put(row, ch, mm, x, ll);
-                    }
+                for (int u = 1; u < kWaves; ++u) {
+                    x += *reinterpret_cast<const f32x4 *>(tile + (u * R + row) * kJoinRow + ch);
+                    mj = fmaxf(mj, stat[0][u][row]);
+                    ll += stat[1][u][row];
                 }
+                put(row, ch, mj, x, ll);
             }
-            __syncthreads();
         }
+        __syncthreads();
     }
 };
 
