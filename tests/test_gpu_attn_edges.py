@@ -231,3 +231,71 @@ def test_infinite_scores_times_a_scale_of_zero(dt, sign):
             got = call(q[-3:].to(dtype).cuda(), [3], held(83, [ctx + 3], sign * k, v, 64, dt), None, 0.0, dt)
             sees = max(at - ctx, 0)
             assert torch.isfinite(got[:sees]).all() and got[sees:].isnan().all()
+
+
+def wide(T, heads, kv_heads, dtype):
+    """q, k, v [T, heads, 64] as parts of rows of 2^24 elements, the longest allowed: the last lie past 2^31."""
+    step = 2 ** 24
+    x = torch.empty(T * step, dtype=dtype, device="cuda")
+    at, out = 0, []
+    for i, h in enumerate((heads, kv_heads, kv_heads)):
+        y = x.as_strided((T, h, 64), (step, 64, 1), at)
+        y.copy_(ac.normal(90 + i, T, h, 64))
+        out.append(y)
+        at += h * 64
+    assert (T - 1) * step > 2 ** 31
+    return out
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("heads,kv_heads", [(4, 2), (512, 128)])
+def test_rows_past_32_bits(dt, heads, kv_heads):
+    """Prompts (both tile forms), cache writes and cache attention of tokens whose offsets pass 2^31 elements."""
+    T, bf = 200, dt == "bf16"
+    q, k, v = wide(T, heads, kv_heads, torch.bfloat16 if bf else torch.float32)
+    got = attn.kda_attn_fwd(q, k, v, ac.offsets([T]), scale=0.125)
+    for h in (0, heads - 1):
+        g = h // (heads // kv_heads)
+        ref, lim = ac.prompt_reference(q[:, h:h + 1].contiguous(), k[:, g:g + 1].contiguous(), v[:, g:g + 1].contiguous(), [T],
+                                       0.125, bf, bf)
+        ac.check(f"prompt {dt} head {h}", got[:, h:h + 1], ref, lim)
+    if heads > 4:
+        return
+    c = ac.Cache([T], kv_heads, 64, 64, 64, dt)
+    attn.kda_kv_write(k, v, ac.offsets([T]), *c.args())
+    held_k, held_v = c.values(0, T)
+    assert torch.equal(held_k, k.double().cpu()) and torch.equal(held_v, v.double().cpu())
+    # the whole sequence as new tokens: what the prompt gives, from rows of the same width
+    got = attn.kda_attn_cache_fwd(q, ac.offsets([T]), *c.args(), scale=0.125)
+    ref, lim = ac.prompt_reference(q.contiguous(), k.contiguous(), v.contiguous(), [T], 0.125, bf, bf)
+    ac.check(f"over the cache {dt}", got, ref, lim)
+
+
+@pytest.mark.parametrize("dt,T,heads", [("bf16", 20000, 4), ("bf16", 9001, 32), ("f32", 6000, 4)])
+def test_long_prompts(dt, T, heads):
+    """Rows throughout one long prompt (the larger one's tiles are 256 rows), some at tiles' edges."""
+    bf, dtype = dt == "bf16", torch.bfloat16 if dt == "bf16" else torch.float32
+    q, k, v = (ac.normal(100 + i, T, h, 64).to(dtype).cuda() for i, h in enumerate((heads, heads // 4, heads // 4)))
+    got = attn.kda_attn_fwd(q, k, v, ac.offsets([T]), scale=0.125)
+    rows = torch.tensor([0, 1, 63, 64, 1023, T // 2, T // 2 + 1, T - 65, T - 2, T - 1])
+    sees = torch.arange(T)[None] <= rows[:, None]
+    for h in (0, heads - 1):
+        r = ac.attend(q[rows.cuda(), h].cpu(), k[:, h // 4].cpu(), v[:, h // 4].cpu(), sees, 0.125)
+        ac.check(f"{dt} {T} head {h}", got[rows.cuda(), h], r[0], ac.bound(*r, 64, bf, bf))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,ctx", [(700, 0), (700, 1500)])
+def test_chunks_of_prompts_over_the_cache(kv, new, ctx):
+    """A prompt's chunk of many new tokens, beside a single token of another sequence."""
+    T = ctx + new
+    c = held(110, [T, 40], ac.normal(111, T + 40, 2, 64), ac.normal(112, T + 40, 2, 64), 64, kv)
+    q = ac.normal(113, new + 1, 8, 64).bfloat16().cuda()
+    got = call(q, [new, 1], c, None, 0.125, "bf16")
+    rows = torch.tensor([0, 1, 31, 32, 63, 64, 300, new - 2, new - 1])
+    for n, at, count, total in ((0, rows, new, T), (1, torch.tensor([new]), 1, 40)):
+        k, v = c.values(n, total)
+        sees = torch.arange(total)[None] <= (at - (0 if n == 0 else new))[:, None] + total - count
+        for h in (0, 7):
+            r = ac.attend(q[at.cuda(), h].cpu(), k[:, h // 4], v[:, h // 4], sees, 0.125)
+            ac.check(f"{kv} sequence {n} head {h}", got[at.cuda(), h], r[0], ac.bound(*r, 64, True, True))
