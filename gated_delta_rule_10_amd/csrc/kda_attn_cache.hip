@@ -21,9 +21,14 @@
 //
 // What bounds it: the cache's bytes. One token for each of 64 sequences of 1000 to 16000
 // tokens, H = 32, Hk = 8, d = 128: a bf16 cache of 1.37 GB in 247 us (5.55 TB/s; a copy
-// reaches 4.9), an e4m3 one of 0.69 GB in 140 us (4.93 TB/s). One sequence of 524288
-// tokens: 2.15 GB in 367 us (5.85 TB/s), 8 us of them the join. 24 drafted tokens for
-// each of 16 sequences of 500 to 20000 tokens, e4m3: 106 us (2.43 TB/s, 450 TFLOP/s).
+// reaches 4.9), an e4m3 one of 0.69 GB in 140 us (4.93 TB/s), an fp32 one of 2.75 GB in 480 us
+// (5.7 TB/s, though its kernel at d = 128 spills 6 registers). One sequence of 524288 tokens: 2.15
+// GB in 366 us (5.86 TB/s), 9 us of them the join. 24 drafted tokens for each of 16 sequences of
+// 500 to 20000 tokens: 125 us from bf16 (4.05 TB/s), 105 from e4m3 (2.45 TB/s, 450 TFLOP/s).
+// Chunks of a prompt (2048 tokens over 30000): 1.05 ms from bf16 (990 TFLOP/s), 1.30 from e4m3.
+// Every row tile of a sequence has as many steps on the line, also those that its causal rows do
+// not see; with no tokens before a chunk that is half of them (2048 over 0: 81 and 105 us, 420
+// and 330 TFLOP/s).
 #include "kda_attn_stream.h"
 
 namespace kda {
@@ -303,7 +308,9 @@ __global__ __launch_bounds__(64 * kWaves, kPerCu) void attn_cache_kernel(AttnArg
 // joining about five (its launch and its reads). Whole against cut at 500 tokens: 11.4 and 12.6
 // us for one token, 30 and 34 for one token of 64 sequences, 19.2 and 14.3 for 16 tokens of one
 // sequence, 20.5 and 27.6 for 12 tokens of 16. At 1000 tokens: 16.6 and 12.7, 54 and 58, 31.8
-// and 14.5.
+// and 14.5. The lengths are the device's, so a short sequence in a table that reaches further is
+// cut: whole calls of one token at 300 tokens take 12.8 us with tables of up to 512 tokens and
+// 18.5 beyond, those of 64 such sequences 19.8 and 23.7.
 constexpr int kWhole = 512;
 
 // Joins the pieces of the (sequence, kv head, row tile)s that the line was cut inside: a
@@ -378,7 +385,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
 // tile of their own (exactly: four bits of significand and a power of two), so that the
 // products are the bf16 ones. Two workgroups share a compute unit, so that one's softmax and
 // waits run under the other's products. 24 tokens of 4 heads to a kv head, 16 sequences of 8000
-// tokens: 120 us from a bf16 cache (524 MB, 4.4 TB/s), 115 from e4m3 (270 MB, 2.3 TB/s), where
+// tokens: 115 us from a bf16 cache (524 MB, 4.6 TB/s), 107 from e4m3 (270 MB, 2.5 TB/s), where
 // the turn to bf16, the products and the softmax are what it waits for.
 template <int K, int V, typename TC> struct Tiles {
     using X = Rows<K, V>;
@@ -568,8 +575,15 @@ __global__ __launch_bounds__(256, 2) void attn_cache_rows_kernel(AttnArgs a) {
 // against 128 rows, 16 sequences of 8000 tokens, us: 16 rows 107 and 110 from bf16, 62 and 94
 // from e4m3; 20 and 32 rows 164 and 110, 92 and 94; 48 rows 274 and 113, 137 and 101; 96 rows
 // 481 and 120, 245 and 115. (From e4m3, 32 rows are even closer: 64 sequences of 6000 tokens 294
-// and 240, one of 100000 64 and 78.) fp32 is bound by its products from 16 rows on, so larger
-// tiles would save nothing.
+// and 240, one of 100000 64 and 78.)
+// The counts are the device's, and the mean stands for them. One chunk among single tokens (chunk
+// @ tokens before it + others, each @ its own), 16 against 128 rows, bf16 and e4m3: mean of 8 rows,
+// 500 @ 2000 + 500 @ 2000 815 and 892, 438 and 830; 100 @ 1000 + 200 @ 1000 176 and 228, 106 and
+// 217; 64 @ 4000 + 64 @ 4000 204 and 226, 116 and 208. Of 24, 500 @ 2000 + 100 @ 2000 286 and 209,
+// but 154 and 206. Of 44, 2000 @ 20000 + 200 @ 2000 6623 and 1061, 3497 and 1231; of 68, 512 @
+// 8000 + 32 @ 4000 717 and 189, 377 and 202; of 132, 2048 @ 0 + 64 @ 4000 420 and 281, 322 and 301.
+// fp32 has the 16-row form alone: 24 tokens of 4 heads, 16 sequences of 500 to 20000 tokens take
+// 919 us against a floor of 310 (its products).
 int tile_rows(int64_t T, int64_t N, int64_t G, bool f32) { return f32 || (T + N - 1) / N * G <= 16 ? 16 : 128; }
 
 template <int V, int R, int STEP> hipError_t launch_join(const AttnArgs &a, hipStream_t st) {

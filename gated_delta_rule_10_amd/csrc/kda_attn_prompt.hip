@@ -3,9 +3,10 @@
 // A workgroup takes one tile of R rows of a (sequence, kv head), row r being
 // token r / G and query head r % G, and streams the keys and values up to the
 // tile's last token. fp32 inputs take tiles of 16 rows of the streaming form
-// (kda_attn_stream.h), two workgroups to a compute unit: 76 us for 1448 tokens,
-// H = 16, d = 128, against 88 us for tiles of 32 rows, whose registers leave room
-// for one workgroup.
+// (kda_attn_stream.h), two workgroups to a compute unit: 71 us for prompts of
+// 1000, 37 and 411 tokens, H = 16, Hk = 4, d = 128 (tiles of 32 rows, whose registers leave
+// room for one workgroup, were a sixth slower). Each of them stages all its keys and values
+// through registers for those 16 rows, which is what it waits for beside its products.
 #include "kda_attn_rows.h"
 #include "kda_attn_stream.h"
 
@@ -63,11 +64,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_prompt_kernel(AttnArgs a,
 // sums and outputs are joined in LDS in the end.
 //
 // What bounds it: at d = 128 the matrix cores (2 L^2 d H operations for L tokens)
-// under the card's power limit: 7.4 ms for one prompt of 32768, H = 32, Hk = 8 (1190
-// TFLOP/s; a large library product reaches 1385). At d = 64 the softmax, whose vector
-// instructions per score are the same for half the products: 191 us for 4 x 4096, H = Hk
-// = 16 (718 TFLOP/s). Short prompts add what a workgroup cannot overlap, its start and its
-// store: 400 us for 16 prompts of 200 to 4000 tokens, H = 32 (880 TFLOP/s).
+// under the card's power limit: 7.3 to 8.0 ms by the card's state for one prompt of 32768, H =
+// 32, Hk = 8 (1200 to 1100 TFLOP/s; a large library product reaches 1385). At d = 64 the softmax's
+// latencies: its vector instructions per score are the same for half the products, one of a
+// SIMD's two waves issues them at a time, and neither pipe is full (59 % and 32 %): 185 to 198 us
+// for 4 x 4096, H = Hk = 16 (740 to 690 TFLOP/s). Short prompts add each workgroup's start and its
+// store, which nothing overlaps here: 409 to 434 us for 16 prompts of 217 to 3448 tokens, H = 32
+// (860 to 810 TFLOP/s).
 
 constexpr int NW = 8;
 
@@ -280,7 +283,8 @@ hipError_t launch_f32(const AttnArgs &a, hipStream_t st) {
 // 22, 1 x 3500 81 and 53, 4 x 1100 35 and 27; H = 32, Hk = 8: 1 x 65 10.9 and 9.5, 1 x 1100 36
 // and 26); up to two they were if the walks are long (H = 32: 1 x 1500 46 and 38, 1 x 2000 58
 // and 51; H = 8: 1 x 8000 181 and 140; but 16 x 300 18 and 25); beyond, they were slower (H =
-// 32: 1 x 3500 109 and 123, 4 x 1100 66 and 81).
+// 32: 1 x 3500 109 and 123, 4 x 1100 66 and 81). (At d_k = 64, d_v = 128 the halves' form spills 10
+// registers; 1 x 1100, H = 32 takes 21 us there, between 17 at 64 / 64 and 23 at 128 / 128.)
 bool halves(const AttnArgs &a) {
     const int64_t units = compute_units(), tiles = (static_cast<int64_t>(a.T) * a.G / 64 + a.N) * a.Hk / 2;
     return 8 * tiles <= 9 * units || (tiles <= 2 * units && a.T >= static_cast<int64_t>(1024) * a.N);

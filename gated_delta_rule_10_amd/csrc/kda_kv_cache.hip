@@ -1,8 +1,9 @@
 // The paged key/value cache: writing new tokens (kda_kv_write), with the
 // rounding to e4m3 where the cache holds codes, and reading them back
 // (kda_kv_read). Both move each byte once; they are bound by memory.
-// 32768 tokens, Hk = 8, d = 128, bf16 to e4m3 (204 MB each way): written in 55 us (3.7
-// TB/s), read back in 33 us (6.2 TB/s, part of it from the last-level cache).
+// 32768 tokens, Hk = 8, d = 128, bf16 to e4m3 (202 MB each way): written in 54 us (3.7
+// TB/s), read back in 33 us (6.2 TB/s, part of it from the last-level cache). To bf16 (268 MB)
+// 42 and 42 us (6.4 TB/s), fp32 (537 MB) 91 and 133 us (5.9 and 4.0 TB/s).
 //
 // A workgroup takes 64 (token, kv head) rows of keys and of values, d / 8 lanes
 // (8 elements each) to a row. One lane per row finds its place in the cache

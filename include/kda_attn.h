@@ -4,8 +4,11 @@
  *
  * A hybrid stack interleaves KDA layers with full softmax attention (3:1 in
  * the Kimi Linear article, "Kimi Linear爆发背后的秘密：重新定义长上下文推理效率",
- * xugj520.cn). These entry points are that layer's two steps, on the packed
- * variable-length layout of kda.h, and the paged key/value cache between them:
+ * xugj520.cn). These entry points are the two steps of such a layer with grouped
+ * query heads of 64 or 128 channels, on the packed variable-length layout of
+ * kda.h, and the paged key/value cache between them. (The article's own full
+ * layers are MLA, whose expanded keys are wider and whose cache is a latent:
+ * neither is here.)
  *
  *     kda_attn_fwd        causal attention inside each packed sequence (prompt)
  *     kda_kv_write        new keys and values into the paged cache
@@ -158,6 +161,9 @@ kda_status_t kda_kv_read(void *k, void *v, const int32_t *cu_seqlens, int32_t N,
  * dtype pairs as for kda_attn_fwd; F32 inputs with an F32 cache, BF16 inputs
  * with a BF16 or E4M3 one. Sizes: N >= 1, H >= 1, T_total >= 0, 16 N H < 2^31,
  * T_total H + 128 N Hk < 2^27, N max_pages < 2^31, max_pages page_size < 2^31 - 1024.
+ * Meant for single tokens and drafts: chunks of a prompt are right here too, but
+ * without the prompt kernel's overlap. The form is chosen for the whole call, from
+ * the mean number of new tokens.
  * workspace: kda_attn_cache_fwd_workspace_size bytes of device scratch, whatever
  * they hold (NULL if that is 0). Calls that may overlap must not share one.
  */
