@@ -17,12 +17,14 @@ __device__ __forceinline__ f32x16 mma32(bf16x8 a, bf16x8 b, f32x16 c) {
 
 // Copies from memory straight to LDS: 16 (4) bytes per lane from base (wave-uniform) + off, to
 // dst (wave-uniform) + 16 (4) * lane. Unknown to the compiler's wait insertion: awaited by
-// wait_copies() before a barrier. (The clobber keeps the compiler from holding anything in M0
-// across them; its warning only says that it will not save and restore M0.)
+// wait_copies() before a barrier. A scalar base may come from a vector instruction (a spilled
+// register's return), and may be read five wait states later: the s_nop 3. (The clobber keeps
+// the compiler from holding anything in M0 across them; its warning only says that it will not
+// save and restore M0.)
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy_to_lds(uint32_t dst, const void *base, uint32_t off) {
-    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(off), "s"(base) : "memory", "m0");
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(off), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void copy_word_to_lds(uint32_t dst, const void *src) {
     __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(dst), "v"(src) : "memory", "m0");

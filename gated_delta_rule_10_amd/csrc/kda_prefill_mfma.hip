@@ -852,12 +852,14 @@ __device__ __forceinline__ uint64_t uniform_addr(const void *p) {
 }
 // (the clobber keeps the compiler from assuming an M0 value across these; the
 // warning only says it will not save and restore M0 around them)
+// The scalar base comes from a readfirstlane, and may be read five wait states
+// later: the s_nop of the copies that have one (one is enough after M0's write).
 #pragma clang diagnostic push
 #pragma clang diagnostic ignored "-Winline-asm"
 // Record reads (dma16, dma4) are nontemporal: a pass reads each record byte once.
 // 16 bytes per lane from uniform base + per-lane 32-bit offset
 __device__ __forceinline__ void dma16(const void *base, uint32_t voff, const char *lds) {
-    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2 nt"
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2 nt"
                      :
                      : "s"(lds_addr(lds)), "v"(voff), "s"(uniform_addr(base))
                      : "memory", "m0");
@@ -871,7 +873,7 @@ __device__ __forceinline__ void dma16v(const void *addr, const char *lds) {
 }
 // 4 bytes per lane, 64 lanes = 256 B, uniform base + 4 lane
 __device__ __forceinline__ void dma4(const void *base, uint32_t voff, const char *lds) {
-    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2 nt"
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, %2 nt"
                      :
                      : "s"(lds_addr(lds)), "v"(voff), "s"(uniform_addr(base))
                      : "memory", "m0");

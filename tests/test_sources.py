@@ -40,3 +40,14 @@ def test_inline_assembly_names_what_it_writes(name):
     for ops, text in asm_statements(name):
         if re.search(r"s_mov_b32 m0", text):
             assert re.search(r'"m0"', text.split(":")[-1]), text
+
+
+@pytest.mark.parametrize("name", SOURCES)
+def test_copies_wait_for_their_base(name):
+    """A memory instruction may read a scalar base five wait states after a vector instruction wrote it (a
+    readfirstlane, or a spilled register's return); in inline assembly the compiler leaves none of them."""
+    for ops, text in asm_statements(name):
+        if any(op.startswith("global_load") for op in ops) and not re.search(r"global_load\w+ %\d+, off", text):
+            before = text[:text.index("global_load")]
+            states = sum(int(n) + 1 for n in re.findall(r"s_nop (\d+)", before)) + len(re.findall(r"s_mov_b32", before))
+            assert states >= 5, text
