@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libkda.so")
 SOURCES = ["kda_api.cpp", "kda_decode.hip", "kda_prefill_valu.hip", "kda_prefill_mfma.hip",
-           "kda_attn_api.cpp", "kda_attn_prompt.hip", "kda_attn_cache.hip", "kda_kv_cache.hip"]
+           "kda_attn_api.cpp", "kda_attn_prompt.hip", "kda_attn_cache.hip", "kda_kv_cache.hip",
+           "kda_lin_api.cpp", "kda_lin_chunk.hip", "kda_lin_decode.hip", "kda_beam_api.cpp", "kda_beam.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",

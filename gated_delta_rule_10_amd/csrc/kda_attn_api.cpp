@@ -6,26 +6,18 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
-#include <cstring>
 
 #include "kda_attn.h"
 #include "kda_attn_internal.h"
+#include "kda_checks.h"
+
+using namespace kda;
 
 namespace {
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool given(const void *p) { return p && aligned16(p); }
-bool head_dim_ok(int32_t d) { return d == 64 || d == 128; }
-bool dtype_valid(kda_dtype_t d) { return d == KDA_F32 || d == KDA_BF16; }
 bool kv_dtype_valid(kda_kv_dtype_t d) { return d == KDA_KV_F32 || d == KDA_KV_BF16 || d == KDA_KV_E4M3; }
 
-bool dtype_pair_ok(kda_dtype_t in, kda_dtype_t out) { return in == KDA_BF16 || out == KDA_F32; }
 bool kv_pair_ok(kda_dtype_t in, kda_kv_dtype_t kv) { return (in == KDA_F32) == (kv == KDA_KV_F32); }
-
-bool stride_ok(int64_t stride, int64_t heads, int32_t d) {
-    return stride >= heads * d && stride % 8 == 0 && stride <= (int64_t(1) << 24);
-}
 
 // Sizes shared by all entry points. d_k and d_v are checked separately (KDA_ERR_UNSUPPORTED).
 bool sizes_ok(int32_t N, int32_t T, int32_t H, int32_t Hk) {
@@ -60,18 +52,6 @@ kda_status_t check_cache(const kda_kv_cache_t *c, int32_t N) {
     if (static_cast<int64_t>(c->max_pages) * c->page_size >= INT32_MAX - 1023) return KDA_ERR_INVALID_ARG;
     if (static_cast<int64_t>(N) * c->max_pages > INT32_MAX) return KDA_ERR_INVALID_ARG;
     return KDA_OK;
-}
-
-// A call's end: its launch status and, with KDA_DEBUG_SYNC=1 (read once per process), that of
-// its work on `stream`.
-hipError_t finish(hipError_t e, hipStream_t stream) {
-    static const bool wait = [] {
-        const char *x = std::getenv("KDA_DEBUG_SYNC");
-        return x && std::strcmp(x, "1") == 0;
-    }();
-    if (e == hipSuccess && wait) e = hipStreamSynchronize(stream);
-    if (e == hipSuccess && wait) e = hipGetLastError();
-    return e;
 }
 
 // scale in the log2 domain has to be finite too
