@@ -1,0 +1,320 @@
+// The chunk step of kda_lin_chunk.hip for bf16 inputs, on the matrix cores.
+//
+// 64 tokens to a chunk. A wave holds 32 value channels: its part of the state as
+// K / 32 results of 32 x 32 products, S[m] register r of lane l being row
+// 32 m + 8 (r / 4) + 4 (l / 32) + r % 4 (a key channel) and column l % 32 (a value
+// channel). In that form the state feeds products without moving between lanes,
+// if the other operand takes the key channels in the same order:
+//
+//     O^T = S^T Q^T e^(G_i) + V^T P^T        P = (Q K^T) * e^(G_i - G_j), j <= i
+//     S   = e^(G_C) S + K^T (V e^(G_C - G_j))
+//
+// P is formed once per workgroup, 16 rows of it to a wave, and shared in LDS.
+// q, k and v are exact bf16 operands. S and P are two bf16 parts each (16 bits);
+// V e^(..) is three (24 bits, all of fp32): its rounding would stay in the state.
+#pragma once
+
+#include "kda_attn_rows.h"
+#include "kda_lin_device.h"
+
+namespace kda {
+
+// x as a sum of bf16 parts, the first the nearest to it
+__device__ __forceinline__ void split_bf16(float (&x)[8], bf16x8 &part) {
+    part = to_frag(x, bf16x8{});
+    const u32x4 u = __builtin_bit_cast(u32x4, part);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] -= __uint_as_float(u[i] << 16);
+        x[2 * i + 1] -= __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void widen(const bf16x8 &v, float (&x)[8]) {
+    const u32x4 u = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+}
+
+template <int K, int V, bool OUT> struct LinBf16 {
+    using T = bf16_t;
+    static constexpr int C = 64, NW = V / 32, NT = 64 * NW, M = K / 32, kRegs = 16;
+    static constexpr int CK = K / 8, CV = V / 8;          // 16-byte pieces of a row
+    static constexpr int LK = C * CK / NT, LV = C * CV / NT;  // of a thread
+    static constexpr int kQ = 0, kK = OUT ? C * K * 2 : 0, kV = kK + C * K * 2, kP = kV + C * V * 2;
+    static constexpr int kLds = kP + (OUT ? 2 * C * C * 2 : 0);
+
+    // Piece c of token t lies at piece c ^ swz(t) of its row: 16 rows read at one piece, and 4 rows
+    // read at 4 pieces (the transposing reads), fall on different banks.
+    static __device__ __forceinline__ int swz16(int t) { return ((t & 3) << 2) | ((t >> 2) & 3); }
+    static __device__ __forceinline__ int swz8(int t) { return (((t >> 1) & 1) << 2) | ((t >> 2) & 3); }
+    template <int CH> static __device__ __forceinline__ int at(int t, int c) {
+        return t * (CH * 16) + 16 * (c ^ (CH == 16 ? swz16(t) : swz8(t)));
+    }
+
+    u32x4 q[OUT ? LK : 1], k[LK], v[LV];  // the next chunk, on its way
+    f32x16 S[M];
+
+    // a state of zeros, and zeros where no chunk writes scores: right of the diagonal's 16 x 16 tiles
+    __device__ __forceinline__ void clear(char *lds, int tid) {
+        if (OUT)
+            for (int i = tid; i < 2 * C * 8; i += NT) *reinterpret_cast<u32x4 *>(lds + kP + 16 * i) = u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) S[m][r] = 0.f;
+    }
+
+    template <int CH, int L> static __device__ __forceinline__ void load_rows(u32x4 (&x)[L], const T *p, int64_t stride, int count, int tid) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            const int t = (i * NT + tid) / CH, c = tid % CH;
+            x[i] = t < count ? *reinterpret_cast<const u32x4 *>(p + t * stride + 8 * c) : u32x4{0, 0, 0, 0};
+        }
+    }
+    template <int CH, int L> static __device__ __forceinline__ void store_rows(const u32x4 (&x)[L], char *p, int tid) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) *reinterpret_cast<u32x4 *>(p + at<CH>((i * NT + tid) / CH, tid % CH)) = x[i];
+    }
+    // rows of the chunk that starts at these; zeros from row `count` on
+    __device__ __forceinline__ void load(const T *qp, const T *kp, const T *vp, const LinArgs &a, int count, int tid) {
+        if (OUT) load_rows<CK>(q, qp, a.qs, count, tid);
+        load_rows<CK>(k, kp, a.ks, count, tid);
+        load_rows<CV>(v, vp, a.vs, count, tid);
+    }
+    // whether some of this thread's values is an infinity or NaN
+    __device__ __forceinline__ bool to_lds(char *lds, int tid) {
+        if (OUT) store_rows<CK>(q, lds + kQ, tid);
+        store_rows<CK>(k, lds + kK, tid);
+        store_rows<CV>(v, lds + kV, tid);
+        uint32_t odd = 0;
+#pragma unroll
+        for (int i = 0; i < LV; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) odd |= not_finite<bf16_t>(v[i][j]);
+        return odd != 0;
+    }
+
+    // rows (16-byte pieces of) 32 d + l % 32 of the transposed tile, tokens 16 x + {0..3, 8..11} + 4 (l / 32)
+    template <int CH> static __device__ __forceinline__ bf16x8 transposed(const char *p, int x, int d, int lane) {
+        typedef __attribute__((address_space(3))) i16x4 lds4;
+        const int i = lane & 15, t = 16 * x + 4 * (lane >> 5) + (i >> 2);
+        const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
+        const bf16x4 y = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(p + at<CH>(t, c) + 8 * (i & 1))));
+        const bf16x4 z = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(p + at<CH>(t + 8, c) + 8 * (i & 1))));
+        return (bf16x8){y[0], y[1], y[2], y[3], z[0], z[1], z[2], z[3]};
+    }
+    // row t, elements 16 x + {0..3, 8..11} + 4 half
+    template <int CH> static __device__ __forceinline__ bf16x8 halves(const char *p, int x, int t, int half) {
+        const bf16x4 y = *reinterpret_cast<const bf16x4 *>(p + at<CH>(t, 2 * x) + 8 * half);
+        const bf16x4 z = *reinterpret_cast<const bf16x4 *>(p + at<CH>(t, 2 * x + 1) + 8 * half);
+        return (bf16x8){y[0], y[1], y[2], y[3], z[0], z[1], z[2], z[3]};
+    }
+
+    // 16 rows of P, from row 16 s on, as two bf16 parts in LDS
+    static __device__ __forceinline__ void scores(char *lds, const Decays &d, int s, int lane) {
+        const int i = 16 * s + (lane & 15), g = lane >> 4;
+        bf16x8 qf[K / 32];
+#pragma unroll
+        for (int x = 0; x < K / 32; ++x) qf[x] = *reinterpret_cast<const bf16x8 *>(lds + kQ + at<CK>(i, 4 * x + g));
+        const float hi = d.hi[i], lo = d.lo[i];
+#pragma unroll 1
+        for (int j0 = 0; j0 <= 16 * s; j0 += 16) {
+            f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < K / 32; ++x)
+                p = mma16(*reinterpret_cast<const bf16x8 *>(lds + kK + at<CK>(j0 + (lane & 15), 4 * x + g)), qf[x], p);
+            const int j = j0 + 4 * g;  // p[r]: column j + r
+            const f32x4 dh = *reinterpret_cast<const f32x4 *>(d.hi + j), dl = *reinterpret_cast<const f32x4 *>(d.lo + j);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                p[r] = j + r <= i ? p[r] * __builtin_amdgcn_exp2f((hi - dh[r]) + (lo - dl[r])) : 0.f;
+            const bf16x2 a = pack_bf16(p[0], p[1]), b = pack_bf16(p[2], p[3]);
+            const bf16x2 e = pack_bf16(p[0] - static_cast<float>(a[0]), p[1] - static_cast<float>(a[1]));
+            const bf16x2 f = pack_bf16(p[2] - static_cast<float>(b[0]), p[3] - static_cast<float>(b[1]));
+            const int to = at<8>(i, j >> 3) + 8 * (g & 1);
+            *reinterpret_cast<bf16x4 *>(lds + kP + to) = (bf16x4){a[0], a[1], b[0], b[1]};
+            *reinterpret_cast<bf16x4 *>(lds + kP + C * C * 2 + to) = (bf16x4){e[0], e[1], f[0], f[1]};
+        }
+    }
+
+    // O^T (channels 32 w + ..) from the state before the chunk: column l % 32 is token 32 b + l % 32
+    __device__ __forceinline__ void from_state(f32x16 (&o)[2], const char *lds, const Decays &d, int lane) const {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[b][r] = 0.f;
+#pragma unroll
+        for (int x = 0; x < K / 16; ++x) {
+            float s[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] = S[x / 2][8 * (x & 1) + i];
+            bf16x8 p[2];
+            split_bf16(s, p[0]);
+            p[1] = to_frag(s, bf16x8{});
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const bf16x8 f = halves<CK>(lds + kQ, x, 32 * b + (lane & 31), lane >> 5);
+                o[b] = mma32(p[0], f, o[b]);
+                o[b] = mma32(p[1], f, o[b]);
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const float e = d.grown[32 * b + (lane & 31)];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[b][r] *= e;
+        }
+    }
+
+    // adds V^T P^T; a product of a masked score's 0 with an infinity or NaN would be NaN, so such
+    // values are taken out of it and added to the rows that they reach one by one
+    static __device__ __forceinline__ void from_chunk(f32x16 (&o)[2], const bf16x8 (&vf)[4], bool strange, const char *lds, int w, int lane) {
+        const int half = lane >> 5;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            bf16x8 f = vf[x];
+            if (strange) {
+                u32x4 u = __builtin_bit_cast(u32x4, f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u[i] &= ~((not_finite<bf16_t>(u[i]) >> 15) * 0xFFFFu);
+                f = __builtin_bit_cast(bf16x8, u);
+            }
+#pragma unroll
+            for (int b = x / 2; b < 2; ++b)
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+                    o[b] = mma32(f, halves<8>(lds + kP + part * C * C * 2, x, 32 * b + (lane & 31), half), o[b]);
+        }
+        if (!strange) return;
+#pragma unroll 1
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int i = 32 * b + (lane & 31), p = kP + at<8>(i, j >> 3) + 2 * (j & 7);
+                const float s = bf16_to_f32(*reinterpret_cast<const bf16_t *>(lds + p)) +
+                                bf16_to_f32(*reinterpret_cast<const bf16_t *>(lds + p + C * C * 2));
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int c = 32 * w + 8 * (r >> 2) + 4 * half + (r & 3);
+                    const float x = bf16_to_f32(*reinterpret_cast<const bf16_t *>(lds + kV + at<CV>(j, c >> 3) + 2 * (c & 7)));
+                    if (j <= i && !(fabsf(x) < INFINITY)) o[b][r] += s * x;
+                }
+            }
+    }
+
+    // rows of o through the wave's own columns of v's tile, whose values are in registers by now
+    static __device__ __forceinline__ void store(bf16_t *out, int64_t stride, const f32x16 (&o)[2], float scale, char *lds, int count, int w, int lane) {
+        const int half = lane >> 5;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const bf16x2 x = pack_bf16(scale * o[b][4 * c], scale * o[b][4 * c + 1]), y = pack_bf16(scale * o[b][4 * c + 2], scale * o[b][4 * c + 3]);
+                *reinterpret_cast<bf16x4 *>(lds + kV + at<CV>(32 * b + (lane & 31), 4 * w + c) + 8 * half) = (bf16x4){x[0], x[1], y[0], y[1]};
+            }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = 16 * i + (lane >> 2), c = 4 * w + (lane & 3);
+            const u32x4 x = *reinterpret_cast<const u32x4 *>(lds + kV + at<CV>(t, c));
+            if (t < count) *reinterpret_cast<u32x4 *>(out + t * stride + 8 * c) = x;
+        }
+    }
+    static __device__ __forceinline__ void store(float *out, int64_t stride, const f32x16 (&o)[2], float scale, char *, int count, int w, int lane) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int t = 32 * b + (lane & 31);
+            if (t >= count) continue;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<f32x4 *>(out + t * stride + 32 * w + 8 * c + 4 * (lane >> 5)) =
+                    (f32x4){scale * o[b][4 * c], scale * o[b][4 * c + 1], scale * o[b][4 * c + 2], scale * o[b][4 * c + 3]};
+        }
+    }
+
+    // S = e^(G_C) S + K^T (V e^(G_C - G_j))
+    __device__ __forceinline__ void update(const bf16x8 (&vf)[4], const char *lds, const Decays &d, int lane) {
+        const int half = lane >> 5;
+        const float all = d.grown[C - 1];
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) S[m][r] *= all;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            float f[8];
+            widen(vf[x], f);
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(d.left + 16 * x + 4 * half), b = *reinterpret_cast<const f32x4 *>(d.left + 16 * x + 8 + 4 * half);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[i] *= a[i];
+                f[4 + i] *= b[i];
+            }
+            bf16x8 p[3];
+            split_bf16(f, p[0]);
+            split_bf16(f, p[1]);
+            p[2] = to_frag(f, bf16x8{});
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const bf16x8 kf = transposed<CK>(lds + kK, x, m, lane);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) S[m] = mma32(kf, p[i], S[m]);
+            }
+        }
+    }
+
+    // one chunk, whose tiles are in LDS
+    template <typename TOut>
+    __device__ __forceinline__ void chunk(TOut *out, int64_t stride, float scale, char *lds, const Decays &d, bool strange, int count, int w, int lane) {
+        f32x16 o[2];
+        if (OUT) {
+            // rows 16 s of P take s + 1 products of 16 columns: an even share for two waves
+            if (NW == 4) {
+                scores(lds, d, w, lane);
+            } else {
+                scores(lds, d, w, lane);
+                scores(lds, d, 3 - w, lane);
+            }
+            from_state(o, lds, d, lane);
+            __syncthreads();
+        }
+        bf16x8 vf[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) vf[x] = transposed<CV>(lds + kV, x, w, lane);
+        if (OUT) {
+            from_chunk(o, vf, strange, lds, w, lane);
+            store(out, stride, o, scale, lds, count, w, lane);
+        }
+        update(vf, lds, d, lane);
+    }
+
+    // the state as the registers hold it, in memory
+    __device__ __forceinline__ void put(float *p, int w, int lane) const {
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                *reinterpret_cast<f32x4 *>(p + (((w * M + m) * 4 + r) * 64 + lane) * 4) =
+                    (f32x4){S[m][4 * r], S[m][4 * r + 1], S[m][4 * r + 2], S[m][4 * r + 3]};
+    }
+    __device__ __forceinline__ void get(const float *p, int w, int lane) {
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const f32x4 x = *reinterpret_cast<const f32x4 *>(p + (((w * M + m) * 4 + r) * 64 + lane) * 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) S[m][4 * r + i] = x[i];
+            }
+    }
+
+    // register r of S[m] and the element of a [K, V] state
+    static __device__ __forceinline__ int element(int m, int r, int w, int lane) {
+        return (32 * m + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * V + 32 * w + (lane & 31);
+    }
+};
+
+}  // namespace kda

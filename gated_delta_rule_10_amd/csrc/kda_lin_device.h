@@ -23,6 +23,13 @@ __device__ __forceinline__ int slot_of(const LinArgs &a, int n) {
     return s >= 0 && s < a.nslots ? s : -1;
 }
 
+// What a chunk's tokens keep, in LDS. With G the inclusive sums of log2 e^g over the chunk: G in two
+// fp32 parts (so that differences, which may be small between large sums, are right to fp32), e^G,
+// and e^(G of the last token - G).
+struct Decays {
+    const float *hi, *lo, *grown, *left;
+};
+
 // fp32 to an output element: bf16 to nearest even, a NaN stays one
 __device__ __forceinline__ void store_out(float *p, float x) { *p = x; }
 __device__ __forceinline__ void store_out(bf16_t *p, float x) {
