@@ -38,6 +38,14 @@ __device__ __forceinline__ void widen(const bf16x8 &v, float (&x)[8]) {
     }
 }
 
+// The lane's number as a value that the compiler does not see through: addresses in LDS, an exclusive
+// or away from it, are then made where they are used instead of being kept over the chunks, which
+// takes more registers than there are.
+__device__ __forceinline__ int opaque(int lane) {
+    __asm__ volatile("" : "+v"(lane));
+    return lane;
+}
+
 template <int K, int V, bool OUT> struct LinBf16 {
     using T = bf16_t;
     static constexpr int C = 64, NW = V / 32, NT = 64 * NW, M = K / 32, kRegs = 16;
@@ -115,6 +123,7 @@ template <int K, int V, bool OUT> struct LinBf16 {
 
     // 16 rows of P, from row 16 s on, as two bf16 parts in LDS
     static __device__ __forceinline__ void scores(char *lds, const Decays &d, int s, int lane) {
+        lane = opaque(lane);
         const int i = 16 * s + (lane & 15), g = lane >> 4;
         bf16x8 qf[K / 32];
 #pragma unroll
@@ -142,6 +151,7 @@ template <int K, int V, bool OUT> struct LinBf16 {
 
     // O^T (channels 32 w + ..) from the state before the chunk: column l % 32 is token 32 b + l % 32
     __device__ __forceinline__ void from_state(f32x16 (&o)[2], const char *lds, const Decays &d, int lane) const {
+        lane = opaque(lane);
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -154,12 +164,13 @@ template <int K, int V, bool OUT> struct LinBf16 {
             bf16x8 p[2];
             split_bf16(s, p[0]);
             p[1] = to_frag(s, bf16x8{});
+            bf16x8 f[2];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const bf16x8 f = halves<CK>(lds + kQ, x, 32 * b + (lane & 31), lane >> 5);
-                o[b] = mma32(p[0], f, o[b]);
-                o[b] = mma32(p[1], f, o[b]);
-            }
+            for (int b = 0; b < 2; ++b) f[b] = halves<CK>(lds + kQ, x, 32 * b + (lane & 31), lane >> 5);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) o[b] = mma32(p[i], f[b], o[b]);
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
@@ -172,6 +183,7 @@ template <int K, int V, bool OUT> struct LinBf16 {
     // adds V^T P^T; a product of a masked score's 0 with an infinity or NaN would be NaN, so such
     // values are taken out of it and added to the rows that they reach one by one
     static __device__ __forceinline__ void from_chunk(f32x16 (&o)[2], const bf16x8 (&vf)[4], bool strange, const char *lds, int w, int lane) {
+        lane = opaque(lane);
         const int half = lane >> 5;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
@@ -183,9 +195,9 @@ template <int K, int V, bool OUT> struct LinBf16 {
                 f = __builtin_bit_cast(bf16x8, u);
             }
 #pragma unroll
-            for (int b = x / 2; b < 2; ++b)
+            for (int part = 0; part < 2; ++part)
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                for (int b = x / 2; b < 2; ++b)
                     o[b] = mma32(f, halves<8>(lds + kP + part * C * C * 2, x, 32 * b + (lane & 31), half), o[b]);
         }
         if (!strange) return;
@@ -207,6 +219,7 @@ template <int K, int V, bool OUT> struct LinBf16 {
 
     // rows of o through the wave's own columns of v's tile, whose values are in registers by now
     static __device__ __forceinline__ void store(bf16_t *out, int64_t stride, const f32x16 (&o)[2], float scale, char *lds, int count, int w, int lane) {
+        lane = opaque(lane);
         const int half = lane >> 5;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
@@ -237,6 +250,7 @@ template <int K, int V, bool OUT> struct LinBf16 {
 
     // S = e^(G_C) S + K^T (V e^(G_C - G_j))
     __device__ __forceinline__ void update(const bf16x8 (&vf)[4], const char *lds, const Decays &d, int lane) {
+        lane = opaque(lane);
         const int half = lane >> 5;
         const float all = d.grown[C - 1];
 #pragma unroll
@@ -257,18 +271,19 @@ template <int K, int V, bool OUT> struct LinBf16 {
             split_bf16(f, p[0]);
             split_bf16(f, p[1]);
             p[2] = to_frag(f, bf16x8{});
+            bf16x8 kf[M];
 #pragma unroll
-            for (int m = 0; m < M; ++m) {
-                const bf16x8 kf = transposed<CK>(lds + kK, x, m, lane);
+            for (int m = 0; m < M; ++m) kf[m] = transposed<CK>(lds + kK, x, m, lane);
 #pragma unroll
-                for (int i = 0; i < 3; ++i) S[m] = mma32(kf, p[i], S[m]);
-            }
+            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                for (int m = 0; m < M; ++m) S[m] = mma32(kf[m], p[i], S[m]);
         }
     }
 
-    // one chunk, whose tiles are in LDS
-    template <typename TOut>
-    __device__ __forceinline__ void chunk(TOut *out, int64_t stride, float scale, char *lds, const Decays &d, bool strange, int count, int w, int lane) {
+    // one chunk, whose tiles are in LDS; odd: not 0 if some value is an infinity or NaN
+    template <typename TOut, typename Next>
+    __device__ __forceinline__ void chunk(TOut *out, int64_t stride, float scale, char *lds, const Decays &d, const int &odd, int count, int w, int lane, Next next) {
         f32x16 o[2];
         if (OUT) {
             // rows 16 s of P take s + 1 products of 16 columns: an even share for two waves
@@ -281,11 +296,12 @@ template <int K, int V, bool OUT> struct LinBf16 {
             from_state(o, lds, d, lane);
             __syncthreads();
         }
+        if (OUT) next();  // the loads of the next chunk leave
         bf16x8 vf[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) vf[x] = transposed<CV>(lds + kV, x, w, lane);
+        for (int x = 0; x < 4; ++x) vf[x] = transposed<CV>(lds + kV, x, w, opaque(lane));
         if (OUT) {
-            from_chunk(o, vf, strange, lds, w, lane);
+            from_chunk(o, vf, odd != 0, lds, w, lane);
             store(out, stride, o, scale, lds, count, w, lane);
         }
         update(vf, lds, d, lane);

@@ -130,15 +130,18 @@ __global__ __launch_bounds__(W::NT, 2) void lin_segments_kernel(LinArgs a, Segme
         const int b = c & 1, rows = min(C, tokens - c * C);
         __syncthreads();  // all have read the chunk before
         if (s.to_lds(lds, tid)) strange[b] = 1;
-        qp += C * a.qs, kp += C * a.ks, vp += C * a.vs;
-        if (c + 1 < chunks) s.load(qp, kp, vp, a, min(C, tokens - (c + 1) * C), tid);
+        auto next = [&] {
+            qp += C * a.qs, kp += C * a.ks, vp += C * a.vs;
+            if (c + 1 < chunks) s.load(qp, kp, vp, a, min(C, tokens - (c + 1) * C), tid);
+        };
+        if (!OUT) next();
         __syncthreads();
         if (w == 0 && c + 1 < chunks) {
             tabulate(g, b ^ 1);
             if (c + 2 < chunks) g = decay(c + 2);
         }
         const Decays d = {table[b][0], table[b][1], table[b][2], table[b][3]};
-        s.template chunk<TOut>(op, static_cast<int64_t>(a.H) * V, a.scale, lds, d, strange[b] != 0, rows, w, lane);
+        s.template chunk<TOut>(op, static_cast<int64_t>(a.H) * V, a.scale, lds, d, strange[b], rows, w, lane, next);
         op += static_cast<int64_t>(C) * a.H * V;
     }
     if (OUT) {
