@@ -1,10 +1,11 @@
 // The chunk step of kda_lin_chunk.hip for bf16 inputs, on the matrix cores.
 //
 // 64 tokens to a chunk. A wave holds 32 value channels: its part of the state as
-// K / 32 results of 32 x 32 products, S[m] register r of lane l being row
-// 32 m + 8 (r / 4) + 4 (l / 32) + r % 4 (a key channel) and column l % 32 (a value
-// channel). In that form the state feeds products without moving between lanes,
-// if the other operand takes the key channels in the same order:
+// K / 32 results of 32 x 32 products, S[m] register r of lane l being value channel
+// l % 32 and key channel 32 m + 16 (r / 8) + 8 (l / 32) + r % 8: the rows of these
+// products are taken in an order that leaves 8 neighbouring key channels in a lane.
+// In that form the state feeds products without moving between lanes, and what it
+// is multiplied with is read 16 bytes at a time:
 //
 //     O^T = S^T Q^T e^(G_i) + V^T P^T        P = (Q K^T) * e^(G_i - G_j), j <= i
 //     S   = e^(G_C) S + K^T (V e^(G_C - G_j))
@@ -19,14 +20,27 @@
 
 namespace kda {
 
-// x as a sum of bf16 parts, the first the nearest to it
+// x as a sum of bf16 parts, the first the nearest to it; x keeps what is left. The subtraction is a
+// dot product of two with (-1, 0) or (0, -1), one instruction instead of an unpacking and a
+// difference, and exact: what is left has fewer bits than x.
+// (The factors are in scalar registers: as an inline constant, -1.0 is not the pair (-1, 0).)
+__device__ __forceinline__ float less_first(bf16x2 p, float x) {
+    uint32_t f = 0x0000BF80u;
+    __asm__("" : "+s"(f));
+    return __builtin_amdgcn_fdot2_f32_bf16(p, __builtin_bit_cast(bf16x2, f), x, false);
+}
+__device__ __forceinline__ float less_second(bf16x2 p, float x) {
+    uint32_t f = 0xBF800000u;
+    __asm__("" : "+s"(f));
+    return __builtin_amdgcn_fdot2_f32_bf16(p, __builtin_bit_cast(bf16x2, f), x, false);
+}
 __device__ __forceinline__ void split_bf16(float (&x)[8], bf16x8 &part) {
     part = to_frag(x, bf16x8{});
-    const u32x4 u = __builtin_bit_cast(u32x4, part);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        x[2 * i] -= __uint_as_float(u[i] << 16);
-        x[2 * i + 1] -= __uint_as_float(u[i] & 0xFFFF0000u);
+        const bf16x2 p = {part[2 * i], part[2 * i + 1]};
+        x[2 * i] = less_first(p, x[2 * i]);
+        x[2 * i + 1] = less_second(p, x[2 * i + 1]);
     }
 }
 __device__ __forceinline__ void widen(const bf16x8 &v, float (&x)[8]) {
@@ -75,18 +89,27 @@ template <int K, int V, bool OUT> struct LinBf16 {
             for (int r = 0; r < 16; ++r) S[m][r] = 0.f;
     }
 
+    // Rows from `count` on are the last one again: their scores are masked and their values weigh 0.
     template <int CH, int L> static __device__ __forceinline__ void load_rows(u32x4 (&x)[L], const T *p, int64_t stride, int count, int tid) {
+        const char *base = reinterpret_cast<const char *>(p);
+        constexpr int STEP = NT / CH;  // rows from one load to the next
+        if (count == C) {
+            const uint32_t off = static_cast<uint32_t>(tid / CH) * static_cast<uint32_t>(2 * stride) + 16 * (tid % CH);
 #pragma unroll
-        for (int i = 0; i < L; ++i) {
-            const int t = (i * NT + tid) / CH, c = tid % CH;
-            x[i] = t < count ? *reinterpret_cast<const u32x4 *>(p + t * stride + 8 * c) : u32x4{0, 0, 0, 0};
+            for (int i = 0; i < L; ++i) x[i] = *reinterpret_cast<const u32x4 *>(base + i * STEP * 2 * stride + off);
+        } else {
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const uint32_t t = min(i * STEP + tid / CH, count - 1);
+                x[i] = *reinterpret_cast<const u32x4 *>(base + t * static_cast<uint32_t>(2 * stride) + 16 * (tid % CH));
+            }
         }
     }
     template <int CH, int L> static __device__ __forceinline__ void store_rows(const u32x4 (&x)[L], char *p, int tid) {
 #pragma unroll
         for (int i = 0; i < L; ++i) *reinterpret_cast<u32x4 *>(p + at<CH>((i * NT + tid) / CH, tid % CH)) = x[i];
     }
-    // rows of the chunk that starts at these; zeros from row `count` on
+    // rows of the chunk that starts at these
     __device__ __forceinline__ void load(const T *qp, const T *kp, const T *vp, const LinArgs &a, int count, int tid) {
         if (OUT) load_rows<CK>(q, qp, a.qs, count, tid);
         load_rows<CK>(k, kp, a.ks, count, tid);
@@ -105,44 +128,46 @@ template <int K, int V, bool OUT> struct LinBf16 {
         return odd != 0;
     }
 
-    // rows (16-byte pieces of) 32 d + l % 32 of the transposed tile, tokens 16 x + {0..3, 8..11} + 4 (l / 32)
-    template <int CH> static __device__ __forceinline__ bf16x8 transposed(const char *p, int x, int d, int lane) {
+    // Columns 32 d .. of a tile as rows of a product, tokens 16 x + 8 (l / 32) + 0..7. Each read gives 16
+    // lanes 4 tokens of 16 columns, 4 neighbouring ones from the address of every fourth lane. Of the
+    // 8 groups of 4 rows of a product, the 2nd and 3rd (6th and 7th) change places where `swap`.
+    template <int CH, bool SWAP> static __device__ __forceinline__ bf16x8 transposed(const char *p, int x, int d, int lane) {
         typedef __attribute__((address_space(3))) i16x4 lds4;
-        const int i = lane & 15, t = 16 * x + 4 * (lane >> 5) + (i >> 2);
-        const int c = 4 * d + 2 * ((lane >> 4) & 1) + ((i >> 1) & 1);
-        const bf16x4 y = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(p + at<CH>(t, c) + 8 * (i & 1))));
-        const bf16x4 z = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(p + at<CH>(t + 8, c) + 8 * (i & 1))));
+        const int i = lane & 15, t = 16 * x + 8 * (lane >> 5) + (i >> 2);
+        const int hi = SWAP ? i & 1 : (i >> 1) & 1, lo = SWAP ? (i >> 1) & 1 : i & 1;
+        const int c = 4 * d + 2 * ((lane >> 4) & 1) + hi;
+        const bf16x4 y = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(p + at<CH>(t, c) + 8 * lo)));
+        const bf16x4 z = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(p + at<CH>(t + 4, c) + 8 * lo)));
         return (bf16x8){y[0], y[1], y[2], y[3], z[0], z[1], z[2], z[3]};
     }
-    // row t, elements 16 x + {0..3, 8..11} + 4 half
-    template <int CH> static __device__ __forceinline__ bf16x8 halves(const char *p, int x, int t, int half) {
-        const bf16x4 y = *reinterpret_cast<const bf16x4 *>(p + at<CH>(t, 2 * x) + 8 * half);
-        const bf16x4 z = *reinterpret_cast<const bf16x4 *>(p + at<CH>(t, 2 * x + 1) + 8 * half);
-        return (bf16x8){y[0], y[1], y[2], y[3], z[0], z[1], z[2], z[3]};
+    // row t, elements 16 x + 8 half + 0..7
+    template <int CH> static __device__ __forceinline__ bf16x8 eight(const char *p, int x, int t, int half) {
+        return *reinterpret_cast<const bf16x8 *>(p + at<CH>(t, 2 * x + half));
     }
 
-    // 16 rows of P, from row 16 s on, as two bf16 parts in LDS
-    static __device__ __forceinline__ void scores(char *lds, const Decays &d, int s, int lane) {
+    // The 10 tiles of 16 x 16 of P on and below the diagonal, 3 to each of four waves or 5 to each of
+    // two (a wave of fewer does its last one again), as two bf16 parts in LDS.
+    static __device__ __forceinline__ void scores(char *lds, const Decays &d, float scale, int w, int lane) {
         lane = opaque(lane);
-        const int i = 16 * s + (lane & 15), g = lane >> 4;
-        bf16x8 qf[K / 32];
+        const int l = lane & 15, g = lane >> 4;
+        constexpr int N = NW == 4 ? 3 : 5;
 #pragma unroll
-        for (int x = 0; x < K / 32; ++x) qf[x] = *reinterpret_cast<const bf16x8 *>(lds + kQ + at<CK>(i, 4 * x + g));
-        const float hi = d.hi[i], lo = d.lo[i];
-#pragma unroll 1
-        for (int j0 = 0; j0 <= 16 * s; j0 += 16) {
+        for (int k = 0; k < N; ++k) {
+            const int i0 = 16 * (NW == 4 ? (w == 0 && k > 0 ? 3 : w) : w == 0 ? (k + 1) / 2 : k == 0 ? 2 : 3);
+            const int j0 = 16 * (NW == 4 ? (w == 0 ? 0 : w == 1 ? min(k, 1) : w == 2 ? k : k + 1) : w == 0 ? (k == 2 || k == 4) : k == 0 ? 2 : k - 1);
             f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int x = 0; x < K / 32; ++x)
-                p = mma16(*reinterpret_cast<const bf16x8 *>(lds + kK + at<CK>(j0 + (lane & 15), 4 * x + g)), qf[x], p);
-            const int j = j0 + 4 * g;  // p[r]: column j + r
+                p = mma16(*reinterpret_cast<const bf16x8 *>(lds + kK + at<CK>(j0 + l, 4 * x + g)),
+                          *reinterpret_cast<const bf16x8 *>(lds + kQ + at<CK>(i0 + l, 4 * x + g)), p);
+            const int i = i0 + l, j = j0 + 4 * g;  // p[r]: row i, column j + r
+            const float hi = d.hi[i], lo = d.lo[i];
             const f32x4 dh = *reinterpret_cast<const f32x4 *>(d.hi + j), dl = *reinterpret_cast<const f32x4 *>(d.lo + j);
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                p[r] = j + r <= i ? p[r] * __builtin_amdgcn_exp2f((hi - dh[r]) + (lo - dl[r])) : 0.f;
+                p[r] = j + r <= i ? p[r] * (scale * __builtin_amdgcn_exp2f((hi - dh[r]) + (lo - dl[r]))) : 0.f;
             const bf16x2 a = pack_bf16(p[0], p[1]), b = pack_bf16(p[2], p[3]);
-            const bf16x2 e = pack_bf16(p[0] - static_cast<float>(a[0]), p[1] - static_cast<float>(a[1]));
-            const bf16x2 f = pack_bf16(p[2] - static_cast<float>(b[0]), p[3] - static_cast<float>(b[1]));
+            const bf16x2 e = pack_bf16(less_first(a, p[0]), less_second(a, p[1])), f = pack_bf16(less_first(b, p[2]), less_second(b, p[3]));
             const int to = at<8>(i, j >> 3) + 8 * (g & 1);
             *reinterpret_cast<bf16x4 *>(lds + kP + to) = (bf16x4){a[0], a[1], b[0], b[1]};
             *reinterpret_cast<bf16x4 *>(lds + kP + C * C * 2 + to) = (bf16x4){e[0], e[1], f[0], f[1]};
@@ -150,12 +175,9 @@ template <int K, int V, bool OUT> struct LinBf16 {
     }
 
     // O^T (channels 32 w + ..) from the state before the chunk: column l % 32 is token 32 b + l % 32
-    __device__ __forceinline__ void from_state(f32x16 (&o)[2], const char *lds, const Decays &d, int lane) const {
+    __device__ __forceinline__ void from_state(f32x16 (&o)[2], const char *lds, const Decays &d, float scale, int lane) const {
         lane = opaque(lane);
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) o[b][r] = 0.f;
+        const f32x16 zero = {};
 #pragma unroll
         for (int x = 0; x < K / 16; ++x) {
             float s[8];
@@ -166,41 +188,45 @@ template <int K, int V, bool OUT> struct LinBf16 {
             p[1] = to_frag(s, bf16x8{});
             bf16x8 f[2];
 #pragma unroll
-            for (int b = 0; b < 2; ++b) f[b] = halves<CK>(lds + kQ, x, 32 * b + (lane & 31), lane >> 5);
+            for (int b = 0; b < 2; ++b) f[b] = eight<CK>(lds + kQ, x, 32 * b + (lane & 31), lane >> 5);
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) o[b] = mma32(p[i], f[b], o[b]);
+                for (int b = 0; b < 2; ++b) o[b] = mma32(p[i], f[b], x + i == 0 ? zero : o[b]);
         }
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const float e = d.grown[32 * b + (lane & 31)];
+            const float e = scale * d.grown[32 * b + (lane & 31)];
 #pragma unroll
             for (int r = 0; r < 16; ++r) o[b][r] *= e;
         }
     }
 
-    // adds V^T P^T; a product of a masked score's 0 with an infinity or NaN would be NaN, so such
-    // values are taken out of it and added to the rows that they reach one by one
-    static __device__ __forceinline__ void from_chunk(f32x16 (&o)[2], const bf16x8 (&vf)[4], bool strange, const char *lds, int w, int lane) {
+    // adds V^T P^T
+    static __device__ __forceinline__ void from_chunk(f32x16 (&o)[2], const bf16x8 (&vf)[4], const char *lds, int lane) {
         lane = opaque(lane);
-        const int half = lane >> 5;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            bf16x8 f = vf[x];
-            if (strange) {
-                u32x4 u = __builtin_bit_cast(u32x4, f);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) u[i] &= ~((not_finite<bf16_t>(u[i]) >> 15) * 0xFFFFu);
-                f = __builtin_bit_cast(bf16x8, u);
-            }
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int b = x / 2; b < 2; ++b)
-                    o[b] = mma32(f, halves<8>(lds + kP + part * C * C * 2, x, 32 * b + (lane & 31), half), o[b]);
+                    o[b] = mma32(vf[x], eight<8>(lds + kP + part * C * C * 2, x, 32 * b + (lane & 31), lane >> 5), o[b]);
+    }
+    // The same where some value is an infinity or NaN: a masked score's 0 times it would be NaN, so such
+    // values are taken out of the products and added to the rows that they reach one by one.
+    static __device__ __forceinline__ void from_odd_chunk(f32x16 (&o)[2], const bf16x8 (&vf)[4], const char *lds, int w, int lane) {
+        bf16x8 fine[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            u32x4 u = __builtin_bit_cast(u32x4, vf[x]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] &= ~((not_finite<bf16_t>(u[i]) >> 15) * 0xFFFFu);
+            fine[x] = __builtin_bit_cast(bf16x8, u);
         }
-        if (!strange) return;
+        from_chunk(o, fine, lds, lane);
+        lane = opaque(lane);
+        const int half = lane >> 5;
 #pragma unroll 1
         for (int j = 0; j < C; ++j)
 #pragma unroll
@@ -218,14 +244,14 @@ template <int K, int V, bool OUT> struct LinBf16 {
     }
 
     // rows of o through the wave's own columns of v's tile, whose values are in registers by now
-    static __device__ __forceinline__ void store(bf16_t *out, int64_t stride, const f32x16 (&o)[2], float scale, char *lds, int count, int w, int lane) {
+    static __device__ __forceinline__ void store(bf16_t *out, int64_t stride, const f32x16 (&o)[2], char *lds, int count, int w, int lane) {
         lane = opaque(lane);
         const int half = lane >> 5;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const bf16x2 x = pack_bf16(scale * o[b][4 * c], scale * o[b][4 * c + 1]), y = pack_bf16(scale * o[b][4 * c + 2], scale * o[b][4 * c + 3]);
+                const bf16x2 x = pack_bf16(o[b][4 * c], o[b][4 * c + 1]), y = pack_bf16(o[b][4 * c + 2], o[b][4 * c + 3]);
                 *reinterpret_cast<bf16x4 *>(lds + kV + at<CV>(32 * b + (lane & 31), 4 * w + c) + 8 * half) = (bf16x4){x[0], x[1], y[0], y[1]};
             }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -236,7 +262,7 @@ template <int K, int V, bool OUT> struct LinBf16 {
             if (t < count) *reinterpret_cast<u32x4 *>(out + t * stride + 8 * c) = x;
         }
     }
-    static __device__ __forceinline__ void store(float *out, int64_t stride, const f32x16 (&o)[2], float scale, char *, int count, int w, int lane) {
+    static __device__ __forceinline__ void store(float *out, int64_t stride, const f32x16 (&o)[2], char *, int count, int w, int lane) {
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             const int t = 32 * b + (lane & 31);
@@ -244,7 +270,7 @@ template <int K, int V, bool OUT> struct LinBf16 {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 *reinterpret_cast<f32x4 *>(out + t * stride + 32 * w + 8 * c + 4 * (lane >> 5)) =
-                    (f32x4){scale * o[b][4 * c], scale * o[b][4 * c + 1], scale * o[b][4 * c + 2], scale * o[b][4 * c + 3]};
+                    (f32x4){o[b][4 * c], o[b][4 * c + 1], o[b][4 * c + 2], o[b][4 * c + 3]};
         }
     }
 
@@ -261,7 +287,7 @@ template <int K, int V, bool OUT> struct LinBf16 {
         for (int x = 0; x < 4; ++x) {
             float f[8];
             widen(vf[x], f);
-            const f32x4 a = *reinterpret_cast<const f32x4 *>(d.left + 16 * x + 4 * half), b = *reinterpret_cast<const f32x4 *>(d.left + 16 * x + 8 + 4 * half);
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(d.left + 16 * x + 8 * half), b = *reinterpret_cast<const f32x4 *>(d.left + 16 * x + 8 * half + 4);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 f[i] *= a[i];
@@ -273,7 +299,7 @@ template <int K, int V, bool OUT> struct LinBf16 {
             p[2] = to_frag(f, bf16x8{});
             bf16x8 kf[M];
 #pragma unroll
-            for (int m = 0; m < M; ++m) kf[m] = transposed<CK>(lds + kK, x, m, lane);
+            for (int m = 0; m < M; ++m) kf[m] = transposed<CK, true>(lds + kK, x, m, lane);
 #pragma unroll
             for (int i = 0; i < 3; ++i)
 #pragma unroll
@@ -285,24 +311,21 @@ template <int K, int V, bool OUT> struct LinBf16 {
     template <typename TOut, typename Next>
     __device__ __forceinline__ void chunk(TOut *out, int64_t stride, float scale, char *lds, const Decays &d, const int &odd, int count, int w, int lane, Next next) {
         f32x16 o[2];
+        next();  // the loads of the next chunk leave
         if (OUT) {
-            // rows 16 s of P take s + 1 products of 16 columns: an even share for two waves
-            if (NW == 4) {
-                scores(lds, d, w, lane);
-            } else {
-                scores(lds, d, w, lane);
-                scores(lds, d, 3 - w, lane);
-            }
-            from_state(o, lds, d, lane);
+            scores(lds, d, scale, w, lane);
+            from_state(o, lds, d, scale, lane);
             __syncthreads();
         }
-        if (OUT) next();  // the loads of the next chunk leave
         bf16x8 vf[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) vf[x] = transposed<CV>(lds + kV, x, w, opaque(lane));
+        for (int x = 0; x < 4; ++x) vf[x] = transposed<CV, false>(lds + kV, x, w, opaque(lane));
         if (OUT) {
-            from_chunk(o, vf, odd != 0, lds, w, lane);
-            store(out, stride, o, scale, lds, count, w, lane);
+            if (__builtin_amdgcn_readfirstlane(odd) == 0)
+                from_chunk(o, vf, lds, lane);
+            else
+                from_odd_chunk(o, vf, lds, w, lane);
+            store(out, stride, o, lds, count, w, lane);
         }
         update(vf, lds, d, lane);
     }
@@ -329,7 +352,7 @@ template <int K, int V, bool OUT> struct LinBf16 {
 
     // register r of S[m] and the element of a [K, V] state
     static __device__ __forceinline__ int element(int m, int r, int w, int lane) {
-        return (32 * m + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * V + 32 * w + (lane & 31);
+        return (32 * m + 16 * (r >> 3) + 8 * (lane >> 5) + (r & 7)) * V + 32 * w + (lane & 31);
     }
 };
 

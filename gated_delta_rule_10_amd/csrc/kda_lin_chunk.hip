@@ -101,7 +101,7 @@ __global__ __launch_bounds__(W::NT, 2) void lin_segments_kernel(LinArgs a, Segme
     TOut *op = static_cast<TOut *>(a.o) + (static_cast<int64_t>(t0) * a.H + h) * V;
     double sum = 0.0;  // of the segment's decays so far
     auto decay = [&](int c) { return lane < min(C, tokens - c * C) ? log_decay_of(a, t0 + c * C + lane, h) : 0.f; };
-    auto tabulate = [&](float g, int b) {
+    auto tabulate = [&](float g, int b, int rows) {
         double x = static_cast<double>(g) * kLog2e;
 #pragma unroll
         for (int d = 1; d < C; d <<= 1) {
@@ -115,13 +115,13 @@ __global__ __launch_bounds__(W::NT, 2) void lin_segments_kernel(LinArgs a, Segme
             table[b][0][lane] = hi;
             table[b][1][lane] = static_cast<float>(x - static_cast<double>(hi));
             table[b][2][lane] = __builtin_amdgcn_exp2f(hi);
-            table[b][3][lane] = __builtin_amdgcn_exp2f(static_cast<float>(all - x));
+            table[b][3][lane] = lane < rows ? __builtin_amdgcn_exp2f(static_cast<float>(all - x)) : 0.f;
         }
         if (lane == 0) strange[b] = 0;
     };
     float g = 0.f;
     if (w == 0 && chunks > 0) {
-        tabulate(decay(0), 0);
+        tabulate(decay(0), 0, tokens);
         g = chunks > 1 ? decay(1) : 0.f;
     }
     if (chunks > 0) s.load(qp, kp, vp, a, min(C, tokens), tid);
@@ -134,10 +134,9 @@ __global__ __launch_bounds__(W::NT, 2) void lin_segments_kernel(LinArgs a, Segme
             qp += C * a.qs, kp += C * a.ks, vp += C * a.vs;
             if (c + 1 < chunks) s.load(qp, kp, vp, a, min(C, tokens - (c + 1) * C), tid);
         };
-        if (!OUT) next();
         __syncthreads();
         if (w == 0 && c + 1 < chunks) {
-            tabulate(g, b ^ 1);
+            tabulate(g, b ^ 1, tokens - (c + 1) * C);
             if (c + 2 < chunks) g = decay(c + 2);
         }
         const Decays d = {table[b][0], table[b][1], table[b][2], table[b][3]};
