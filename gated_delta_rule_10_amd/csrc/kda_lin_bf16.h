@@ -10,9 +10,10 @@
 //     O^T = S^T Q^T e^(G_i) + V^T P^T        P = (Q K^T) * e^(G_i - G_j), j <= i
 //     S   = e^(G_C) S + K^T (V e^(G_C - G_j))
 //
-// P is formed once per workgroup, 16 rows of it to a wave, and shared in LDS.
-// q, k and v are exact bf16 operands. S and P are two bf16 parts each (16 bits);
-// V e^(..) is three (24 bits, all of fp32): its rounding would stay in the state.
+// P is formed once per workgroup, a quarter of 32 x 32 to a wave, and shared in LDS.
+// q, k and v are exact bf16 operands. V e^(..) is three bf16 parts (24 bits, all of
+// fp32): its rounding would stay in the state. S and P only go into the outputs: one
+// part for bf16 outputs, which round them as much again, two for fp32 ones.
 #pragma once
 
 #include "kda_attn_rows.h"
@@ -60,13 +61,17 @@ __device__ __forceinline__ int opaque(int lane) {
     return lane;
 }
 
-template <int K, int V, bool OUT> struct LinBf16 {
+// PARTS: of S and P; 0 where there are no outputs
+template <int K, int V, int PARTS> struct LinBf16 {
     using T = bf16_t;
+    static constexpr bool OUT = PARTS > 0;
     static constexpr int C = 64, NW = V / 32, NT = 64 * NW, M = K / 32, kRegs = 16;
+    // with two waves a thread holds twice as much of the next chunk, and 256 registers do not do
+    static constexpr int kWavesPerSimd = OUT && NW == 2 && K == 128 ? 1 : 2;
     static constexpr int CK = K / 8, CV = V / 8;          // 16-byte pieces of a row
     static constexpr int LK = C * CK / NT, LV = C * CV / NT;  // of a thread
     static constexpr int kQ = 0, kK = OUT ? C * K * 2 : 0, kV = kK + C * K * 2, kP = kV + C * V * 2;
-    static constexpr int kLds = kP + (OUT ? 2 * C * C * 2 : 0);
+    static constexpr int kLds = kP + PARTS * C * C * 2;
 
     // Piece c of token t lies at piece c ^ swz(t) of its row: 16 rows read at one piece, and 4 rows
     // read at 4 pieces (the transposing reads), fall on different banks.
@@ -79,10 +84,7 @@ template <int K, int V, bool OUT> struct LinBf16 {
     u32x4 q[OUT ? LK : 1], k[LK], v[LV];  // the next chunk, on its way
     f32x16 S[M];
 
-    // a state of zeros, and zeros where no chunk writes scores: right of the diagonal's 16 x 16 tiles
-    __device__ __forceinline__ void clear(char *lds, int tid) {
-        if (OUT)
-            for (int i = tid; i < 2 * C * 8; i += NT) *reinterpret_cast<u32x4 *>(lds + kP + 16 * i) = u32x4{0, 0, 0, 0};
+    __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int m = 0; m < M; ++m)
 #pragma unroll
@@ -145,32 +147,33 @@ template <int K, int V, bool OUT> struct LinBf16 {
         return *reinterpret_cast<const bf16x8 *>(p + at<CH>(t, 2 * x + half));
     }
 
-    // The 10 tiles of 16 x 16 of P on and below the diagonal, 3 to each of four waves or 5 to each of
-    // two (a wave of fewer does its last one again), as two bf16 parts in LDS.
-    static __device__ __forceinline__ void scores(char *lds, const Decays &d, float scale, int w, int lane) {
+    // The quarter of P of rows i0.. and columns j0.., in bf16 parts in LDS
+    static __device__ __forceinline__ void scores(char *lds, const Decays &d, float scale, int i0, int j0, int lane) {
         lane = opaque(lane);
-        const int l = lane & 15, g = lane >> 4;
-        constexpr int N = NW == 4 ? 3 : 5;
+        const int l = lane & 31, half = lane >> 5, i = i0 + l;
+        f32x16 p = {};
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int i0 = 16 * (NW == 4 ? (w == 0 && k > 0 ? 3 : w) : w == 0 ? (k + 1) / 2 : k == 0 ? 2 : 3);
-            const int j0 = 16 * (NW == 4 ? (w == 0 ? 0 : w == 1 ? min(k, 1) : w == 2 ? k : k + 1) : w == 0 ? (k == 2 || k == 4) : k == 0 ? 2 : k - 1);
-            f32x4 p = {0.f, 0.f, 0.f, 0.f};
+        for (int x = 0; x < K / 16; ++x) p = mma32(eight<CK>(lds + kK, x, j0 + l, half), eight<CK>(lds + kQ, x, i, half), p);
+        const float hi = d.hi[i], lo = d.lo[i];
 #pragma unroll
-            for (int x = 0; x < K / 32; ++x)
-                p = mma16(*reinterpret_cast<const bf16x8 *>(lds + kK + at<CK>(j0 + l, 4 * x + g)),
-                          *reinterpret_cast<const bf16x8 *>(lds + kQ + at<CK>(i0 + l, 4 * x + g)), p);
-            const int i = i0 + l, j = j0 + 4 * g;  // p[r]: row i, column j + r
-            const float hi = d.hi[i], lo = d.lo[i];
+        for (int c = 0; c < 4; ++c) {
+            const int j = j0 + 8 * c + 4 * half;  // p[4 c + r]: row i, column j + r
             const f32x4 dh = *reinterpret_cast<const f32x4 *>(d.hi + j), dl = *reinterpret_cast<const f32x4 *>(d.lo + j);
+            float e[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                p[r] = j + r <= i ? p[r] * (scale * __builtin_amdgcn_exp2f((hi - dh[r]) + (lo - dl[r]))) : 0.f;
-            const bf16x2 a = pack_bf16(p[0], p[1]), b = pack_bf16(p[2], p[3]);
-            const bf16x2 e = pack_bf16(less_first(a, p[0]), less_second(a, p[1])), f = pack_bf16(less_first(b, p[2]), less_second(b, p[3]));
-            const int to = at<8>(i, j >> 3) + 8 * (g & 1);
-            *reinterpret_cast<bf16x4 *>(lds + kP + to) = (bf16x4){a[0], a[1], b[0], b[1]};
-            *reinterpret_cast<bf16x4 *>(lds + kP + C * C * 2 + to) = (bf16x4){e[0], e[1], f[0], f[1]};
+                e[r] = j + r <= i ? p[4 * c + r] * (scale * __builtin_amdgcn_exp2f((hi - dh[r]) + (lo - dl[r]))) : 0.f;
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part) {
+                const bf16x2 a = pack_bf16(e[0], e[1]), b = pack_bf16(e[2], e[3]);
+                *reinterpret_cast<bf16x4 *>(lds + kP + part * C * C * 2 + at<8>(i, j >> 3) + 8 * half) = (bf16x4){a[0], a[1], b[0], b[1]};
+                if (part + 1 < PARTS) {
+                    e[0] = less_first(a, e[0]);
+                    e[1] = less_second(a, e[1]);
+                    e[2] = less_first(b, e[2]);
+                    e[3] = less_second(b, e[3]);
+                }
+            }
         }
     }
 
@@ -183,14 +186,15 @@ template <int K, int V, bool OUT> struct LinBf16 {
             float s[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) s[i] = S[x / 2][8 * (x & 1) + i];
-            bf16x8 p[2];
-            split_bf16(s, p[0]);
-            p[1] = to_frag(s, bf16x8{});
-            bf16x8 f[2];
+            bf16x8 p[PARTS], f[2];
+#pragma unroll
+            for (int i = 0; i < PARTS - 1; ++i) split_bf16(s, p[i]);
+            p[PARTS - 1] = to_frag(s, bf16x8{});
+
 #pragma unroll
             for (int b = 0; b < 2; ++b) f[b] = eight<CK>(lds + kQ, x, 32 * b + (lane & 31), lane >> 5);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < PARTS; ++i)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) o[b] = mma32(p[i], f[b], x + i == 0 ? zero : o[b]);
         }
@@ -208,7 +212,7 @@ template <int K, int V, bool OUT> struct LinBf16 {
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+            for (int part = 0; part < PARTS; ++part)
 #pragma unroll
                 for (int b = x / 2; b < 2; ++b)
                     o[b] = mma32(vf[x], eight<8>(lds + kP + part * C * C * 2, x, 32 * b + (lane & 31), lane >> 5), o[b]);
@@ -232,8 +236,9 @@ template <int K, int V, bool OUT> struct LinBf16 {
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const int i = 32 * b + (lane & 31), p = kP + at<8>(i, j >> 3) + 2 * (j & 7);
-                const float s = bf16_to_f32(*reinterpret_cast<const bf16_t *>(lds + p)) +
-                                bf16_to_f32(*reinterpret_cast<const bf16_t *>(lds + p + C * C * 2));
+                float s = 0.f;
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) s += bf16_to_f32(*reinterpret_cast<const bf16_t *>(lds + p + part * C * C * 2));
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const int c = 32 * w + 8 * (r >> 2) + 4 * half + (r & 3);
@@ -310,24 +315,29 @@ template <int K, int V, bool OUT> struct LinBf16 {
     // one chunk, whose tiles are in LDS; odd: not 0 if some value is an infinity or NaN
     template <typename TOut, typename Next>
     __device__ __forceinline__ void chunk(TOut *out, int64_t stride, float scale, char *lds, const Decays &d, const int &odd, int count, int w, int lane, Next next) {
-        f32x16 o[2];
         next();  // the loads of the next chunk leave
-        if (OUT) {
-            scores(lds, d, scale, w, lane);
+        if constexpr (OUT) {
+            f32x16 o[2];
+            // the three quarters on and below the diagonal; the last wave has the next chunk's decays to sum
+            if (w < 3 && w < NW) scores(lds, d, scale, w ? 32 : 0, w == 2 ? 32 : 0, lane);
+            if (NW == 2 && w == 0) scores(lds, d, scale, 32, 32, lane);
             from_state(o, lds, d, scale, lane);
             __syncthreads();
-        }
-        bf16x8 vf[4];
+            bf16x8 vf[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) vf[x] = transposed<CV, false>(lds + kV, x, w, opaque(lane));
-        if (OUT) {
+            for (int x = 0; x < 4; ++x) vf[x] = transposed<CV, false>(lds + kV, x, w, opaque(lane));
             if (__builtin_amdgcn_readfirstlane(odd) == 0)
                 from_chunk(o, vf, lds, lane);
             else
                 from_odd_chunk(o, vf, lds, w, lane);
             store(out, stride, o, lds, count, w, lane);
+            update(vf, lds, d, lane);
+        } else {
+            bf16x8 vf[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) vf[x] = transposed<CV, false>(lds + kV, x, w, opaque(lane));
+            update(vf, lds, d, lane);
         }
-        update(vf, lds, d, lane);
     }
 
     // the state as the registers hold it, in memory

@@ -65,10 +65,11 @@ struct Segments {
     double *sum;
 };
 
-template <typename W, typename TOut, bool OUT, int K, int V>
-__global__ __launch_bounds__(W::NT, 2) void lin_segments_kernel(LinArgs a, Segments ws, int R) {
+template <typename W, typename TOut, int K, int V>
+__global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(LinArgs a, Segments ws, int R) {
     using T = typename W::T;
     constexpr int C = W::C;
+    constexpr bool OUT = W::OUT;
     __shared__ __align__(16) char lds[W::kLds];
     __shared__ __align__(16) float table[2][4][C];
     __shared__ int strange[2];
@@ -85,7 +86,7 @@ __global__ __launch_bounds__(W::NT, 2) void lin_segments_kernel(LinArgs a, Segme
     const int64_t piece = static_cast<int64_t>(place) * a.H + h;
 
     W s;
-    s.clear(lds, tid);
+    s.clear();
     if (OUT && segs > 1) {
         s.get(ws.state + piece * (K * V), w, lane);
     } else if (seg == 0 && a.s0 && slot >= 0) {
@@ -120,7 +121,7 @@ __global__ __launch_bounds__(W::NT, 2) void lin_segments_kernel(LinArgs a, Segme
         if (lane == 0) strange[b] = 0;
     };
     float g = 0.f;
-    if (w == 0 && chunks > 0) {
+    if (w == W::NW - 1 && chunks > 0) {
         tabulate(decay(0), 0, tokens);
         g = chunks > 1 ? decay(1) : 0.f;
     }
@@ -135,7 +136,7 @@ __global__ __launch_bounds__(W::NT, 2) void lin_segments_kernel(LinArgs a, Segme
             if (c + 1 < chunks) s.load(qp, kp, vp, a, min(C, tokens - (c + 1) * C), tid);
         };
         __syncthreads();
-        if (w == 0 && c + 1 < chunks) {
+        if (w == W::NW - 1 && c + 1 < chunks) {
             tabulate(g, b ^ 1, tokens - (c + 1) * C);
             if (c + 2 < chunks) g = decay(c + 2);
         }
@@ -151,7 +152,7 @@ __global__ __launch_bounds__(W::NT, 2) void lin_segments_kernel(LinArgs a, Segme
                 for (int r = 0; r < W::kRegs; ++r) a.sT[held + W::element(m, r, w, lane)] = s.S[m][r];
     } else {
         s.put(ws.state + (piece + a.H) * (K * V), w, lane);  // the next segment's
-        if (tid == 0) ws.sum[piece] = sum;
+        if (tid == W::NT - 1) ws.sum[piece] = sum;
     }
 }
 
@@ -199,16 +200,16 @@ template <int K, int V, typename TOut> hipError_t launch_bf16(const LinArgs &a, 
         ws.sum = static_cast<double *>(a.ws);
         ws.state = reinterpret_cast<float *>(static_cast<char *>(a.ws) + (p.places * a.H * 8 + 255) / 256 * 256);
     }
-    const dim3 grid(static_cast<unsigned>(p.places * a.H)), block(LinBf16<K, V, true>::NT);
+    const dim3 grid(static_cast<unsigned>(p.places * a.H)), block(LinBf16<K, V, 0>::NT);
     if (p.cut) {
-        hipLaunchKernelGGL((lin_segments_kernel<LinBf16<K, V, false>, float, false, K, V>), grid, block, 0, st, a, ws, p.R);
+        hipLaunchKernelGGL((lin_segments_kernel<LinBf16<K, V, 0>, float, K, V>), grid, block, 0, st, a, ws, p.R);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL((lin_join_kernel<K * V>), dim3(a.N * a.H * (K * V / 1024)), dim3(256), 0, st, a, ws, p.R);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((lin_segments_kernel<LinBf16<K, V, true>, TOut, true, K, V>), grid, block, 0, st, a, ws, p.R);
+    hipLaunchKernelGGL((lin_segments_kernel<LinBf16<K, V, sizeof(TOut) / 2>, TOut, K, V>), grid, block, 0, st, a, ws, p.R);
     return hipGetLastError();
 }
 

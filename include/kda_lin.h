@@ -40,13 +40,13 @@
  *    [0, num_slots) holds nothing: its sequence starts from zeros and its state
  *    is not written (padding).
  *  - Arithmetic: the state, decays and sums are fp32 (sums of g in fp64). fp32
- *    inputs are multiplied in fp32. With bf16 inputs q, k and v are exact, and
- *    what the matrix cores take besides them is split into bf16 parts: the
- *    decayed values into three (24 bits), so that states are fp32 to their last
- *    bits, and the decayed scores and the state that q reads into two (16 bits
- *    of significand, an error of 2^-16 of each). Results do not depend on
- *    timing: no atomics. They may differ in the last bits between batches, which
- *    decide where long sequences are cut into segments.
+ *    inputs are multiplied in fp32. With bf16 inputs q, k and v are exact, the
+ *    decayed values go into the state with 24 bits, so that states are right to
+ *    fp32, and the decayed scores and the state that q reads are rounded for the
+ *    outputs: to one bf16 number (by at most 2^-8 of each term) for bf16 outputs,
+ *    to the sum of two (2^-16) for fp32 ones. Single tokens are fp32 throughout.
+ *    Results do not depend on timing: no atomics. They may differ in the last bits
+ *    between batches, which decide where long sequences are cut into segments.
  *  - Range: products and states have to stay below 2^120 in magnitude. An
  *    infinity or NaN in a token's q reaches that token's output only; in its k, v
  *    or g the outputs of its head from that token on and the state, never an

@@ -9,8 +9,9 @@ rounding, is rounded
    at most when one is taken per 16 tokens (a longer step takes fewer), and in the products with k and v by 3 2^-24;
  - in its sums, each at most 2^-24 of A: over d_k channels, 64 tokens, one more for each step of 16 tokens and
    one for each of up to 64 segments.
-With bf16 inputs the decayed scores and the state that q reads are held in 16 bits where they are multiplied
-(2^-16 of each term, once); the decayed values in 24 (2^-24). Single tokens: no such splitting, one step.
+With bf16 inputs the decayed scores and the state that q reads are held in bf16 where they are multiplied, one
+number for bf16 outputs (2^-8 of each term, once), two for fp32 ones (2^-16); the decayed values in 24 bits
+(2^-24). Single tokens: no such rounding, one step.
 """
 
 import numpy as np
@@ -96,14 +97,15 @@ class Inputs:
             at += L
         return out
 
-    def bound(self, L, dk):
-        return e32(L, dk) + (2.0 ** -16 if self.dt == "bf16" else 0.0)
+    def bound(self, L, dk, bf16_out):
+        return e32(L, dk) + (0.0 if self.dt == "f32" else 2.0 ** -8 if bf16_out else 2.0 ** -16)
 
     def check(self, o, state, S0, scale, what=""):
         at = 0
         for n, (L, (ro, ao, rs, as_)) in enumerate(zip(self.lens, self.reference(S0, scale))):
             dk = self.q.shape[2]
-            check(f"{what} o {n} ({L})", o[at:at + L], ro, ao, self.bound(L, dk), o.dtype == torch.bfloat16)
+            half = o.dtype == torch.bfloat16
+            check(f"{what} o {n} ({L})", o[at:at + L], ro, ao, self.bound(L, dk, half), half)
             if state is not None:
                 check(f"{what} state {n} ({L})", state[n], rs, as_, e32(L, dk))
             at += L
