@@ -65,7 +65,7 @@ __device__ __forceinline__ int opaque(int lane) {
 template <int K, int V, int PARTS> struct LinBf16 {
     using T = bf16_t;
     static constexpr bool OUT = PARTS > 0;
-    static constexpr int C = 64, NW = V / 32, NT = 64 * NW, M = K / 32, kRegs = 16;
+    static constexpr int C = 64, NW = V / 32, NT = 64 * NW, M = K / 32;
     // with two waves a thread holds twice as much of the next chunk, and 256 registers do not do
     static constexpr int kWavesPerSimd = OUT && NW == 2 && K == 128 ? 1 : 2;
     static constexpr int CK = K / 8, CV = V / 8;          // 16-byte pieces of a row
@@ -90,6 +90,8 @@ template <int K, int V, int PARTS> struct LinBf16 {
 #pragma unroll
             for (int r = 0; r < 16; ++r) S[m][r] = 0.f;
     }
+
+    static __device__ __forceinline__ void prepare(char *, int) {}  // nothing in LDS outlasts a chunk
 
     // Rows from `count` on are the last one again: their scores are masked and their values weigh 0.
     template <int CH, int L> static __device__ __forceinline__ void load_rows(u32x4 (&x)[L], const T *p, int64_t stride, int count, int tid) {
@@ -122,6 +124,7 @@ template <int K, int V, int PARTS> struct LinBf16 {
         if (OUT) store_rows<CK>(q, lds + kQ, tid);
         store_rows<CK>(k, lds + kK, tid);
         store_rows<CV>(v, lds + kV, tid);
+        if (!OUT) return false;
         uint32_t odd = 0;
 #pragma unroll
         for (int i = 0; i < LV; ++i)
@@ -279,15 +282,28 @@ template <int K, int V, int PARTS> struct LinBf16 {
         }
     }
 
-    // S = e^(G_C) S + K^T (V e^(G_C - G_j))
-    __device__ __forceinline__ void update(const bf16x8 (&vf)[4], const char *lds, const Decays &d, int lane) {
+    // S = e^(G_C) S + K^T (V e^(G_C - G_j)), the first factor only where DECAY
+    template <bool DECAY> __device__ __forceinline__ void update(const char *lds, const Decays &d, int w, int lane) {
+        bf16x8 vf[4];
+        values(vf, lds, w, lane);
+        update<DECAY>(vf, lds, d, lane);
+    }
+    static __device__ __forceinline__ void values(bf16x8 (&vf)[4], const char *lds, int w, int lane) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) vf[x] = transposed<CV, false>(lds + kV, x, w, opaque(lane));
+    }
+    template <bool DECAY> __device__ __forceinline__ void update(const bf16x8 (&vf)[4], const char *lds, const Decays &d, int lane) {
+        // first in line for the matrix cores: the products here are most of a chunk's (1 x 131072 1480 -> 1461 us)
+        __builtin_amdgcn_s_setprio(1);
         lane = opaque(lane);
         const int half = lane >> 5;
-        const float all = d.grown[C - 1];
+        if (DECAY) {
+            const float all = d.grown[C - 1];
 #pragma unroll
-        for (int m = 0; m < M; ++m)
+            for (int m = 0; m < M; ++m)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) S[m][r] *= all;
+                for (int r = 0; r < 16; ++r) S[m][r] *= all;
+        }
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             float f[8];
@@ -310,34 +326,27 @@ template <int K, int V, int PARTS> struct LinBf16 {
 #pragma unroll
                 for (int m = 0; m < M; ++m) S[m] = mma32(kf[m], p[i], S[m]);
         }
+        __builtin_amdgcn_s_setprio(0);
     }
 
     // one chunk, whose tiles are in LDS; odd: not 0 if some value is an infinity or NaN
     template <typename TOut, typename Next>
     __device__ __forceinline__ void chunk(TOut *out, int64_t stride, float scale, char *lds, const Decays &d, const int &odd, int count, int w, int lane, Next next) {
+        f32x16 o[2];
+        // the three quarters on and below the diagonal; the last wave has the next chunk's decays to sum
+        if (w < 3 && w < NW) scores(lds, d, scale, w ? 32 : 0, w == 2 ? 32 : 0, lane);
+        if (NW == 2 && w == 0) scores(lds, d, scale, 32, 32, lane);
         next();  // the loads of the next chunk leave
-        if constexpr (OUT) {
-            f32x16 o[2];
-            // the three quarters on and below the diagonal; the last wave has the next chunk's decays to sum
-            if (w < 3 && w < NW) scores(lds, d, scale, w ? 32 : 0, w == 2 ? 32 : 0, lane);
-            if (NW == 2 && w == 0) scores(lds, d, scale, 32, 32, lane);
-            from_state(o, lds, d, scale, lane);
-            __syncthreads();
-            bf16x8 vf[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) vf[x] = transposed<CV, false>(lds + kV, x, w, opaque(lane));
-            if (__builtin_amdgcn_readfirstlane(odd) == 0)
-                from_chunk(o, vf, lds, lane);
-            else
-                from_odd_chunk(o, vf, lds, w, lane);
-            store(out, stride, o, lds, count, w, lane);
-            update(vf, lds, d, lane);
-        } else {
-            bf16x8 vf[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) vf[x] = transposed<CV, false>(lds + kV, x, w, opaque(lane));
-            update(vf, lds, d, lane);
-        }
+        from_state(o, lds, d, scale, lane);
+        __syncthreads();
+        bf16x8 vf[4];
+        values(vf, lds, w, lane);
+        if (__builtin_amdgcn_readfirstlane(odd) == 0)
+            from_chunk(o, vf, lds, lane);
+        else
+            from_odd_chunk(o, vf, lds, w, lane);
+        store(out, stride, o, lds, count, w, lane);
+        update<true>(vf, lds, d, lane);
     }
 
     // the state as the registers hold it, in memory
@@ -360,7 +369,20 @@ template <int K, int V, int PARTS> struct LinBf16 {
             }
     }
 
-    // register r of S[m] and the element of a [K, V] state
+    // a [K, V] state
+    __device__ __forceinline__ void take(const float *p, int w, int lane) {
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) S[m][r] = p[element(m, r, w, lane)];
+    }
+    __device__ __forceinline__ void give(float *p, int w, int lane) const {
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) p[element(m, r, w, lane)] = S[m][r];
+    }
+    // register r of S[m] and its element
     static __device__ __forceinline__ int element(int m, int r, int w, int lane) {
         return (32 * m + 16 * (r >> 3) + 8 * (lane >> 5) + (r & 7)) * V + 32 * w + (lane & 31);
     }

@@ -1,7 +1,7 @@
 // Linear attention with one decay per head over packed prompts (kda_lin_chunk_fwd).
 //
 // A workgroup walks a segment of a sequence for one value head, chunk by chunk,
-// with the state in registers (kda_lin_bf16.h). A sequence is one segment where
+// with the state in registers (kda_lin_bf16.h, kda_lin_f32.h). A sequence is one segment where
 // there are enough sequences and heads to fill the card; otherwise it is cut, and
 // two more launches come before: one walks all segments but each sequence's last
 // from a state of zeros (the first from the initial state) to their ends, without
@@ -11,50 +11,10 @@
 #include "kda_attn_internal.h"
 #include "kda_lin_bf16.h"
 #include "kda_lin_device.h"
+#include "kda_lin_f32.h"
 
 namespace kda {
 namespace {
-
-constexpr int kThreads = 256;
-
-__device__ __forceinline__ int clamp_to(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
-
-template <int K, int V, typename TIn, typename TOut>
-__global__ __launch_bounds__(kThreads) void lin_tokens_kernel(LinArgs a) {
-    constexpr int P = kThreads / V, R = K / P;  // threads to a column, rows of each
-    __shared__ float qs[K], ks[K], part[P][V];
-    const int tid = threadIdx.x, col = tid % V, p = tid / V;
-    const int n = blockIdx.x / a.H, h = blockIdx.x - n * a.H, hk = h / (a.H / a.Hk);
-    const int start = clamp_to(a.cu[n], 0, a.T), end = clamp_to(a.cu[n + 1], start, a.T), slot = slot_of(a, n);
-    const int64_t base = (static_cast<int64_t>(slot) * a.H + h) * (K * V) + col;
-    float S[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) S[i] = a.s0 && slot >= 0 ? a.s0[base + (p * R + i) * V] : 0.f;
-    for (int t = start; t < end; ++t) {
-        __syncthreads();
-        if (tid < K) {
-            qs[tid] = io<TIn>::load(static_cast<const TIn *>(a.q) + t * a.qs + hk * K + tid);
-            ks[tid] = io<TIn>::load(static_cast<const TIn *>(a.k) + t * a.ks + hk * K + tid);
-        }
-        const float v = io<TIn>::load(static_cast<const TIn *>(a.v) + t * a.vs + h * V + col), d = __expf(log_decay_of(a, t, h));
-        __syncthreads();
-        float o = 0.f;
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            S[i] = fmaf(ks[p * R + i], v, d * S[i]);
-            o = fmaf(qs[p * R + i], S[i], o);
-        }
-        part[p][col] = o;
-        __syncthreads();
-        if (p == 0) {
-            for (int i = 1; i < P; ++i) o += part[i][col];
-            store_out(static_cast<TOut *>(a.o) + (static_cast<int64_t>(t) * a.H + h) * V + col, a.scale * o);
-        }
-    }
-    if (a.sT && slot >= 0)
-#pragma unroll
-        for (int i = 0; i < R; ++i) a.sT[base + (p * R + i) * V] = S[i];
-}
 
 constexpr double kLog2e = 1.4426950408889634;
 
@@ -65,58 +25,155 @@ struct Segments {
     double *sum;
 };
 
+// What a workgroup works on: segment `seg` of `segs` of sequence n, `tokens` of them from t0 on.
+struct Span {
+    int n, seg, segs, t0, tokens;
+    __device__ __forceinline__ Span(const LinArgs &a, int R, int place, int lane) {
+        n = seq_of_slot(a.cu, a.N, a.T, 1, R, place, lane);
+        int start, count;
+        seq_rows(a.cu, n, a.T, start, count);
+        seg = place - (start / R + n);
+        segs = max(1, (count + R - 1) / R);
+        t0 = start + seg * R;
+        tokens = min(R, count - seg * R);
+    }
+};
+
+// x of the lane that a DPP control names, 0 where there is none (or its row is masked)
+template <int CTRL, int ROWS> __device__ __forceinline__ double from_dpp(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, ROWS, 0xF, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, ROWS, 0xF, true);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+// Inclusive sums over a chunk of log2 e^g, one token to a lane, and their total: shifts within rows of
+// 16 lanes, then each row's last lane to the rows behind it.
+__device__ __forceinline__ double sums(float g, double &all) {
+    double x = static_cast<double>(g) * kLog2e;
+    x += from_dpp<0x111, 0xF>(x);
+    x += from_dpp<0x112, 0xF>(x);
+    x += from_dpp<0x114, 0xF>(x);
+    x += from_dpp<0x118, 0xF>(x);
+    x += from_dpp<0x142, 0xA>(x);  // lane 15 to row 1, lane 47 to row 3
+    x += from_dpp<0x143, 0xC>(x);  // lane 31 to rows 2 and 3
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), 63), hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), 63);
+    all = __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+    return x;
+}
+
+// The states at the ends of all segments but each sequence's last, from zeros (the first: from the
+// initial state). Chunk by chunk from the end: a token's value is weighed with all the decay between
+// it and the segment's end, the state itself is not decayed step by step, and the walk ends where all
+// further weights are 0 in fp32. (Heads that forget fast look at a few chunks only.)
+template <typename W, int K, int V>
+__global__ __launch_bounds__(W::NT, 2) void lin_ends_kernel(LinArgs a, Segments ws, int R) {
+    using T = typename W::T;
+    constexpr int C = W::C;
+    constexpr double kNothing = -160.0;  // 2^-150 is 0 in fp32
+    __shared__ __align__(16) char lds[2][W::kLds];
+    __shared__ __align__(16) float left[2][C];
+    __shared__ int over[2];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int place = blockIdx.x / a.H, h = blockIdx.x - place * a.H, hk = h / (a.H / a.Hk);
+    const Span x(a, R, place, lane);
+    if (x.seg < 0 || x.seg >= x.segs - 1) return;
+    const int chunks = R / C;  // all whole
+    const int64_t piece = static_cast<int64_t>(place) * a.H + h;
+    const T *kp = static_cast<const T *>(a.k) + (x.t0 + R - C) * a.ks + hk * K, *vp = static_cast<const T *>(a.v) + (x.t0 + R - C) * a.vs + h * V;
+    W s;
+    s.clear();
+    double sum = 0.0;  // from the chunk's end to the segment's
+    auto decay = [&](int i) { return lane < C ? log_decay_of(a, x.t0 + R - (i + 1) * C + lane, h) : 0.f; };
+    auto tabulate = [&](float g, int b) {
+        double all;
+        const double y = sums(g, all);
+        if (lane < C) left[b][lane] = __builtin_amdgcn_exp2f(static_cast<float>(sum + (all - y)));
+        if (lane == 0) over[b] = sum < kNothing;
+        sum += all;
+    };
+    auto load = [&] {
+        s.load(nullptr, kp, vp, a, C, tid);
+        kp -= C * a.ks, vp -= C * a.vs;
+    };
+    float g = 0.f;
+    if (w == W::NW - 1) {
+        tabulate(decay(0), 0);
+        g = chunks > 1 ? decay(1) : 0.f;
+    }
+    load();
+    s.to_lds(lds[0], tid);
+    if (chunks > 1) load();
+#pragma unroll 1
+    for (int i = 0; i < chunks; ++i) {
+        const int b = i & 1;
+        __syncthreads();
+        if (over[b]) break;
+        if (w == W::NW - 1 && i + 1 < chunks) {
+            tabulate(g, b ^ 1);
+            if (i + 2 < chunks) g = decay(i + 2);
+        }
+        s.template update<false>(lds[b], {nullptr, nullptr, nullptr, left[b]}, w, lane);
+        if (i + 1 < chunks) s.to_lds(lds[b ^ 1], tid);
+        if (i + 2 < chunks) load();
+    }
+    float *out = ws.state + piece * (K * V);
+    if (x.seg == 0) {
+        // the last wave has the sum
+        __shared__ float whole;
+        if (tid == W::NT - 1) whole = __builtin_amdgcn_exp2f(static_cast<float>(sum));
+        __syncthreads();
+        const float e = whole;
+        const int slot = slot_of(a, x.n);
+        const float *s0 = a.s0 + (static_cast<int64_t>(slot) * a.H + h) * (K * V);
+        W first;
+        first.clear();
+        if (a.s0 && slot >= 0) first.take(s0, w, lane);
+        first.put(out, w, lane);
+#pragma unroll
+        for (int m = 0; m < W::M; ++m)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s.S[m][r] = fmaf(e, first.S[m][r], s.S[m][r]);
+    }
+    s.put(out + static_cast<int64_t>(a.H) * (K * V), w, lane);  // the next segment's
+    if (tid == W::NT - 1) ws.sum[piece] = sum;
+}
+
 template <typename W, typename TOut, int K, int V>
 __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(LinArgs a, Segments ws, int R) {
     using T = typename W::T;
     constexpr int C = W::C;
-    constexpr bool OUT = W::OUT;
     __shared__ __align__(16) char lds[W::kLds];
     __shared__ __align__(16) float table[2][4][C];
     __shared__ int strange[2];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int place = blockIdx.x / a.H, h = blockIdx.x - place * a.H, hk = h / (a.H / a.Hk);
-    const int n = seq_of_slot(a.cu, a.N, a.T, 1, R, place, lane);
-    int start, count;
-    seq_rows(a.cu, n, a.T, start, count);
-    const int seg = place - (start / R + n), segs = max(1, (count + R - 1) / R);
-    if (seg < 0 || seg >= segs || (!OUT && seg == segs - 1)) return;
-    const int t0 = start + seg * R, tokens = min(R, count - seg * R), chunks = (tokens + C - 1) / C;
-    const int slot = slot_of(a, n);
+    const Span x(a, R, place, lane);
+    if (x.seg < 0 || x.seg >= x.segs) return;
+    const int t0 = x.t0, tokens = x.tokens, chunks = (tokens + C - 1) / C, slot = slot_of(a, x.n);
     const int64_t held = (static_cast<int64_t>(slot) * a.H + h) * (K * V);
-    const int64_t piece = static_cast<int64_t>(place) * a.H + h;
 
     W s;
     s.clear();
-    if (OUT && segs > 1) {
-        s.get(ws.state + piece * (K * V), w, lane);
-    } else if (seg == 0 && a.s0 && slot >= 0) {
-#pragma unroll
-        for (int m = 0; m < W::M; ++m)
-#pragma unroll
-            for (int r = 0; r < W::kRegs; ++r) s.S[m][r] = a.s0[held + W::element(m, r, w, lane)];
-    }
-    if (!OUT && seg == 0) s.put(ws.state + piece * (K * V), w, lane);
+    W::prepare(lds, tid);
+    if (x.segs > 1)
+        s.get(ws.state + (static_cast<int64_t>(place) * a.H + h) * (K * V), w, lane);
+    else if (a.s0 && slot >= 0)
+        s.take(a.s0 + held, w, lane);
 
     const T *qp = static_cast<const T *>(a.q) + t0 * a.qs + hk * K, *kp = static_cast<const T *>(a.k) + t0 * a.ks + hk * K;
     const T *vp = static_cast<const T *>(a.v) + t0 * a.vs + h * V;
     TOut *op = static_cast<TOut *>(a.o) + (static_cast<int64_t>(t0) * a.H + h) * V;
-    double sum = 0.0;  // of the segment's decays so far
     auto decay = [&](int c) { return lane < min(C, tokens - c * C) ? log_decay_of(a, t0 + c * C + lane, h) : 0.f; };
     auto tabulate = [&](float g, int b, int rows) {
-        double x = static_cast<double>(g) * kLog2e;
-#pragma unroll
-        for (int d = 1; d < C; d <<= 1) {
-            const double y = __shfl_up(x, d);
-            x += lane >= d ? y : 0.0;
-        }
-        const double all = __shfl(x, C - 1);
-        sum += all;
+        double all;
+        const double y = sums(g, all);
         if (lane < C) {
-            const float hi = static_cast<float>(x);
+            const float hi = static_cast<float>(y);
             table[b][0][lane] = hi;
-            table[b][1][lane] = static_cast<float>(x - static_cast<double>(hi));
+            table[b][1][lane] = static_cast<float>(y - static_cast<double>(hi));
             table[b][2][lane] = __builtin_amdgcn_exp2f(hi);
-            table[b][3][lane] = lane < rows ? __builtin_amdgcn_exp2f(static_cast<float>(all - x)) : 0.f;
+            table[b][3][lane] = lane < rows ? __builtin_amdgcn_exp2f(static_cast<float>(all - y)) : 0.f;
         }
         if (lane == 0) strange[b] = 0;
     };
@@ -144,16 +201,7 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
         s.template chunk<TOut>(op, static_cast<int64_t>(a.H) * V, a.scale, lds, d, strange[b], rows, w, lane, next);
         op += static_cast<int64_t>(C) * a.H * V;
     }
-    if (OUT) {
-        if (seg == segs - 1 && a.sT && slot >= 0)
-#pragma unroll
-            for (int m = 0; m < W::M; ++m)
-#pragma unroll
-                for (int r = 0; r < W::kRegs; ++r) a.sT[held + W::element(m, r, w, lane)] = s.S[m][r];
-    } else {
-        s.put(ws.state + (piece + a.H) * (K * V), w, lane);  // the next segment's
-        if (tid == W::NT - 1) ws.sum[piece] = sum;
-    }
+    if (x.seg == x.segs - 1 && a.sT && slot >= 0) s.give(a.sT + held, w, lane);
 }
 
 // The states at the starts of each sequence's segments from the third on: that of the one before,
@@ -193,35 +241,30 @@ Plan plan_of(int32_t N, int32_t T, int32_t H) {
     return {static_cast<int>(64 * L), T / (64 * L) + N, true};
 }
 
-template <int K, int V, typename TOut> hipError_t launch_bf16(const LinArgs &a, hipStream_t st) {
+size_t sums_bytes(const Plan &p, int32_t H) { return (static_cast<size_t>(p.places) * H * sizeof(double) + 255) / 256 * 256; }
+
+template <typename Ends, typename All, typename TOut, int K, int V> hipError_t launch(const LinArgs &a, hipStream_t st) {
     const Plan p = plan_of(a.N, a.T, a.H);
     Segments ws{};
+    const dim3 grid(static_cast<unsigned>(p.places * a.H)), block(All::NT);
     if (p.cut) {
         ws.sum = static_cast<double *>(a.ws);
-        ws.state = reinterpret_cast<float *>(static_cast<char *>(a.ws) + (p.places * a.H * 8 + 255) / 256 * 256);
-    }
-    const dim3 grid(static_cast<unsigned>(p.places * a.H)), block(LinBf16<K, V, 0>::NT);
-    if (p.cut) {
-        hipLaunchKernelGGL((lin_segments_kernel<LinBf16<K, V, 0>, float, K, V>), grid, block, 0, st, a, ws, p.R);
+        ws.state = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sums_bytes(p, a.H));
+        hipLaunchKernelGGL((lin_ends_kernel<Ends, K, V>), grid, block, 0, st, a, ws, p.R);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         hipLaunchKernelGGL((lin_join_kernel<K * V>), dim3(a.N * a.H * (K * V / 1024)), dim3(256), 0, st, a, ws, p.R);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((lin_segments_kernel<LinBf16<K, V, sizeof(TOut) / 2>, TOut, K, V>), grid, block, 0, st, a, ws, p.R);
+    hipLaunchKernelGGL((lin_segments_kernel<All, TOut, K, V>), grid, block, 0, st, a, ws, p.R);
     return hipGetLastError();
 }
 
 template <int K, int V> hipError_t launch_dims(const LinArgs &a, hipStream_t st) {
-    const dim3 grid(a.N * a.H), block(kThreads);
-    if (a.in_dtype == KDA_F32)
-        hipLaunchKernelGGL((lin_tokens_kernel<K, V, float, float>), grid, block, 0, st, a);
-    else if (a.out_dtype == KDA_BF16)
-        return launch_bf16<K, V, bf16_t>(a, st);
-    else
-        return launch_bf16<K, V, float>(a, st);
-    return hipGetLastError();
+    if (a.in_dtype == KDA_F32) return launch<LinF32<K, V, false>, LinF32<K, V, true>, float, K, V>(a, st);
+    if (a.out_dtype == KDA_BF16) return launch<LinBf16<K, V, 0>, LinBf16<K, V, 1>, bf16_t, K, V>(a, st);
+    return launch<LinBf16<K, V, 0>, LinBf16<K, V, 2>, float, K, V>(a, st);
 }
 
 }  // namespace
@@ -231,11 +274,9 @@ hipError_t launch_lin_chunk(const LinArgs &a, hipStream_t st) {
     return a.V == 128 ? launch_dims<64, 128>(a, st) : launch_dims<64, 64>(a, st);
 }
 
-size_t lin_chunk_workspace(int32_t N, int32_t T, int32_t H, int32_t K, int32_t V, kda_dtype_t in_dtype) {
-    if (in_dtype != KDA_BF16) return 0;
+size_t lin_chunk_workspace(int32_t N, int32_t T, int32_t H, int32_t K, int32_t V) {
     const Plan p = plan_of(N, T, H);
-    if (!p.cut) return 0;
-    return (static_cast<size_t>(p.places) * H * 8 + 255) / 256 * 256 + static_cast<size_t>(p.places) * H * K * V * 4;
+    return p.cut ? sums_bytes(p, H) + static_cast<size_t>(p.places) * H * K * V * sizeof(float) : 0;
 }
 
 }  // namespace kda
