@@ -67,11 +67,11 @@ __device__ __forceinline__ double sums(float g, double &all) {
 // it and the segment's end, the state itself is not decayed step by step, and the walk ends where all
 // further weights are 0 in fp32. (Heads that forget fast look at a few chunks only.)
 template <typename W, int K, int V>
-__global__ __launch_bounds__(W::NT, 2) void lin_ends_kernel(LinArgs a, Segments ws, int R) {
+__global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_ends_kernel(LinArgs a, Segments ws, int R) {
     using T = typename W::T;
     constexpr int C = W::C;
     constexpr double kNothing = -160.0;  // 2^-150 is 0 in fp32
-    __shared__ __align__(16) char lds[2][W::kLds];
+    __shared__ __align__(16) char lds[2][W::kTiles];
     __shared__ __align__(16) float left[2][C];
     __shared__ int over[2];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -130,20 +130,19 @@ __global__ __launch_bounds__(W::NT, 2) void lin_ends_kernel(LinArgs a, Segments 
         first.clear();
         if (a.s0 && slot >= 0) first.take(s0, w, lane);
         first.put(out, w, lane);
-#pragma unroll
-        for (int m = 0; m < W::M; ++m)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) s.S[m][r] = fmaf(e, first.S[m][r], s.S[m][r]);
+        s.add(first, e);
     }
     s.put(out + static_cast<int64_t>(a.H) * (K * V), w, lane);  // the next segment's
     if (tid == W::NT - 1) ws.sum[piece] = sum;
 }
 
+// All outputs, and the states at the sequences' ends.
 template <typename W, typename TOut, int K, int V>
 __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(LinArgs a, Segments ws, int R) {
     using T = typename W::T;
     constexpr int C = W::C;
-    __shared__ __align__(16) char lds[W::kLds];
+    __shared__ __align__(16) char tiles[W::kTiles];
+    __shared__ __align__(16) char scores[W::kScores];
     __shared__ __align__(16) float table[2][4][C];
     __shared__ int strange[2];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -155,7 +154,7 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
 
     W s;
     s.clear();
-    W::prepare(lds, tid);
+    W::prepare(scores, tid);
     if (x.segs > 1)
         s.get(ws.state + (static_cast<int64_t>(place) * a.H + h) * (K * V), w, lane);
     else if (a.s0 && slot >= 0)
@@ -164,6 +163,7 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
     const T *qp = static_cast<const T *>(a.q) + t0 * a.qs + hk * K, *kp = static_cast<const T *>(a.k) + t0 * a.ks + hk * K;
     const T *vp = static_cast<const T *>(a.v) + t0 * a.vs + h * V;
     TOut *op = static_cast<TOut *>(a.o) + (static_cast<int64_t>(t0) * a.H + h) * V;
+    const bool summing = w == W::NW - 1;  // the last wave sums the decays, a chunk ahead
     auto decay = [&](int c) { return lane < min(C, tokens - c * C) ? log_decay_of(a, t0 + c * C + lane, h) : 0.f; };
     auto tabulate = [&](float g, int b, int rows) {
         double all;
@@ -177,28 +177,34 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
         }
         if (lane == 0) strange[b] = 0;
     };
+    auto load = [&](int c) {
+        s.load(qp, kp, vp, a, min(C, tokens - c * C), tid);
+        qp += C * a.qs, kp += C * a.ks, vp += C * a.vs;
+    };
     float g = 0.f;
-    if (w == W::NW - 1 && chunks > 0) {
+    if (chunks > 0) load(0);
+    if (summing && chunks > 0) {
         tabulate(decay(0), 0, tokens);
-        g = chunks > 1 ? decay(1) : 0.f;
+        if (chunks > 1) g = decay(1);
     }
-    if (chunks > 0) s.load(qp, kp, vp, a, min(C, tokens), tid);
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c) {
-        const int b = c & 1, rows = min(C, tokens - c * C);
+        const int b = c & 1;
+        const Decays d = {table[b][0], table[b][1], table[b][2], table[b][3]};
         __syncthreads();  // all have read the chunk before
-        if (s.to_lds(lds, tid)) strange[b] = 1;
-        auto next = [&] {
-            qp += C * a.qs, kp += C * a.ks, vp += C * a.vs;
-            if (c + 1 < chunks) s.load(qp, kp, vp, a, min(C, tokens - (c + 1) * C), tid);
-        };
+        if (s.to_lds(tiles, tid)) strange[b] = 1;
         __syncthreads();
-        if (w == W::NW - 1 && c + 1 < chunks) {
+        if (summing && c + 1 < chunks) {
             tabulate(g, b ^ 1, tokens - (c + 1) * C);
             if (c + 2 < chunks) g = decay(c + 2);
         }
-        const Decays d = {table[b][0], table[b][1], table[b][2], table[b][3]};
-        s.template chunk<TOut>(op, static_cast<int64_t>(a.H) * V, a.scale, lds, d, strange[b], rows, w, lane, next);
+        W::scores(scores, tiles, d, a.scale, w, lane);
+        if (c + 1 < chunks) load(c + 1);
+        s.from_state(tiles, d, a.scale, lane);
+        __syncthreads();
+        s.from_chunk(scores, tiles, __builtin_amdgcn_readfirstlane(strange[b]) != 0, w, lane);
+        s.store(op, static_cast<int64_t>(a.H) * V, tiles, min(C, tokens - c * C), w, lane);
+        s.advance(tiles, d, w, lane);
         op += static_cast<int64_t>(C) * a.H * V;
     }
     if (x.seg == x.segs - 1 && a.sT && slot >= 0) s.give(a.sT + held, w, lane);

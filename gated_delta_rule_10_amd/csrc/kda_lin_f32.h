@@ -21,15 +21,15 @@ template <int K, int V, bool OUT_> struct LinF32 {
     static constexpr int kWavesPerSimd = 2;
     static constexpr int CK = K / 4, CV = V / 4;              // 16-byte pieces of a row
     static constexpr int LK = C * CK / NT, LV = C * CV / NT;  // of a thread
-    static constexpr int kQ = 0, kK = OUT ? C * K * 4 : 0, kV = kK + C * K * 4, kP = kV + C * V * 4;
-    static constexpr int kLds = kP + (OUT ? C * C * 4 : 0);
+    static constexpr int kQ = 0, kK = OUT ? C * K * 4 : 0, kV = kK + C * K * 4;  // in LDS
+    static constexpr int kTiles = kV + C * V * 4, kScores = OUT ? C * C * 4 : 0;
     typedef float keys_t __attribute__((ext_vector_type(M)));
 
     // piece c of row t: 16 rows read at one piece fall on different banks
     template <int CH> static __device__ __forceinline__ int at(int t, int c) { return t * (CH * 16) + 16 * (c ^ (CH == 8 ? (t >> 1) & 7 : t & 15)); }
 
     f32x4 q[OUT ? LK : 1], k[LK], v[LV];  // the next chunk, on its way
-    f32x16 S[M];
+    f32x16 S[M], o;                       // the state; the chunk's outputs, transposed
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -38,8 +38,8 @@ template <int K, int V, bool OUT_> struct LinF32 {
             for (int r = 0; r < 16; ++r) S[m][r] = 0.f;
     }
     // what no chunk writes: the scores of the first 16 rows for the last 16 columns are 0
-    static __device__ __forceinline__ void prepare(char *lds, int tid) {
-        if (OUT && tid < 64) *reinterpret_cast<f32x4 *>(lds + kP + at<8>(tid & 15, 4 + (tid >> 4))) = f32x4{0.f, 0.f, 0.f, 0.f};
+    static __device__ __forceinline__ void prepare(char *scores, int tid) {
+        if (OUT && tid < 64) *reinterpret_cast<f32x4 *>(scores + at<8>(tid & 15, 4 + (tid >> 4))) = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
     // Rows from `count` on are the last one again: their scores are masked and their values weigh 0.
@@ -82,7 +82,7 @@ template <int K, int V, bool OUT_> struct LinF32 {
     }
 
     // 16 x 16 scores
-    static __device__ __forceinline__ void scores(char *lds, const Decays &d, float scale, int i0, int j0, int lane) {
+    static __device__ __forceinline__ void score_tile(char *scores, const char *lds, const Decays &d, float scale, int i0, int j0, int lane) {
         const int l = lane & 15, g = lane >> 4, i = i0 + l, j = j0 + 4 * g;  // p[r]: row i, column j + r
         f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -93,12 +93,17 @@ template <int K, int V, bool OUT_> struct LinF32 {
         const float hi = d.hi[i], lo = d.lo[i];
 #pragma unroll
         for (int r = 0; r < 4; ++r) p[r] = j + r <= i ? p[r] * (scale * __builtin_amdgcn_exp2f((hi - dh[r]) + (lo - dl[r]))) : 0.f;
-        *reinterpret_cast<f32x4 *>(lds + kP + at<8>(i, j >> 2)) = p;
+        *reinterpret_cast<f32x4 *>(scores + at<8>(i, j >> 2)) = p;
+    }
+    // the three tiles on and below the diagonal; the last wave has a later chunk's decays to sum
+    static __device__ __forceinline__ void scores(char *scores, const char *lds, const Decays &d, float scale, int w, int lane) {
+        if (w < 3 && w < NW) score_tile(scores, lds, d, scale, w ? 16 : 0, w == 2 ? 16 : 0, lane);
+        if (NW == 2 && w == 0) score_tile(scores, lds, d, scale, 16, 16, lane);
     }
 
     // O^T from the state before the chunk: column l % 32 is the token
-    __device__ __forceinline__ f32x16 from_state(const char *lds, const Decays &d, float scale, int lane) const {
-        f32x16 o = {};
+    __device__ __forceinline__ void from_state(const char *lds, const Decays &d, float scale, int lane) {
+        o = f32x16{};
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
             const keys_t x = keys(lds + kQ, lane & 31, 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3));
@@ -108,16 +113,15 @@ template <int K, int V, bool OUT_> struct LinF32 {
         const float e = scale * d.grown[lane & 31];
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[r] *= e;
-        return o;
     }
 
     // Adds V^T P^T, tokens 8 (r / 4) + 4 (l / 32) + r % 4 in step r. A masked score's 0 times an infinity or
     // NaN would be NaN: such values are left out of the products and added to the rows that they reach.
-    static __device__ __forceinline__ void from_chunk(f32x16 &o, bool odd, const char *lds, int w, int lane) {
+    __device__ __forceinline__ void from_chunk(const char *scores, const char *lds, bool odd, int w, int lane) {
         const int half = lane >> 5, i = lane & 31;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const f32x4 p = *reinterpret_cast<const f32x4 *>(lds + kP + at<8>(i, 2 * c + half));
+            const f32x4 p = *reinterpret_cast<const f32x4 *>(scores + at<8>(i, 2 * c + half));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float x = value(lds, 8 * c + 4 * half + e, 32 * w + i);
@@ -128,7 +132,7 @@ template <int K, int V, bool OUT_> struct LinF32 {
         if (!odd) return;
 #pragma unroll 1
         for (int j = 0; j < C; ++j) {
-            const float p = *reinterpret_cast<const float *>(lds + kP + at<8>(i, j >> 2) + 4 * (j & 3));
+            const float p = *reinterpret_cast<const float *>(scores + at<8>(i, j >> 2) + 4 * (j & 3));
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const float x = value(lds, j, 32 * w + 8 * (r >> 2) + 4 * half + (r & 3));
@@ -160,23 +164,14 @@ template <int K, int V, bool OUT_> struct LinF32 {
         }
     }
 
-    // one chunk, whose tiles are in LDS; odd: not 0 if some value is an infinity or NaN
-    template <typename TOut, typename Next>
-    __device__ __forceinline__ void chunk(TOut *out, int64_t stride, float scale, char *lds, const Decays &d, const int &odd, int count, int w, int lane, Next next) {
-        // the three 16 x 16 tiles on and below the diagonal; the last wave has the next chunk's decays to sum
-        if (w < 3 && w < NW) scores(lds, d, scale, w ? 16 : 0, w == 2 ? 16 : 0, lane);
-        if (NW == 2 && w == 0) scores(lds, d, scale, 16, 16, lane);
-        next();  // the loads of the next chunk leave
-        f32x16 o = from_state(lds, d, scale, lane);
-        __syncthreads();
-        from_chunk(o, __builtin_amdgcn_readfirstlane(odd) != 0, lds, w, lane);
+    __device__ __forceinline__ void store(float *out, int64_t stride, char *, int count, int w, int lane) const {
         const int half = lane >> 5, t = lane & 31;
         if (t < count)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 *reinterpret_cast<f32x4 *>(out + t * stride + 32 * w + 8 * c + 4 * half) = (f32x4){o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]};
-        update<true>(lds, d, w, lane);
     }
+    __device__ __forceinline__ void advance(const char *lds, const Decays &d, int w, int lane) { update<true>(lds, d, w, lane); }
 
     // the state as the registers hold it, in memory
     __device__ __forceinline__ void put(float *p, int w, int lane) const {
@@ -196,6 +191,13 @@ template <int K, int V, bool OUT_> struct LinF32 {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) S[m][4 * r + i] = x[i];
             }
+    }
+    // S = S + e first
+    __device__ __forceinline__ void add(const LinF32 &first, float e) {
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) S[m][r] = fmaf(e, first.S[m][r], S[m][r]);
     }
     // a [K, V] state
     __device__ __forceinline__ void take(const float *p, int w, int lane) {
