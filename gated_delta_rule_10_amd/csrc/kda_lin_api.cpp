@@ -31,7 +31,7 @@ extern "C" {
 size_t kda_lin_chunk_fwd_workspace_size(int32_t N, int32_t T_total, int32_t H, int32_t d_k, int32_t d_v,
                                         kda_dtype_t in_dtype) {
     if (!sizes_ok(N, T_total, H) || !head_dim_ok(d_k) || !head_dim_ok(d_v) || !dtype_valid(in_dtype)) return 0;
-    return lin_chunk_workspace(N, T_total, H, d_k, d_v);
+    return lin_chunk_workspace(N, T_total, H, d_k, d_v, in_dtype);
 }
 
 kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const void *v, const float *log_decay,
@@ -54,7 +54,7 @@ kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const void *v, cons
     if (!stride_ok(q_stride, Hk, d_k) || !stride_ok(k_stride, Hk, d_k) || !stride_ok(v_stride, H, d_v) ||
         !decay_ok(decay_stride, H))
         return KDA_ERR_INVALID_ARG;
-    const size_t need = lin_chunk_workspace(N, T_total, H, d_k, d_v);
+    const size_t need = lin_chunk_workspace(N, T_total, H, d_k, d_v, in_dtype);
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     LinArgs a{};
     a.q = q; a.k = k; a.v = v; a.g = log_decay; a.qs = q_stride; a.ks = k_stride; a.vs = v_stride; a.gs = decay_stride;

@@ -239,18 +239,30 @@ struct Plan {
     int64_t places;
     bool cut;
 };
-constexpr int kLeastChunks = 8;
-Plan plan_of(int32_t N, int32_t T, int32_t H) {
-    const int64_t chunks = static_cast<int64_t>(T) / 64 + N, groups = 2 * compute_units();
-    const int64_t L = max(static_cast<int64_t>(kLeastChunks), (chunks * H + groups - 1) / groups);
-    if (64 * L >= T) return {(T + 63) / 64 * 64 + 64, N, false};
+
+// The host knows the number of tokens and sequences, not the lengths. A compute unit holds one workgroup of
+// 8 waves (d_v = 128) or two of 4. Where sequences and heads alone fill the card, only a sequence of more
+// than four times the mean length is cut (16 of 217 to 3448, H = 32: uncut 199 us, at best 252 cut); else
+// segments are as long as lets all of them run at once (1 x 4000, H = 32: 63 chunks uncut 204 us, 8 to a
+// segment 64, 4 in two rounds 79, 16 on half of the card 96). From 128 chunks on, two rounds of half as
+// many end more evenly (1 x 131072: 1421 against 1503 us). Cutting is worth it from a few chunks on: uncut,
+// a chunk takes 3.3 us (fp32 11.8), cut 4.5 (16) with both walks, and 20 for two launches more.
+Plan plan_of(int32_t N, int32_t T, int32_t H, int32_t V, kda_dtype_t in_dtype) {
+    const int64_t room = compute_units() * (V == 64 ? 2 : 1), rows = static_cast<int64_t>(N) * H;
+    const int64_t mean = (static_cast<int64_t>(T) + 64 * static_cast<int64_t>(N) - 1) / (64 * static_cast<int64_t>(N));  // chunks of 64
+    int64_t L = max(static_cast<int64_t>(2), ((static_cast<int64_t>(T) / 64 + N) * H + room - 1) / room);
+    if (L >= 128) L = (L + 1) / 2;
+    const int64_t walk = in_dtype == KDA_F32 ? 118 : 33, both = in_dtype == KDA_F32 ? 160 : 45;  // tenths of us
+    const bool full = rows >= room;
+    if (full) L = max(L, 4 * mean);
+    if (64 * L >= T || (!full && 200 + both * L >= walk * mean)) return {(T + 63) / 64 * 64 + 64, N, false};
     return {static_cast<int>(64 * L), T / (64 * L) + N, true};
 }
 
 size_t sums_bytes(const Plan &p, int32_t H) { return (static_cast<size_t>(p.places) * H * sizeof(double) + 255) / 256 * 256; }
 
 template <typename Ends, typename All, typename TOut, int K, int V> hipError_t launch(const LinArgs &a, hipStream_t st) {
-    const Plan p = plan_of(a.N, a.T, a.H);
+    const Plan p = plan_of(a.N, a.T, a.H, V, a.in_dtype);
     Segments ws{};
     const dim3 grid(static_cast<unsigned>(p.places * a.H)), block(All::NT);
     if (p.cut) {
@@ -280,8 +292,8 @@ hipError_t launch_lin_chunk(const LinArgs &a, hipStream_t st) {
     return a.V == 128 ? launch_dims<64, 128>(a, st) : launch_dims<64, 64>(a, st);
 }
 
-size_t lin_chunk_workspace(int32_t N, int32_t T, int32_t H, int32_t K, int32_t V) {
-    const Plan p = plan_of(N, T, H);
+size_t lin_chunk_workspace(int32_t N, int32_t T, int32_t H, int32_t K, int32_t V, kda_dtype_t in_dtype) {
+    const Plan p = plan_of(N, T, H, V, in_dtype);
     return p.cut ? sums_bytes(p, H) + static_cast<size_t>(p.places) * H * K * V * sizeof(float) : 0;
 }
 

@@ -1,10 +1,10 @@
 // The chunk step of kda_lin_chunk.hip for fp32 inputs, with fp32 matrix
 // instructions: the products of kda_lin_bf16.h, nothing rounded below fp32.
 //
-// 32 tokens to a chunk. A wave holds 32 value channels: S[m] register r of lane l
-// is value channel l % 32 and key channel M (8 (r / 4) + 4 (l / 32) + r % 4) + m,
-// so that one read of M neighbouring key channels serves M products, both where k
-// is multiplied into the state and where the state is read.
+// 32 tokens to a chunk. A wave holds 16 value channels: S[m] register r of lane l
+// is value channel l % 16 and key channel 64 (m / 4) + 16 (l / 16) + 4 r + m % 4, so
+// that one read of 4 neighbouring key channels serves 4 products, both where k is
+// multiplied into the state and where the state is read.
 #pragma once
 
 #include "kda_attn_device.h"
@@ -12,30 +12,28 @@
 
 namespace kda {
 
-__device__ __forceinline__ f32x16 mma32(float a, float b, f32x16 c) { return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0); }
+// 4 products: one a lane of the lanes of one l / 16
+__device__ __forceinline__ f32x4 mma16(float a, float b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
 template <int K, int V, bool OUT_> struct LinF32 {
     using T = float;
     static constexpr bool OUT = OUT_;
-    static constexpr int C = 32, NW = V / 32, NT = 64 * NW, M = K / 32;
+    static constexpr int C = 32, NW = V / 16, NT = 64 * NW, M = K / 16;
     static constexpr int kWavesPerSimd = 2;
     static constexpr int CK = K / 4, CV = V / 4;              // 16-byte pieces of a row
     static constexpr int LK = C * CK / NT, LV = C * CV / NT;  // of a thread
     static constexpr int kQ = 0, kK = OUT ? C * K * 4 : 0, kV = kK + C * K * 4;  // in LDS
     static constexpr int kTiles = kV + C * V * 4, kScores = OUT ? C * C * 4 : 0;
-    typedef float keys_t __attribute__((ext_vector_type(M)));
 
-    // piece c of row t: 16 rows read at one piece fall on different banks
+    // piece c of row t: 16 rows read at one piece, and one piece of 4 rows in a row's order, fall on different banks
     template <int CH> static __device__ __forceinline__ int at(int t, int c) { return t * (CH * 16) + 16 * (c ^ (CH == 8 ? (t >> 1) & 7 : t & 15)); }
 
     f32x4 q[OUT ? LK : 1], k[LK], v[LV];  // the next chunk, on its way
-    f32x16 S[M], o;                       // the state; the chunk's outputs, transposed
+    f32x4 S[M], o[2];                     // the state; the chunk's outputs, transposed
 
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) S[m][r] = 0.f;
+        for (int m = 0; m < M; ++m) S[m] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     // what no chunk writes: the scores of the first 16 rows for the last 16 columns are 0
     static __device__ __forceinline__ void prepare(char *scores, int tid) {
@@ -76,9 +74,8 @@ template <int K, int V, bool OUT_> struct LinF32 {
     static __device__ __forceinline__ float value(const char *lds, int t, int c) {
         return *reinterpret_cast<const float *>(lds + kV + at<CV>(t, c >> 2) + 4 * (c & 3));
     }
-    // M neighbouring key channels of a row
-    static __device__ __forceinline__ keys_t keys(const char *p, int t, int group) {
-        return *reinterpret_cast<const keys_t *>(p + at<CK>(t, group * M / 4) + (M == 2 ? 8 * (group & 1) : 0));
+    template <int CH> static __device__ __forceinline__ f32x4 row(const char *p, int t, int c) {
+        return *reinterpret_cast<const f32x4 *>(p + at<CH>(t, c));
     }
 
     // 16 x 16 scores
@@ -86,9 +83,7 @@ template <int K, int V, bool OUT_> struct LinF32 {
         const int l = lane & 15, g = lane >> 4, i = i0 + l, j = j0 + 4 * g;  // p[r]: row i, column j + r
         f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int x = 0; x < CK / 4; ++x)
-            p = mma16(*reinterpret_cast<const f32x4 *>(lds + kK + at<CK>(j0 + l, 4 * x + g)),
-                      *reinterpret_cast<const f32x4 *>(lds + kQ + at<CK>(i, 4 * x + g)), p);
+        for (int x = 0; x < CK / 4; ++x) p = mma16(row<CK>(lds + kK, j0 + l, 4 * x + g), row<CK>(lds + kQ, i, 4 * x + g), p);
         const f32x4 dh = *reinterpret_cast<const f32x4 *>(d.hi + j), dl = *reinterpret_cast<const f32x4 *>(d.lo + j);
         const float hi = d.hi[i], lo = d.lo[i];
 #pragma unroll
@@ -97,123 +92,132 @@ template <int K, int V, bool OUT_> struct LinF32 {
     }
     // the three tiles on and below the diagonal; the last wave has a later chunk's decays to sum
     static __device__ __forceinline__ void scores(char *scores, const char *lds, const Decays &d, float scale, int w, int lane) {
-        if (w < 3 && w < NW) score_tile(scores, lds, d, scale, w ? 16 : 0, w == 2 ? 16 : 0, lane);
-        if (NW == 2 && w == 0) score_tile(scores, lds, d, scale, 16, 16, lane);
+        if (w < 3) score_tile(scores, lds, d, scale, w ? 16 : 0, w == 2 ? 16 : 0, lane);
     }
 
-    // O^T from the state before the chunk: column l % 32 is the token
+    // O^T from the state before the chunk: o[b] register r is channel 16 w + 4 (l / 16) + r, token 16 b + l % 16
     __device__ __forceinline__ void from_state(const char *lds, const Decays &d, float scale, int lane) {
-        o = f32x16{};
+        const int l = lane & 15, g = lane >> 4;
+        o[0] = o[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const keys_t x = keys(lds + kQ, lane & 31, 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3));
+        for (int x = 0; x < M / 4; ++x)
 #pragma unroll
-            for (int m = 0; m < M; ++m) o = mma32(S[m][r], x[m], o);
+            for (int r = 0; r < 4; ++r) {
+                f32x4 f[2];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) f[b] = row<CK>(lds + kQ, 16 * b + l, 16 * x + 4 * g + r);
+#pragma unroll
+                for (int m = 0; m < 4; ++m)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) o[b] = mma16(S[4 * x + m][r], f[b][m], o[b]);
+            }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const float e = scale * d.grown[16 * b + l];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[b][r] *= e;
         }
-        const float e = scale * d.grown[lane & 31];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) o[r] *= e;
     }
 
-    // Adds V^T P^T, tokens 8 (r / 4) + 4 (l / 32) + r % 4 in step r. A masked score's 0 times an infinity or
-    // NaN would be NaN: such values are left out of the products and added to the rows that they reach.
+    // Adds V^T P^T, tokens 16 u + 4 (l / 16) + e at a time. A masked score's 0 times an infinity or NaN
+    // would be NaN: such values are left out of the products and added to the rows that they reach.
     __device__ __forceinline__ void from_chunk(const char *scores, const char *lds, bool odd, int w, int lane) {
-        const int half = lane >> 5, i = lane & 31;
+        const int l = lane & 15, g = lane >> 4;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const f32x4 p = *reinterpret_cast<const f32x4 *>(scores + at<8>(i, 2 * c + half));
+        for (int u = 0; u < 2; ++u) {
+            f32x4 p[2];
+#pragma unroll
+            for (int b = u; b < 2; ++b) p[b] = row<8>(scores, 16 * b + l, 4 * u + g);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float x = value(lds, 8 * c + 4 * half + e, 32 * w + i);
+                float x = value(lds, 16 * u + 4 * g + e, 16 * w + l);
                 if (odd && !(fabsf(x) < INFINITY)) x = 0.f;
-                o = mma32(x, p[e], o);
+#pragma unroll
+                for (int b = u; b < 2; ++b) o[b] = mma16(x, p[b][e], o[b]);
             }
         }
         if (!odd) return;
 #pragma unroll 1
-        for (int j = 0; j < C; ++j) {
-            const float p = *reinterpret_cast<const float *>(scores + at<8>(i, j >> 2) + 4 * (j & 3));
+        for (int j = 0; j < C; ++j)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float x = value(lds, j, 32 * w + 8 * (r >> 2) + 4 * half + (r & 3));
-                if (j <= i && !(fabsf(x) < INFINITY)) o[r] += p * x;
+            for (int b = 0; b < 2; ++b) {
+                const int i = 16 * b + l;
+                const float p = *reinterpret_cast<const float *>(scores + at<8>(i, j >> 2) + 4 * (j & 3));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float x = value(lds, j, 16 * w + 4 * g + r);
+                    if (j <= i && !(fabsf(x) < INFINITY)) o[b][r] += p * x;
+                }
             }
+    }
+
+    __device__ __forceinline__ void store(float *out, int64_t stride, char *, int count, int w, int lane) const {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int t = 16 * b + (lane & 15);
+            if (t < count) *reinterpret_cast<f32x4 *>(out + t * stride + 16 * w + 4 * (lane >> 4)) = o[b];
         }
     }
 
+    // S = e^(G_C) S + K^T (V e^(G_C - G_j)), the first factor only where DECAY
     template <bool DECAY> __device__ __forceinline__ void update(const char *lds, const Decays &d, int w, int lane) {
-        const int half = lane >> 5, l = lane & 31;
+        const int l = lane & 15, g = lane >> 4;
         if (DECAY) {
             const float all = d.grown[C - 1];
 #pragma unroll
             for (int m = 0; m < M; ++m)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) S[m][r] *= all;
+                for (int r = 0; r < 4; ++r) S[m][r] *= all;
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const f32x4 e = *reinterpret_cast<const f32x4 *>(d.left + 8 * c + 4 * half);
+        for (int u = 0; u < 2; ++u) {
+            const f32x4 e = *reinterpret_cast<const f32x4 *>(d.left + 16 * u + 4 * g);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int t = 8 * c + 4 * half + i;
-                const float x = e[i] * value(lds, t, 32 * w + l);
-                const keys_t y = keys(lds + kK, t, l);
+                const int t = 16 * u + 4 * g + i;
+                const float x = e[i] * value(lds, t, 16 * w + l);
 #pragma unroll
-                for (int m = 0; m < M; ++m) S[m] = mma32(y[m], x, S[m]);
+                for (int y = 0; y < M / 4; ++y) {
+                    const f32x4 f = row<CK>(lds + kK, t, 16 * y + l);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) S[4 * y + m] = mma16(f[m], x, S[4 * y + m]);
+                }
             }
         }
-    }
-
-    __device__ __forceinline__ void store(float *out, int64_t stride, char *, int count, int w, int lane) const {
-        const int half = lane >> 5, t = lane & 31;
-        if (t < count)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                *reinterpret_cast<f32x4 *>(out + t * stride + 32 * w + 8 * c + 4 * half) = (f32x4){o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]};
     }
     __device__ __forceinline__ void advance(const char *lds, const Decays &d, int w, int lane) { update<true>(lds, d, w, lane); }
 
     // the state as the registers hold it, in memory
     __device__ __forceinline__ void put(float *p, int w, int lane) const {
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                *reinterpret_cast<f32x4 *>(p + (((w * M + m) * 4 + r) * 64 + lane) * 4) =
-                    (f32x4){S[m][4 * r], S[m][4 * r + 1], S[m][4 * r + 2], S[m][4 * r + 3]};
+        for (int m = 0; m < M; ++m) *reinterpret_cast<f32x4 *>(p + ((w * M + m) * 64 + lane) * 4) = S[m];
     }
     __device__ __forceinline__ void get(const float *p, int w, int lane) {
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const f32x4 x = *reinterpret_cast<const f32x4 *>(p + (((w * M + m) * 4 + r) * 64 + lane) * 4);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) S[m][4 * r + i] = x[i];
-            }
+        for (int m = 0; m < M; ++m) S[m] = *reinterpret_cast<const f32x4 *>(p + ((w * M + m) * 64 + lane) * 4);
     }
     // S = S + e first
     __device__ __forceinline__ void add(const LinF32 &first, float e) {
 #pragma unroll
         for (int m = 0; m < M; ++m)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) S[m][r] = fmaf(e, first.S[m][r], S[m][r]);
+            for (int r = 0; r < 4; ++r) S[m][r] = fmaf(e, first.S[m][r], S[m][r]);
     }
     // a [K, V] state
     __device__ __forceinline__ void take(const float *p, int w, int lane) {
 #pragma unroll
         for (int m = 0; m < M; ++m)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) S[m][r] = p[element(m, r, w, lane)];
+            for (int r = 0; r < 4; ++r) S[m][r] = p[element(m, r, w, lane)];
     }
     __device__ __forceinline__ void give(float *p, int w, int lane) const {
 #pragma unroll
         for (int m = 0; m < M; ++m)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) p[element(m, r, w, lane)] = S[m][r];
+            for (int r = 0; r < 4; ++r) p[element(m, r, w, lane)] = S[m][r];
     }
     static __device__ __forceinline__ int element(int m, int r, int w, int lane) {
-        return (M * (8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) + m) * V + 32 * w + (lane & 31);
+        return (64 * (m >> 2) + 16 * (lane >> 4) + 4 * r + (m & 3)) * V + 16 * w + (lane & 15);
     }
 };
 

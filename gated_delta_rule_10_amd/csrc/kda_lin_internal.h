@@ -29,6 +29,6 @@ hipError_t launch_lin_chunk(const LinArgs &a, hipStream_t stream);
 hipError_t launch_lin_decode(const LinArgs &a, hipStream_t stream);  // N sequences of one token
 
 // Workspace bytes of a prompt call on the current device.
-size_t lin_chunk_workspace(int32_t N, int32_t T, int32_t H, int32_t K, int32_t V);
+size_t lin_chunk_workspace(int32_t N, int32_t T, int32_t H, int32_t K, int32_t V, kda_dtype_t in_dtype);
 
 }  // namespace kda
