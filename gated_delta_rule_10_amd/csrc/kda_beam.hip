@@ -2,13 +2,15 @@
 // (kda_beam_select) and the states' reordering after it (kda_state_reorder).
 //
 // Selection. The K best candidates of a request are among the K best logits of
-// each of its beams, so one pass over the logits is enough: every wave keeps, for
-// its piece of a row, the running maximum and sum of the softmax and a list of
-// the K best (logit, token), one entry to a lane, sorted. A piece's threshold
-// starts at the K-th largest of the lanes' own maxima over the first batch (K
-// tokens at least as good are there) and rises with the list, so that few tokens
-// get as far as an insertion. A second launch, one workgroup to a request, joins
-// the pieces: rows' sums in fp64, then the K best of the lists' candidates.
+// each of its beams, so one pass over the logits is enough. A workgroup takes a
+// piece of a row: the running maximum and sum of its softmax, and the tokens that
+// can be among the K best, which are those not below a bar that K tokens reach.
+// Any K lanes' own maxima are such tokens, so the bar is the K-th of them, at best
+// over the waves, and few tokens pass it: they go to a list in LDS, in any order.
+// A second launch, one workgroup to a request, joins the pieces: rows' sums in
+// fp64, a bar over the lists' candidates, and the order of what passes it. Where a
+// list overflows (many equal logits, rising ones), the workgroup looks at its
+// piece again and keeps the K best in order, one insertion after the other.
 #include "kda_attn_internal.h"
 #include "kda_beam_internal.h"
 #include "kda_device.h"
@@ -25,82 +27,106 @@ template <typename F> struct Key {
     uint32_t i;
     __device__ __forceinline__ bool before(const Key &o) const { return v > o.v || (v == o.v && i < o.i); }
 };
-template <typename F> __device__ __forceinline__ Key<F> no_key() { return {static_cast<F>(-INFINITY), 0xFFFFFFFFu}; }
-template <typename F> __device__ __forceinline__ Key<F> from_lane(const Key<F> &k, int lane) {
-    return {__shfl(k.v, lane), static_cast<uint32_t>(__shfl(static_cast<int>(k.i), lane))};
+template <typename F> __device__ __forceinline__ Key<F> no_key();
+template <> __device__ __forceinline__ Key<float> no_key<float>() { return {-INFINITY, 0xFFFFFFFFu}; }
+// (Put together from halves that the compiler does not see: it has set a pair of scalar registers to the
+// constant by one instruction whose literal has 32 bits, which made it 0.)
+template <> __device__ __forceinline__ Key<double> no_key<double>() {
+    uint32_t hi = 0xFFF00000u;
+    __asm__("" : "+s"(hi));
+    return {__builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32), 0xFFFFFFFFu};
 }
-// Lane l and its partner l ^ m: the better one to the lower lane where `down`.
-template <typename F> __device__ __forceinline__ void exchange(Key<F> &k, int m, bool better) {
-    const Key<F> o = {__shfl_xor(k.v, m), static_cast<uint32_t>(__shfl_xor(static_cast<int>(k.i), m))};
-    if (o.before(k) == better) k = o;
+// the value of a lane that is the same in all lanes
+__device__ __forceinline__ float read_lane(float x, int lane) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane)); }
+__device__ __forceinline__ double read_lane(double x, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), lane), hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), lane);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
-// 64 keys, one a lane, into falling order
-template <typename F> __device__ __forceinline__ void sort64(Key<F> &k, int lane) {
-#pragma unroll
-    for (int n = 2; n <= 64; n <<= 1)
-#pragma unroll
-        for (int m = n / 2; m > 0; m >>= 1) exchange(k, m, ((lane & m) == 0) == ((lane & n) == 0 || n == 64));
+template <typename F> __device__ __forceinline__ Key<F> read_lane(const Key<F> &k, int lane) {
+    return {read_lane(k.v, lane), static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(k.i), lane))};
 }
-// The better half of two sorted lists, sorted: of a and the reversed b the better one in each lane
-// is in neither order, but bitonic.
-template <typename F> __device__ __forceinline__ void merge64(Key<F> &a, const Key<F> &b, int lane) {
-    const Key<F> r = from_lane(b, 63 - lane);
-    if (r.before(a)) a = r;
+// the value of the lane below (lane 0: its own)
+__device__ __forceinline__ uint32_t lane_below(uint32_t x) { return __builtin_amdgcn_update_dpp(x, x, 0x138, 0xF, 0xF, false); }
+__device__ __forceinline__ float lane_below(float x) { return __uint_as_float(lane_below(__float_as_uint(x))); }
+__device__ __forceinline__ double lane_below(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(lane_below(static_cast<uint32_t>(u >> 32))) << 32 | lane_below(static_cast<uint32_t>(u)));
+}
+
+// A value that K of the lanes' P numbers each reach (-infinity if they do not): the 16 highest bits of the
+// K-th largest, in the order of unsigned numbers.
+template <int P> __device__ __forceinline__ float reached_by(const float (&x)[P], int K) {
+    uint32_t u[P], p = 0;
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) exchange(a, m, (lane & m) == 0);
+    for (int i = 0; i < P; ++i) {
+        const uint32_t bits = __float_as_uint(x[i]);
+        u[i] = x[i] > -INFINITY ? (bits & 0x80000000u ? ~bits : bits | 0x80000000u) : 0;
+    }
+#pragma unroll
+    for (int b = 31; b >= 16; --b) {
+        const uint32_t q = p | 1u << b;
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) n += __popcll(__ballot(u[i] >= q));
+        if (n >= K) p = q;
+    }
+    // below every number but -infinity: nothing is known
+    return p <= 0x007FFFFFu ? -INFINITY : __uint_as_float(p & 0x80000000u ? p & 0x7FFFFFFFu : ~p);
 }
 
 // A sorted list of the wave's K best so far, entry l in lane l.
 template <typename F> struct Best {
-    Key<F> list, last;  // last: the K-th (wave-uniform)
+    Key<F> list, last;  // last: the K-th (the same in all lanes)
     int K, lane;
     __device__ __forceinline__ void start(int K_, int lane_) {
         list = last = no_key<F>();
         K = K_;
         lane = lane_;
     }
-    __device__ __forceinline__ void take_last() { last = from_lane(list, K - 1); }
     // all lanes' keys for which `in` holds, one after the other
     __device__ __forceinline__ void insert(const Key<F> &k, bool in) {
         uint64_t m = __ballot(in && k.before(last));
         while (m) {
-            const Key<F> x = from_lane(k, __ffsll(static_cast<unsigned long long>(m)) - 1);
+            const Key<F> x = read_lane(k, __ffsll(static_cast<unsigned long long>(m)) - 1);
             m &= m - 1;
             if (!x.before(last)) continue;
             const int at = __popcll(__ballot(list.before(x)));
-            const Key<F> up = {__shfl_up(list.v, 1), static_cast<uint32_t>(__shfl_up(static_cast<int>(list.i), 1))};
+            const Key<F> up = {lane_below(list.v), lane_below(list.i)};
             if (lane > at) list = up;
             if (lane == at) list = x;
-            take_last();
+            last = read_lane(list, K - 1);
         }
     }
 };
 
-// Parts of a row's workspace: pieces are written by the first launch, one per workgroup.
+// Parts of a row's workspace, written by the first launch, one per workgroup: 64 tokens, those that are
+// none with the value -infinity.
 struct Pieces {
     double *sum;
     float *top, *value;
     int32_t *token;
 };
-__host__ __device__ inline Pieces pieces_of(void *ws, int64_t rows, int S, int K) {
+__host__ __device__ inline Pieces pieces_of(void *ws, int64_t rows, int S) {
     Pieces p;
     p.sum = static_cast<double *>(ws);
     p.top = reinterpret_cast<float *>(p.sum + rows * S);
     p.value = p.top + rows * S;
-    p.token = reinterpret_cast<int32_t *>(p.value + rows * S * K);
+    p.token = reinterpret_cast<int32_t *>(p.value + rows * S * 64);
     return p;
 }
 
 template <typename T> struct Batch;
 template <> struct Batch<float> {
     static constexpr int kPer = 4, kLoads = 4;  // elements of 16 bytes, loads of a lane
-    static __device__ __forceinline__ void load(const float *p, float *x) { __builtin_memcpy(x, p, 16); }
+    static __device__ __forceinline__ void unpack(const uint4 &w, float *x) { __builtin_memcpy(x, &w, 16); }
+    static constexpr uint32_t kNothing = 0xFF800000u;  // -infinity
 };
 template <> struct Batch<bf16_t> {
-    static constexpr int kPer = 8, kLoads = 2;
-    static __device__ __forceinline__ void load(const bf16_t *p, float *x) {
-        uint32_t u[4];
-        __builtin_memcpy(u, p, 16);
+    static constexpr int kPer = 8, kLoads = 4;
+    static constexpr uint32_t kNothing = 0xFF80FF80u;
+    static __device__ __forceinline__ void unpack(const uint4 &w, float *x) {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             x[2 * i] = __uint_as_float(u[i] << 16);
@@ -131,20 +157,44 @@ struct RowSum {
             os * static_cast<double>(__builtin_amdgcn_exp2f((om - ref) * kLog2e));
         m = now;
     }
-    __device__ __forceinline__ void join_wave() {
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) {
-            const float om = __shfl_xor(m, d);
-            const double os = __shfl_xor(s, d);
-            join(om, os);
+    // of groups of `lanes` (a power of two) lanes
+    __device__ __forceinline__ void join_lanes(int lanes) {
+        float now = m;
+        for (int d = lanes / 2; d > 0; d >>= 1) now = fmaxf(now, __shfl_xor(now, d));
+        s *= static_cast<double>(__builtin_amdgcn_exp2f((m - (now == -INFINITY ? 0.f : now)) * kLog2e));
+        m = now;
+        for (int d = lanes / 2; d > 0; d >>= 1) s += __shfl_xor(s, d);
+    }
+};
+
+// Candidates in LDS, in no order.
+template <typename F, int SIZE> struct List {
+    F value[SIZE];
+    uint32_t index[SIZE];
+    int count;
+    // what passes is added; the count goes on past the list's end
+    __device__ __forceinline__ void add(const Key<F> &k, bool in, int lane) {
+        const uint64_t m = __ballot(in);
+        if (m == 0) return;
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&count, __popcll(m));
+        at = __builtin_amdgcn_readfirstlane(at) + __popcll(m & ((1ull << lane) - 1));
+        if (in && at < SIZE) {
+            value[at] = k.v;
+            index[at] = k.i;
         }
+    }
+    // all of it (one wave)
+    __device__ __forceinline__ void sort(Best<F> &best, int lane) const {
+        for (int i = lane; i < count + lane; i += 64) best.insert({value[i < count ? i : 0], index[i < count ? i : 0]}, i < count);
     }
 };
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void select_pieces_kernel(SelectArgs a, int S) {
     constexpr int PER = Batch<T>::kPer, LOADS = Batch<T>::kLoads, E = PER * LOADS;
-    __shared__ float lv[kWaves][64], lm[kWaves];
+    __shared__ List<float, 256> list;
+    __shared__ float lm[kWaves], lv[kWaves][64];
     __shared__ uint32_t li[kWaves][64];
     __shared__ double ls[kWaves];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -157,130 +207,235 @@ __global__ __launch_bounds__(kThreads) void select_pieces_kernel(SelectArgs a, i
     const int pieces = S * kWaves, piece = split * kWaves + w;
     const int b0 = static_cast<int>(static_cast<int64_t>(blocks) * piece / pieces);
     const int b1 = static_cast<int>(static_cast<int64_t>(blocks) * (piece + 1) / pieces);
-
-    RowSum sum = {-INFINITY, 0.0};
-    Best<float> best;
-    best.start(a.K, lane);
-    if (piece == 0 && tail < a.V) {
-        const bool in = tail + lane < a.V;
-        const float x[1] = {in ? io<T>::load(x0 + tail + lane) : -INFINITY};
-        sum.add(x);
-        best.insert({x[0], static_cast<uint32_t>(tail + lane)}, x[0] > -INFINITY);
-    }
-    float least = -INFINITY;  // K of the piece's elements are at least this
-    for (int b = b0; b < b1; b += 64 * LOADS) {
-        float x[E];
+    uint4 raw[LOADS];
+    auto load = [&](int b) {
 #pragma unroll
         for (int u = 0; u < LOADS; ++u) {
             const int at = b + 64 * u + lane;
-            if (at < b1) {
-                Batch<T>::load(x0 + static_cast<int64_t>(at) * PER, x + PER * u);
-            } else {
+            raw[u] = make_uint4(Batch<T>::kNothing, Batch<T>::kNothing, Batch<T>::kNothing, Batch<T>::kNothing);
+            if (at < b1) __builtin_memcpy(&raw[u], x0 + static_cast<int64_t>(at) * PER, 16);
+        }
+    };
+    auto token = [&](int b, int u, int j) { return static_cast<uint32_t>((b + 64 * u + lane) * PER + j); };
+    load(b0);
+    const bool odd = w == 0 && split == 0 && tail + lane < a.V;
+    const float last[1] = {odd ? io<T>::load(x0 + tail + lane) : -INFINITY};
+    if (tid == 0) list.count = 0;
+
+    RowSum sum = {-INFINITY, 0.0};
+    sum.add(last);
+    float bar = -INFINITY;
+    for (int b = b0; b < b1 || b == b0; b += 64 * LOADS) {
+        float x[E];
 #pragma unroll
-                for (int j = 0; j < PER; ++j) x[PER * u + j] = -INFINITY;
-            }
-        }
+        for (int u = 0; u < LOADS; ++u) Batch<T>::unpack(raw[u], x + PER * u);
+        if (b + 64 * LOADS < b1) load(b + 64 * LOADS);
         const float top = sum.add(x);
-        if (b == b0) {
-            Key<float> k = {top, static_cast<uint32_t>(lane)};
-            sort64(k, lane);
-            least = __shfl(k.v, a.K - 1);
+        if (b == b0) {  // once, all waves: of all lanes' maxima
+            lv[w][lane] = top;
+            __syncthreads();
+            float tops[kWaves];
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) tops[i] = lv[i][lane];
+            bar = reached_by(tops, a.K);
+            list.add({last[0], static_cast<uint32_t>(tail + lane)}, odd && last[0] >= bar && last[0] > -INFINITY, lane);
+        } else if (__popcll(__ballot(top >= bar)) > a.K) {
+            const float tops[1] = {top};
+            bar = fmaxf(bar, reached_by(tops, a.K));
         }
-        const float bar = fmaxf(least, best.last.v);
         if (!__any(top >= bar && top > -INFINITY)) continue;
 #pragma unroll
         for (int u = 0; u < LOADS; ++u)
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 const float v = x[PER * u + j];
-                best.insert({v, static_cast<uint32_t>((b + 64 * u + lane) * PER + j)}, v >= bar && v > -INFINITY);
+                list.add({v, token(b, u, j)}, v >= bar && v > -INFINITY, lane);
             }
     }
-    sum.join_wave();
-    lv[w][lane] = best.list.v;
-    li[w][lane] = best.list.i;
+    sum.join_lanes(64);
     if (lane == 0) {
         lm[w] = sum.m;
         ls[w] = sum.s;
     }
     __syncthreads();
-    if (w != 0) return;
-#pragma unroll
-    for (int i = 1; i < kWaves; ++i) {
-        merge64(best.list, {lv[i][lane], li[i][lane]}, lane);
-        sum.join(lm[i], ls[i]);
-    }
-    const Pieces p = pieces_of(a.ws, static_cast<int64_t>(a.N) * a.W, S, a.K);
+    const Pieces p = pieces_of(a.ws, static_cast<int64_t>(a.N) * a.W, S);
     const int64_t at = static_cast<int64_t>(row) * S + split;
-    if (lane < a.K) {
-        p.value[at * a.K + lane] = best.list.v;
-        p.token[at * a.K + lane] = static_cast<int32_t>(best.list.i);
+    const int count = list.count;
+    Best<float> best;
+    best.start(a.K, lane);
+    if (count > 256) {  // too many pass: the K best in order, after all
+        best.insert({last[0], static_cast<uint32_t>(tail + lane)}, odd && last[0] > -INFINITY);
+        for (int b = b0; b < b1; b += 64 * LOADS) {
+            float x[E];
+            load(b);
+#pragma unroll
+            for (int u = 0; u < LOADS; ++u) Batch<T>::unpack(raw[u], x + PER * u);
+            float top[1] = {x[0]};
+#pragma unroll
+            for (int i = 1; i < E; ++i) top[0] = fmaxf(top[0], x[i]);
+            bar = fmaxf(bar, reached_by(top, a.K));
+#pragma unroll
+            for (int u = 0; u < LOADS; ++u)
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const float v = x[PER * u + j];
+                    best.insert({v, token(b, u, j)}, v >= bar && v > -INFINITY);
+                }
+        }
+        lv[w][lane] = best.list.v;
+        li[w][lane] = best.list.i;
+        __syncthreads();
     }
+    if (w != 0) return;
+    if (count > 256) {
+        for (int i = 1; i < kWaves; ++i) best.insert({lv[i][lane], li[i][lane]}, lane < a.K && lv[i][lane] > -INFINITY);
+    } else if (count > 64) {
+        list.sort(best, lane);
+    } else if (lane < count) {  // few enough to be handed on as they are
+        best.list = {list.value[lane], list.index[lane]};
+    }
+    p.value[at * 64 + lane] = best.list.v;
+    p.token[at * 64 + lane] = static_cast<int32_t>(best.list.i);
     if (lane == 0) {
+        for (int i = 1; i < kWaves; ++i) sum.join(lm[i], ls[i]);
         p.top[at] = sum.m;
         p.sum[at] = sum.s;
     }
 }
 
+// A request's choice, four waves. A wave holds 16 lists of 64 at a time, each turned by 4 lanes more than
+// the one before: their candidates are at their starts. What is below the bar for sure is sorted out in
+// fp32, by sums that are off by less than the bar is lowered; what passes is computed in fp64.
+constexpr int kLists = 16;
+
 __global__ __launch_bounds__(kThreads) void select_join_kernel(SelectArgs a, int S) {
     __shared__ double lse[64], score[64], lv[kWaves][64];
     __shared__ uint32_t li[kWaves][64];
+    __shared__ float tops[kWaves][64], offset[64 * 64];
+    __shared__ List<double, 256> some;
     __shared__ uint8_t ended[64];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n = blockIdx.x;
-    const Pieces p = pieces_of(a.ws, static_cast<int64_t>(a.N) * a.W, S, a.K);
+    const Pieces p = pieces_of(a.ws, static_cast<int64_t>(a.N) * a.W, S);
     const int64_t row0 = static_cast<int64_t>(n) * a.W;
-    for (int r = w; r < a.W; r += kWaves) {
+    const int lists = a.W * S;
+    float v[kLists];
+    int32_t token[kLists];
+    // (what a row that has ended leaves is whatever was there: its offset is NaN)
+    auto load = [&](int first) {
+#pragma unroll
+        for (int j = 0; j < kLists; ++j) {
+            const int list = min(first + j * kWaves, lists - 1);
+            const int64_t at = (row0 * S + list) * 64 + ((lane + 4 * j) & 63);
+            v[j] = p.value[at];
+            token[j] = p.token[at];
+        }
+    };
+    load(w);
+    if (tid == 0) some.count = 0;
+    const int group = S <= 16 ? 16 : 64;  // lanes to a row's sum
+    for (int r0 = 0; r0 < a.W; r0 += kThreads / group) {
+        const int r = r0 + tid / group, i = tid % group;
+        const bool row = r < a.W, over = row && a.done && a.done[row0 + r];
         RowSum sum = {-INFINITY, 0.0};
-        const bool over = a.done && a.done[row0 + r];
-        if (lane < S && !over) sum = {p.top[(row0 + r) * S + lane], p.sum[(row0 + r) * S + lane]};
-        sum.join_wave();
-        if (lane == 0) {
-            lse[r] = static_cast<double>(sum.m) + log(sum.s);
-            score[r] = static_cast<double>(a.scores[row0 + r]);
-            ended[r] = over;
+        if (row && !over && i < S) sum = {p.top[(row0 + r) * S + i], p.sum[(row0 + r) * S + i]};
+        sum.join_lanes(group);
+        if (row) {
+            const double l = static_cast<double>(sum.m) + log(sum.s), c = static_cast<double>(a.scores[row0 + r]);
+            for (int j = i; j < S; j += group) offset[r * S + j] = over ? NAN : static_cast<float>(c - l);
+            if (i == 0) {
+                lse[r] = l;
+                score[r] = c;
+                ended[r] = over;
+            }
         }
     }
     __syncthreads();
-    // the lists' first entries first: the rest seldom pass them
-    Best<double> best;
-    best.start(a.K, lane);
-    const int lists = a.W * S, all = lists * a.K;
-    for (int c = w * 64; c < all; c += kThreads) {
-        const int i = c + lane, rank = i / lists, list = i - rank * lists, r = list / S;
-        Key<double> k = no_key<double>();
-        if (i < all) {
-            if (!ended[r]) {
-                const int64_t at = (row0 * S + list) * a.K + rank;
-                const float v = p.value[at];
-                if (v > -INFINITY) k = {static_cast<double>(v) - lse[r] + score[r], static_cast<uint32_t>(r) * a.V + p.token[at]};
-            } else if (rank == 0 && list == r * S) {
-                k = {score[r], static_cast<uint32_t>(r) * a.V + a.done_token};
+    const Key<double> done = tid < a.W && ended[tid] ? Key<double>{score[tid], static_cast<uint32_t>(tid) * a.V + a.done_token} : no_key<double>();
+    // all lanes' own maxima give a bar that K candidates reach
+    float top = static_cast<float>(done.v), far = 0.f;
+    for (int list = w; list < lists; list += kLists * kWaves) {
+        if (list != w) load(list);
+#pragma unroll
+        for (int j = 0; j < kLists; ++j)
+            if (list + j * kWaves < lists) {
+                const float x = v[j] + offset[list + j * kWaves];
+                top = fmaxf(top, x);
+                if (x > -INFINITY) far = fmaxf(far, fabsf(v[j]));
             }
-        }
-        const bool in = k.v > -INFINITY;
-        if (c == w * 64) {
-            if (!in) k = no_key<double>();  // NaN
-            sort64(k, lane);
-            best.list = k;
-            best.take_last();
-        } else {
-            best.insert(k, in);
+    }
+    tops[w][lane] = top;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) far = fmaxf(far, __shfl_xor(far, d));
+    if (lane == 0) lv[w][0] = static_cast<double>(far);
+    __syncthreads();
+    float all[kWaves];
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+        all[i] = tops[i][lane];
+        far = fmaxf(far, static_cast<float>(lv[i][0]));
+    }
+    // v + offset rounds the offset and the sum, by 2^-24 of |offset| <= |v| + |x| and of |x|, in the K and in
+    // the one compared with them
+    float bar = reached_by(all, a.K);
+    if (bar > -INFINITY) bar -= 1e-6f * (fabsf(bar) + far);
+    for (int list = w; list < lists; list += kLists * kWaves) {
+        if (lists > kLists * kWaves) load(list);
+#pragma unroll
+        for (int j = 0; j < kLists; ++j) {
+            const int at = list + j * kWaves;
+            const float x = at < lists ? v[j] + offset[at] : -INFINITY;
+            const bool in = x >= bar && x > -INFINITY;
+            if (!__any(in)) continue;
+            const int r = at / S;
+            some.add({static_cast<double>(v[j]) - lse[r] + score[r], static_cast<uint32_t>(r) * a.V + token[j]}, in, lane);
         }
     }
+    some.add(done, done.v > -INFINITY && done.v >= static_cast<double>(bar), lane);
+    __syncthreads();
+    auto write = [&](int rank, const Key<double> &k) {
+        if (rank >= a.K) return;
+        const bool found = k.v > -INFINITY;
+        const int64_t at = static_cast<int64_t>(n) * a.K + rank;
+        const uint32_t r = k.i / static_cast<uint32_t>(a.V);
+        a.out_scores[at] = static_cast<float>(k.v);
+        a.out_parent[at] = found ? static_cast<int32_t>(r) : -1;
+        a.out_token[at] = found ? static_cast<int32_t>(k.i - r * a.V) : -1;
+    };
+    const int count = some.count;
+    if (count <= 256) {  // the places of the few that reach the bar, by counting; behind them, places of none
+        const Key<double> k = tid < count ? Key<double>{some.value[tid], some.index[tid]} : no_key<double>();
+        int rank = 0;
+        if (count <= 64) {
+            if (w != 0) return;
+            for (int i = 0; i < count; ++i) rank += read_lane(k, i).before(k);
+        } else {
+#pragma unroll 4
+            for (int i = 0; i < count; ++i) rank += Key<double>{some.value[i], some.index[i]}.before(k);
+        }
+        write(tid < count ? rank : tid, k);
+        return;
+    }
+    // too many reach it: in order, after all
+    Best<double> best;
+    best.start(a.K, lane);
+    best.insert(done, done.v > -INFINITY);
+    for (int list = w; list < lists; list += kLists * kWaves) {
+#pragma unroll 1
+        for (int j = 0; j < kLists; ++j) {
+            const int at = list + j * kWaves, r = min(at, lists - 1) / S;
+            const int64_t place = (row0 * S + min(at, lists - 1)) * 64 + lane;
+            const float x = p.value[place];
+            best.insert({static_cast<double>(x) - lse[r] + score[r], static_cast<uint32_t>(r) * a.V + p.token[place]},
+                        at < lists && x > -INFINITY && x + offset[min(at, lists - 1)] >= bar);
+        }
+    }
+    __syncthreads();  // lv is free
     lv[w][lane] = best.list.v;
     li[w][lane] = best.list.i;
     __syncthreads();
     if (w != 0) return;
-#pragma unroll
-    for (int i = 1; i < kWaves; ++i) merge64(best.list, {lv[i][lane], li[i][lane]}, lane);
-    if (lane < a.K) {
-        const bool some = best.list.v > -INFINITY;
-        const int64_t at = static_cast<int64_t>(n) * a.K + lane;
-        const uint32_t r = best.list.i / static_cast<uint32_t>(a.V);
-        a.out_scores[at] = static_cast<float>(best.list.v);
-        a.out_parent[at] = some ? static_cast<int32_t>(r) : -1;
-        a.out_token[at] = some ? static_cast<int32_t>(best.list.i - r * a.V) : -1;
-    }
+    for (int i = 1; i < kWaves; ++i) best.insert({lv[i][lane], li[i][lane]}, lane < a.K && lv[i][lane] > -INFINITY);
+    write(lane, best.list);
 }
 
 // Workgroups per row: enough to fill the card, of at least 2048 tokens.
@@ -357,9 +512,9 @@ __global__ __launch_bounds__(kThreads) void reorder_kernel(ReorderArgs a, int X)
 
 }  // namespace
 
-size_t beam_select_workspace(int32_t N, int32_t W, int32_t V, int32_t K) {
+size_t beam_select_workspace(int32_t N, int32_t W, int32_t V) {
     const size_t pieces = static_cast<size_t>(N) * W * splits_of(N, W, V);
-    return pieces * (sizeof(double) + sizeof(float) + K * (sizeof(float) + sizeof(int32_t)));
+    return pieces * (sizeof(double) + sizeof(float) + 64 * (sizeof(float) + sizeof(int32_t)));
 }
 
 hipError_t launch_beam_select(const SelectArgs &a, hipStream_t st) {

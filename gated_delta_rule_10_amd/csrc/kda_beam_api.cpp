@@ -25,7 +25,7 @@ bool select_ok(int32_t N, int32_t W, int32_t V, int32_t K) {
 extern "C" {
 
 size_t kda_beam_select_workspace_size(int32_t N, int32_t W, int32_t V, int32_t K) {
-    return select_ok(N, W, V, K) ? beam_select_workspace(N, W, V, K) : 0;
+    return select_ok(N, W, V, K) ? beam_select_workspace(N, W, V) : 0;
 }
 
 kda_status_t kda_beam_select(const void *logits, int64_t stride, const float *scores, const uint8_t *done,
@@ -37,7 +37,7 @@ kda_status_t kda_beam_select(const void *logits, int64_t stride, const float *sc
     for (const void *p : all)
         if (!given(p)) return KDA_ERR_INVALID_ARG;
     if (!aligned16(done) || (done && (done_token < 0 || done_token >= V)) || !aligned16(workspace)) return KDA_ERR_INVALID_ARG;
-    if (!workspace || workspace_bytes < beam_select_workspace(N, W, V, K)) return KDA_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < beam_select_workspace(N, W, V)) return KDA_ERR_WORKSPACE;
     SelectArgs a{};
     a.logits = logits; a.stride = stride; a.scores = scores; a.done = done; a.done_token = done_token;
     a.N = N; a.W = W; a.V = V; a.K = K; a.dtype = dtype;

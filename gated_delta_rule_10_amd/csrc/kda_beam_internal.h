@@ -34,6 +34,6 @@ hipError_t launch_beam_select(const SelectArgs &a, hipStream_t stream);
 hipError_t launch_state_reorder(const ReorderArgs &a, hipStream_t stream);
 
 // Workspace bytes of a selection on the current device.
-size_t beam_select_workspace(int32_t N, int32_t W, int32_t V, int32_t K);
+size_t beam_select_workspace(int32_t N, int32_t W, int32_t V);
 
 }  // namespace kda
