@@ -11,6 +11,8 @@
 // fp64, a bar over the lists' candidates, and the order of what passes it. Where a
 // list overflows (many equal logits, rising ones), the workgroup looks at its
 // piece again and keeps the K best in order, one insertion after the other.
+#include <cfloat>
+
 #include "kda_attn_internal.h"
 #include "kda_beam_internal.h"
 #include "kda_device.h"
@@ -224,7 +226,8 @@ __global__ __launch_bounds__(kThreads) void select_pieces_kernel(SelectArgs a, i
 
     RowSum sum = {-INFINITY, 0.0};
     sum.add(last);
-    float bar = -INFINITY;
+    // (the lowest finite number where nothing is known: -infinity never passes)
+    float bar = -FLT_MAX;
     for (int b = b0; b < b1 || b == b0; b += 64 * LOADS) {
         float x[E];
 #pragma unroll
@@ -237,19 +240,19 @@ __global__ __launch_bounds__(kThreads) void select_pieces_kernel(SelectArgs a, i
             float tops[kWaves];
 #pragma unroll
             for (int i = 0; i < kWaves; ++i) tops[i] = lv[i][lane];
-            bar = reached_by(tops, a.K);
-            list.add({last[0], static_cast<uint32_t>(tail + lane)}, odd && last[0] >= bar && last[0] > -INFINITY, lane);
+            bar = fmaxf(bar, reached_by(tops, a.K));
+            list.add({last[0], static_cast<uint32_t>(tail + lane)}, odd && last[0] >= bar, lane);
         } else if (__popcll(__ballot(top >= bar)) > a.K) {
             const float tops[1] = {top};
             bar = fmaxf(bar, reached_by(tops, a.K));
         }
-        if (!__any(top >= bar && top > -INFINITY)) continue;
+        if (!__any(top >= bar)) continue;
 #pragma unroll
         for (int u = 0; u < LOADS; ++u)
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
                 const float v = x[PER * u + j];
-                list.add({v, token(b, u, j)}, v >= bar && v > -INFINITY, lane);
+                list.add({v, token(b, u, j)}, v >= bar, lane);
             }
     }
     sum.join_lanes(64);
@@ -279,7 +282,7 @@ __global__ __launch_bounds__(kThreads) void select_pieces_kernel(SelectArgs a, i
 #pragma unroll
                 for (int j = 0; j < PER; ++j) {
                     const float v = x[PER * u + j];
-                    best.insert({v, token(b, u, j)}, v >= bar && v > -INFINITY);
+                    best.insert({v, token(b, u, j)}, v >= bar);
                 }
         }
         lv[w][lane] = best.list.v;
