@@ -38,6 +38,8 @@ kda_status_t kda_beam_select(const void *logits, int64_t stride, const float *sc
         if (!given(p)) return KDA_ERR_INVALID_ARG;
     if (!aligned16(done) || (done && (done_token < 0 || done_token >= V)) || !aligned16(workspace)) return KDA_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < beam_select_workspace(N, W, V)) return KDA_ERR_WORKSPACE;
+    // a request's new scores may only take the place of its own
+    if (out_scores == scores && K != W) return KDA_ERR_INVALID_ARG;
     SelectArgs a{};
     a.logits = logits; a.stride = stride; a.scores = scores; a.done = done; a.done_token = done_token;
     a.N = N; a.W = W; a.V = V; a.K = K; a.dtype = dtype;
@@ -49,7 +51,7 @@ kda_status_t kda_state_reorder(void *states, int64_t layer_stride, int32_t layer
                                int64_t slot_bytes, const int32_t *slots, const int32_t *parent, int32_t *slots_out,
                                int32_t N, int32_t W, hipStream_t stream) {
     if (!beams_ok(N, W) || layers < 1 || num_slots < 1 || static_cast<int64_t>(N) * layers >= 1 << 22) return KDA_ERR_INVALID_ARG;
-    if (!given(states) || !given(slots) || !given(parent) || !given(slots_out) || slots == slots_out) return KDA_ERR_INVALID_ARG;
+    if (!given(states) || !given(slots) || !given(parent) || !given(slots_out) || slots_out == slots || slots_out == parent) return KDA_ERR_INVALID_ARG;
     if (slot_bytes < 16 || slot_bytes % 16 != 0 || slot_bytes > int64_t(1) << 36) return KDA_ERR_INVALID_ARG;
     if (layers > 1 && (layer_stride % 16 != 0 || layer_stride / slot_bytes < num_slots)) return KDA_ERR_INVALID_ARG;
     ReorderArgs a{};

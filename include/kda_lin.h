@@ -48,9 +48,11 @@
  *    Results do not depend on timing: no atomics. They may differ in the last bits
  *    between batches, which decide where long sequences are cut into segments.
  *  - Range: products and states have to stay below 2^120 in magnitude. An
- *    infinity or NaN in a token's q reaches that token's output only; in its k, v
- *    or g the outputs of its head from that token on and the state, never an
- *    earlier token, another head or another sequence.
+ *    infinity or NaN in a token's q reaches that token's output only. In its k, v
+ *    or g it may reach the outputs of its head from that token on and the state,
+ *    and does as long as it has not decayed to 0 (how far it goes then depends on
+ *    where the sequence is cut); never an earlier token, another head or another
+ *    sequence.
  */
 #ifndef KDA_LIN_H_
 #define KDA_LIN_H_

@@ -1,0 +1,171 @@
+"""Linear attention and beam search where they could go wrong and ordinary sizes do not look: batches of one
+long sequence and many short ones, offsets past 31 and 32 bits, candidates that hardly differ, calls that run
+at the same time."""
+
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+from gated_delta_rule_10_amd import beam, lin
+from tests import lin_common as lc
+from tests.test_gpu_beam import BF, check, normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,H", [([20] * 7 + [2600] + [1] * 7 + [0], 32), ([3] * 40 + [0] * 20 + [900, 0, 64, 65] + [7] * 26, 1)])
+def test_one_long_sequence_among_short_ones(dt, lens, H):
+    """Sequences and heads that fill the card, one of them cut; more than 64 sequences."""
+    x = lc.Inputs(H, lens, H, max(1, H // 4), 64, 128, dt, rate=0.02)
+    o, s = lin.kda_lin_chunk_fwd(*x.args(), initial_state=x.s0)
+    x.check(o, s, x.s0, 1.0)
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+def test_order_of_the_sequences_changes_nothing(order):
+    """Whichever sequence is the longest: each has the bits that it has in another order."""
+    lens = [5, 64, 700, 130, 0, 300, 65, 1]
+    x = lc.Inputs(4, lens, 40, 8, 64, 64, "bf16")
+    ref, rs = lin.kda_lin_chunk_fwd(*x.args(), initial_state=x.s0)
+    to = {"rising": np.argsort(lens, kind="stable"), "falling": np.argsort(lens, kind="stable")[::-1], "mixed": [3, 7, 0, 2, 6, 1, 4, 5]}[order]
+    at = np.concatenate([[0], np.cumsum(lens)])
+    rows = torch.from_numpy(np.concatenate([np.arange(at[n], at[n + 1]) for n in to])).cuda()
+    seqs = torch.from_numpy(np.asarray(to).copy()).cuda()
+    o, s = lin.kda_lin_chunk_fwd(x.q[rows], x.k[rows], x.v[rows], x.g[rows], lc.offsets([lens[n] for n in to]),
+                                 initial_state=x.s0[seqs])
+    assert torch.equal(o, ref[rows]) and torch.equal(s, rs[seqs])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_far_apart(dt):
+    """The largest token stride: 2^24 elements, so that the last tokens begin past 2^31 of them; decays too."""
+    lens, H = [130, 20], 2
+    x = lc.Inputs(30, lens, H, 1, 64, 64, dt, rate=0.05)
+    T, stride = x.T, 1 << 24
+    wide = torch.empty(((T - 1) * stride + 512,), dtype=lc.DT[dt], device="cuda")
+    assert (T - 1) * stride > 2 ** 31
+
+    def part(at, heads, d):
+        return wide.as_strided((T, heads, d), (stride, d, 1), at)
+
+    q, k, v = part(0, 1, 64), part(64, 1, 64), part(128, H, 64)
+    q.copy_(x.q), k.copy_(x.k), v.copy_(x.v)
+    g = torch.empty(((T - 1) * stride + 8,), device="cuda").as_strided((T, H), (stride, 1))
+    g.copy_(x.g)
+    ref, rs = lin.kda_lin_chunk_fwd(*x.args(), initial_state=x.s0)
+    o, s = lin.kda_lin_chunk_fwd(q, k, v, g, x.cu, initial_state=x.s0)
+    assert torch.equal(o, ref) and torch.equal(s, rs)
+    cache = torch.zeros((T, H, 64, 64), device="cuda")
+    want = cache.clone()
+    a = lin.kda_lin_decode_step(x.q, x.k, x.v, x.g, want)
+    b = lin.kda_lin_decode_step(q, k, v, g, cache)
+    assert torch.equal(a, b) and torch.equal(cache, want)
+
+
+def test_slots_past_32_bits():
+    """A cache of more than 2^32 bytes and 2^31 elements: prompts, single tokens and reordering in its last slots."""
+    H, d, slots = 32, 128, 4200
+    assert (slots - 8) * H * d * d > 2 ** 31
+    cache = torch.empty((slots, H, d, d), device="cuda")
+    x = lc.Inputs(31, [70, 3], H, 8, d, d, "bf16")
+    where = torch.tensor([slots - 1, slots - 3], dtype=torch.int32, device="cuda")
+    cache[where.long()] = x.s0
+    ref, rs = lin.kda_lin_chunk_fwd(*x.args(), initial_state=x.s0)
+    o, _ = lin.kda_lin_chunk_fwd(*x.args(), initial_state=cache, state_slots=where)
+    assert torch.equal(o, ref) and torch.equal(cache[where.long()], rs)
+    small = rs.clone()
+    a = lin.kda_lin_decode_step(x.q[:2], x.k[:2], x.v[:2], x.g[:2], small)
+    b = lin.kda_lin_decode_step(x.q[:2], x.k[:2], x.v[:2], x.g[:2], cache, where)
+    assert torch.equal(a, b) and torch.equal(cache[where.long()], small)
+    out = beam.kda_state_reorder(cache[None], where[None].contiguous(), torch.zeros((1, 2), dtype=torch.int32, device="cuda"))
+    assert torch.equal(out[0], where) and torch.equal(cache[where.long()], small[:1].expand(2, -1, -1, -1))
+
+
+def test_layers_past_32_bits():
+    """Layers more than 2^32 bytes apart."""
+    layer = (1 << 32) + 64
+    memory = torch.empty((2 * layer + 4096,), dtype=torch.uint8, device="cuda")
+    states = memory.as_strided((3, 4, 64), (layer, 64, 1))
+    states.copy_(torch.randint(0, 256, (3, 4, 64), dtype=torch.uint8, generator=torch.Generator().manual_seed(1)))
+    before = states.clone()
+    out = beam.kda_state_reorder(states, torch.tensor([[0, 1], [3, 2]], dtype=torch.int32, device="cuda"),
+                                 torch.tensor([[1, 1], [0, 0]], dtype=torch.int32, device="cuda"))
+    assert out.tolist() == [[1, 0], [3, 2]]
+    assert torch.equal(states, before[:, [1, 1, 3, 3]])
+
+
+def test_logits_past_32_bits():
+    """Rows 2^31 elements apart, the largest stride."""
+    x = (3 * normal(32, 1, 2, 1001)).to(BF)
+    wide = torch.empty(((1 << 31) + 1001,), dtype=BF, device="cuda").as_strided((1, 2, 1001), (1 << 32, 1 << 31, 1))
+    wide.copy_(x)
+    scores = -3 + normal(33, 1, 2)
+    for a, b in zip(check(x, scores, 9), beam.kda_beam_select(wide, scores, 9)):
+        assert torch.equal(a, b)
+
+
+# Logits that agree in their leading bits, so that a bar does not part them. Values are distinct, their
+# distances 2^-12 and more, so that no e^x decides.
+def close(seed, W, V, many):
+    r = np.random.default_rng(seed)
+    x = r.uniform(-4, 4, (1, W, V)).astype(np.float32)
+    at = 8 + np.arange(W * many) * 2.0 ** -12
+    at = r.permutation(at.astype(np.float32)).reshape(W, many)
+    for w in range(W):
+        x[0, w, r.permutation(V)[:many]] = at[w]
+    return torch.from_numpy(x).cuda()
+
+
+@pytest.mark.parametrize("W,many", [(1, 40), (1, 100), (1, 256), (1, 257), (1, 900), (3, 30), (4, 60), (8, 60), (2, 200), (9, 300)])
+@pytest.mark.parametrize("V", [1001, 40003])
+@pytest.mark.parametrize("K", [1, 10, 64])
+def test_candidates_that_hardly_differ(W, many, V, K):
+    """Lists of fewer and more candidates than the kernels hold unsorted, in one piece of a row and in several."""
+    x = close(W * many + V, W, V, many)
+    scores = torch.zeros((1, W), device="cuda")
+    check(x, scores, K)
+
+
+def test_more_places_than_candidates_and_scores_in_place():
+    x = 2 * normal(34, 5, 3, 7)
+    scores = -2 + normal(35, 5, 3)
+    s, p, t = check(x, scores, 64)                      # 21 candidates
+    assert (p[:, 21:] == -1).all() and (t[:, 21:] == -1).all()
+    ref = check(x, scores, 3)
+    out = (scores, torch.empty_like(ref[1]), torch.empty_like(ref[2]))
+    beam.kda_beam_select(x, scores, 3, out=out)
+    assert all(torch.equal(a, b) for a, b in zip(out, ref))
+
+
+def test_calls_at_the_same_time():
+    """Every operator from four threads at once, each on a stream of its own: the bits of calls one by one."""
+    x = lc.Inputs(36, [1500, 40, 300], 8, 4, 128, 128, "bf16")
+    y = lc.Inputs(37, [1] * 6, 8, 4, 128, 128, "bf16")
+    logits, scores = (2 * normal(38, 3, 4, 30011)).to(BF), -3 + normal(39, 3, 4)
+    slots, parent = (torch.tensor(a, dtype=torch.int32, device="cuda") for a in ([[0, 3, 1], [5, 4, 2]], [[2, 2, 0], [1, 1, 1]]))
+
+    def work():
+        o, s = lin.kda_lin_chunk_fwd(*x.args(), initial_state=x.s0)
+        cache = y.s0.clone()
+        step = lin.kda_lin_decode_step(y.q, y.k, y.v, y.g, cache)
+        out = beam.kda_state_reorder(cache[None], slots, parent)
+        return (o, s, step, cache, out) + beam.kda_beam_select(logits, scores, 8)
+
+    ref = work()
+    torch.cuda.synchronize()
+    got = [None] * 4
+
+    def thread(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(5):
+                got[i] = work()
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    for g in got:
+        assert g is not None and all(torch.equal(a, b) for a, b in zip(g, ref))

@@ -167,3 +167,8 @@ def test_bindings_refuse_host_tensors_and_wrong_layouts(lib):
     for bad in (torch.zeros(2, 4).t(), torch.zeros(4, 3), torch.zeros(3), torch.zeros(4, 2).double(), torch.zeros(4)[::2]):
         with pytest.raises(ValueError):
             lin._decay(bad, 4, 2, cpu)
+
+
+def test_outputs_in_the_place_of_inputs_are_refused(lib):
+    assert _select(lib, os=A) == INVALID               # K is not W: another request's scores
+    assert _reorder(lib, slots=B, parent=A, out=A) == INVALID
