@@ -39,11 +39,10 @@ struct Span {
     }
 };
 
-// The place whose turn it is, in the order of the grid: up to 64 go by their tokens, most first, so that
-// a long one is not left over at the end (16 prompts of 259 to 3509 tokens, the longest last, H = 32: 216 us, and 277 as
-// they come). A place to a lane.
+// The place whose turn it is, in the order of the grid, where there are more workgroups than the card
+// holds: up to 64 places go by their tokens, most first, so that a long one is not left over at the end (16
+// prompts of 259 to 3509 tokens, the longest last, H = 32: 216 us, and 277 as they come). A place to a lane.
 __device__ __forceinline__ int place_of(const LinArgs &a, int R, int turn, int places, int lane) {
-    if (a.N == 1 || places > 64) return turn;
     int start, count, first = 0, of = 0, rank = 0;
     seq_rows(a.cu, min(lane, a.N - 1), a.T, start, count);
     start = start / R + lane;
@@ -159,7 +158,7 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_ends_kernel(LinAr
 
 // All outputs, and the states at the sequences' ends.
 template <typename W, typename TOut, int K, int V>
-__global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(LinArgs a, Segments ws, int R) {
+__global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(LinArgs a, Segments ws, int R, int sorted) {
     using T = typename W::T;
     constexpr int C = W::C;
     __shared__ __align__(16) char tiles[W::kTiles];
@@ -168,7 +167,7 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
     __shared__ int strange[2];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int turn = blockIdx.x / a.H, h = blockIdx.x - turn * a.H, hk = h / (a.H / a.Hk);
-    const int place = place_of(a, R, turn, gridDim.x / a.H, lane);
+    const int place = sorted ? place_of(a, R, turn, sorted, lane) : turn;
     const Span x(a, R, place, lane);
     if (x.seg < 0 || x.seg >= x.segs) return;
     const int t0 = x.t0, tokens = x.tokens, chunks = (tokens + C - 1) / C, slot = slot_of(a, x.n);
@@ -262,15 +261,17 @@ struct Plan {
     bool cut;
 };
 
-// The host knows the number of tokens and sequences, not the lengths. A compute unit holds one workgroup of
-// 8 waves (d_v = 128) or two of 4. Where sequences and heads alone fill the card, only a sequence of more
+// Workgroups that the card holds: a compute unit, one of 8 waves (d_v = 128) or two of 4.
+int64_t room_of(int32_t V) { return compute_units() * (V == 64 ? 2 : 1); }
+
+// The host knows the number of tokens and sequences, not the lengths. Where sequences and heads alone fill the card, only a sequence of more
 // than four times the mean length is cut (16 of 217 to 3448, H = 32: uncut 199 us, at best 252 cut); else
 // segments are as long as lets all of them run at once (1 x 4000, H = 32: 63 chunks uncut 204 us, 8 to a
 // segment 64, 4 in two rounds 79, 16 on half of the card 96). From 128 chunks on, two rounds of half as
 // many end more evenly (1 x 131072: 1421 against 1503 us). Cutting is worth it from a few chunks on: uncut,
 // a chunk takes 3.3 us (fp32 11.8), cut 4.5 (16) with both walks, and 20 for two launches more.
 Plan plan_of(int32_t N, int32_t T, int32_t H, int32_t V, kda_dtype_t in_dtype) {
-    const int64_t room = compute_units() * (V == 64 ? 2 : 1), rows = static_cast<int64_t>(N) * H;
+    const int64_t room = room_of(V), rows = static_cast<int64_t>(N) * H;
     const int64_t mean = (static_cast<int64_t>(T) + 64 * static_cast<int64_t>(N) - 1) / (64 * static_cast<int64_t>(N));  // chunks of 64
     int64_t L = max(static_cast<int64_t>(2), ((static_cast<int64_t>(T) / 64 + N) * H + room - 1) / room);
     if (L >= 128) L = (L + 1) / 2;
@@ -297,7 +298,8 @@ template <typename Ends, typename All, typename TOut, int K, int V> hipError_t l
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((lin_segments_kernel<All, TOut, K, V>), grid, block, 0, st, a, ws, p.R);
+    const bool sorted = a.N > 1 && p.places <= 64 && p.places * a.H > room_of(V);
+    hipLaunchKernelGGL((lin_segments_kernel<All, TOut, K, V>), grid, block, 0, st, a, ws, p.R, sorted ? static_cast<int>(p.places) : 0);
     return hipGetLastError();
 }
 
