@@ -11,6 +11,14 @@
 // fp64, a bar over the lists' candidates, and the order of what passes it. Where a
 // list overflows (many equal logits, rising ones), the workgroup looks at its
 // piece again and keeps the K best in order, one insertion after the other.
+//
+// 16 x 8 rows of 100003 bf16 logits (25.6 MB, K = 16): 12.6 us for the rows (2 TB/s: a row
+// is short, and a wave's exponentials and comparisons take as long as its loads) and 9
+// for the joins, which are a chain of short steps that only N workgroups take; sorted lists
+// in each wave instead of a bar took 42 in all. 4 rows of 32000 fp32: 5.4 and 7.1.
+//
+// Reordering moves bytes: 16 x 8 beams that all go on from few, 8 layers of 2 MB states,
+// 1.6 GB read and written: 300 us, 5.4 TB/s.
 #include <cfloat>
 
 #include "kda_attn_internal.h"
@@ -441,7 +449,7 @@ __global__ __launch_bounds__(kThreads) void select_join_kernel(SelectArgs a, int
     write(lane, best.list);
 }
 
-// Workgroups per row: enough to fill the card, of at least 2048 tokens.
+// Workgroups per row: up to 4 to a compute unit in all, of at least 2048 tokens.
 int splits_of(int32_t N, int32_t W, int32_t V) {
     const int64_t rows = static_cast<int64_t>(N) * W;
     const int64_t want = (4 * compute_units() + rows - 1) / rows, most = (static_cast<int64_t>(V) + 2047) / 2048;

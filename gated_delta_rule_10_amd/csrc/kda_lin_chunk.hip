@@ -8,6 +8,14 @@
 // outputs, and one joins these, a segment's state being the one before it times
 // e^(its sum of g), plus its own. They read k and v a second time, and are worth
 // it where a few sequences would leave the card empty.
+//
+// What bounds it (H = 32, 128 channels, bf16): long prompts the memory. 131072
+// tokens are 4.37 GB, 930 us at the rate of a large copy (4.7 TB/s); with k and v
+// read twice, 1390 us; it takes 1389 to 1430, 430 to 450 for the ends (4.9 TB/s)
+// and 950 to 1125 for the outputs. The same in pieces of 8192 to 65536 tokens, whose
+// k and v the Infinity Cache could hold for the second walk, is slower (6 to 47 %): the
+// launches drain the card between them. Few prompts are bound by the walk: one
+// workgroup alone takes 3.3 us a chunk of 64 tokens.
 #include "kda_attn_internal.h"
 #include "kda_lin_bf16.h"
 #include "kda_lin_device.h"
@@ -18,10 +26,13 @@ namespace {
 
 constexpr double kLog2e = 1.4426950408889634;
 
-// A segmented call's workspace: the states at the segments' starts (as the registers of a workgroup
-// hold them, see fragment()), and the sums of log2 e^g over them.
+// A segmented call's workspace, as the registers of a workgroup hold states: those at the starts of
+// segments from a sequence's second on, the initial states of sequences that are cut (the final ones may
+// take their place in memory), and the sums of log2 e^g over segments. Segment g of a sequence from token
+// t on has piece t / R + g, the same for no other but one's first and another's last; only sequences of
+// more than R tokens are cut, so that two of them do not begin in one piece.
 struct Segments {
-    float *state;
+    float *state, *first;
     double *sum;
 };
 
@@ -99,7 +110,7 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_ends_kernel(LinAr
     const Span x(a, R, place, lane);
     if (x.seg < 0 || x.seg >= x.segs - 1) return;
     const int chunks = R / C;  // all whole
-    const int64_t piece = static_cast<int64_t>(place) * a.H + h;
+    const int64_t piece = static_cast<int64_t>(place - x.n) * a.H + h;
     const T *kp = static_cast<const T *>(a.k) + (x.t0 + R - C) * a.ks + hk * K, *vp = static_cast<const T *>(a.v) + (x.t0 + R - C) * a.vs + h * V;
     W s;
     s.clear();
@@ -137,7 +148,6 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_ends_kernel(LinAr
         if (i + 1 < chunks) s.to_lds(lds[b ^ 1], tid);
         if (i + 2 < chunks) load();
     }
-    float *out = ws.state + piece * (K * V);
     if (x.seg == 0) {
         // the last wave has the sum
         __shared__ float whole;
@@ -149,11 +159,12 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_ends_kernel(LinAr
         W first;
         first.clear();
         if (a.s0 && slot >= 0) first.take(s0, w, lane);
-        first.put(out, w, lane);
+        first.put(ws.first + piece * (K * V), w, lane);
         s.add(first, e);
+    } else if (tid == W::NT - 1) {
+        ws.sum[piece] = sum;
     }
-    s.put(out + static_cast<int64_t>(a.H) * (K * V), w, lane);  // the next segment's
-    if (tid == W::NT - 1) ws.sum[piece] = sum;
+    s.put(ws.state + (piece + a.H) * (K * V), w, lane);  // the next segment's
 }
 
 // All outputs, and the states at the sequences' ends.
@@ -177,7 +188,7 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
     s.clear();
     W::prepare(scores, tid);
     if (x.segs > 1)
-        s.get(ws.state + (static_cast<int64_t>(place) * a.H + h) * (K * V), w, lane);
+        s.get((x.seg ? ws.state : ws.first) + (static_cast<int64_t>(place - x.n) * a.H + h) * (K * V), w, lane);
     else if (a.s0 && slot >= 0)
         s.take(a.s0 + held, w, lane);
 
@@ -233,23 +244,25 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
 
 // The states at the starts of each sequence's segments from the third on: that of the one before,
 // decayed over it, added to what it wrote itself. Four elements of the state to a thread.
-template <int KV> __global__ __launch_bounds__(256) void lin_join_kernel(LinArgs a, Segments ws, int R) {
+template <int KV> __global__ __launch_bounds__(256) void lin_join_kernel(LinArgs a, Segments ws, int R, int seqs) {
     constexpr int PER = KV / 4 / 256;
-    const int e = (blockIdx.x % PER) * 256 + threadIdx.x, nh = blockIdx.x / PER, n = nh / a.H, h = nh - n * a.H;
-    int start, count;
-    seq_rows(a.cu, n, a.T, start, count);
-    const int segs = (count + R - 1) / R;
-    const int64_t piece = (static_cast<int64_t>(start / R) + n) * a.H + h;
-    if (segs < 3) return;
-    f32x4 *p = reinterpret_cast<f32x4 *>(ws.state + piece * KV) + e;
+    const int e = (blockIdx.x % PER) * 256 + threadIdx.x, nh = blockIdx.x / PER, h = nh % a.H;
     const int64_t step = static_cast<int64_t>(a.H) * (KV / 4);
-    f32x4 x = p[step];
-    for (int g = 2; g < segs; ++g) {
-        const float d = __builtin_amdgcn_exp2f(static_cast<float>(ws.sum[piece + static_cast<int64_t>(g - 1) * a.H]));
-        const f32x4 own = p[g * step];
+    for (int n = nh / a.H; n < a.N; n += seqs) {
+        int start, count;
+        seq_rows(a.cu, n, a.T, start, count);
+        const int segs = (count + R - 1) / R;
+        if (segs < 3) continue;
+        const int64_t piece = static_cast<int64_t>(start / R) * a.H + h;
+        f32x4 *p = reinterpret_cast<f32x4 *>(ws.state + piece * KV) + e;
+        f32x4 x = p[step];
+        for (int g = 2; g < segs; ++g) {
+            const float d = __builtin_amdgcn_exp2f(static_cast<float>(ws.sum[piece + static_cast<int64_t>(g - 1) * a.H]));
+            const f32x4 own = p[g * step];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = fmaf(d, x[i], own[i]);
-        p[g * step] = x;
+            for (int i = 0; i < 4; ++i) x[i] = fmaf(d, x[i], own[i]);
+            p[g * step] = x;
+        }
     }
 }
 
@@ -264,12 +277,13 @@ struct Plan {
 // Workgroups that the card holds: a compute unit, one of 8 waves (d_v = 128) or two of 4.
 int64_t room_of(int32_t V) { return compute_units() * (V == 64 ? 2 : 1); }
 
-// The host knows the number of tokens and sequences, not the lengths. Where sequences and heads alone fill the card, only a sequence of more
-// than four times the mean length is cut (16 of 217 to 3448, H = 32: uncut 199 us, at best 252 cut); else
-// segments are as long as lets all of them run at once (1 x 4000, H = 32: 63 chunks uncut 204 us, 8 to a
-// segment 64, 4 in two rounds 79, 16 on half of the card 96). From 128 chunks on, two rounds of half as
-// many end more evenly (1 x 131072: 1421 against 1503 us). Cutting is worth it from a few chunks on: uncut,
-// a chunk takes 3.3 us (fp32 11.8), cut 4.5 (16) with both walks, and 20 for two launches more.
+// The host knows the number of tokens and sequences, not the lengths. Where sequences and heads alone fill
+// the card, only a sequence of more than four times the mean length is cut (16 of 217 to 3448, H = 32: 209
+// us, and 267 where those of twice the mean are cut); else segments are as long as lets all of them run at
+// once (1 x 4000, H = 32: 63 chunks uncut 204 us, 8 to a segment 64, 4 in two rounds 79, 16 on half of the
+// card 96). From 128 chunks on, two rounds of half as many end more evenly (1 x 131072: 1421 against 1503
+// us). Cutting is worth it from a few chunks on: uncut, a chunk takes 3.3 us (fp32 11.8), cut 4.5 (16) with
+// both walks, and 20 for two launches more.
 Plan plan_of(int32_t N, int32_t T, int32_t H, int32_t V, kda_dtype_t in_dtype) {
     const int64_t room = room_of(V), rows = static_cast<int64_t>(N) * H;
     const int64_t mean = (static_cast<int64_t>(T) + 64 * static_cast<int64_t>(N) - 1) / (64 * static_cast<int64_t>(N));  // chunks of 64
@@ -282,19 +296,24 @@ Plan plan_of(int32_t N, int32_t T, int32_t H, int32_t V, kda_dtype_t in_dtype) {
     return {static_cast<int>(64 * L), T / (64 * L) + N, true};
 }
 
-size_t sums_bytes(const Plan &p, int32_t H) { return (static_cast<size_t>(p.places) * H * sizeof(double) + 255) / 256 * 256; }
+size_t pieces_of(const Plan &p, int32_t T, int32_t H) { return static_cast<size_t>(T / p.R + 1) * H; }
+size_t sums_bytes(size_t pieces) { return (pieces * sizeof(double) + 255) / 256 * 256; }
 
 template <typename Ends, typename All, typename TOut, int K, int V> hipError_t launch(const LinArgs &a, hipStream_t st) {
     const Plan p = plan_of(a.N, a.T, a.H, V, a.in_dtype);
     Segments ws{};
     const dim3 grid(static_cast<unsigned>(p.places * a.H)), block(All::NT);
     if (p.cut) {
+        const size_t pieces = pieces_of(p, a.T, a.H);
         ws.sum = static_cast<double *>(a.ws);
-        ws.state = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sums_bytes(p, a.H));
+        ws.state = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sums_bytes(pieces));
+        ws.first = ws.state + pieces * (K * V);
         hipLaunchKernelGGL((lin_ends_kernel<Ends, K, V>), grid, block, 0, st, a, ws, p.R);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((lin_join_kernel<K * V>), dim3(a.N * a.H * (K * V / 1024)), dim3(256), 0, st, a, ws, p.R);
+        // (a launch holds less than 2^32 threads; of more than 5 H < 2^22 rows, if the card is full)
+        const int seqs = min(min(a.N, 64), max(1, (1 << 18) / a.H));
+        hipLaunchKernelGGL((lin_join_kernel<K * V>), dim3(seqs * a.H * (K * V / 1024)), dim3(256), 0, st, a, ws, p.R, seqs);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -318,7 +337,9 @@ hipError_t launch_lin_chunk(const LinArgs &a, hipStream_t st) {
 
 size_t lin_chunk_workspace(int32_t N, int32_t T, int32_t H, int32_t K, int32_t V, kda_dtype_t in_dtype) {
     const Plan p = plan_of(N, T, H, V, in_dtype);
-    return p.cut ? sums_bytes(p, H) + static_cast<size_t>(p.places) * H * K * V * sizeof(float) : 0;
+    if (!p.cut) return 0;
+    const size_t pieces = pieces_of(p, T, H);
+    return sums_bytes(pieces) + 2 * pieces * K * V * sizeof(float);
 }
 
 }  // namespace kda

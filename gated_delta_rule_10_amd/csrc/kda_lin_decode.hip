@@ -5,7 +5,9 @@
 // columns of a (sequence, head), as in kda_decode.hip: a wave's load covers rows
 // of V / 2 columns, 16 bytes a lane. Unlike the delta rule, a row's update needs
 // nothing but the row, so each piece is written back as soon as it has arrived,
-// and only the output waits for the sum over the rows.
+// and only the output waits for the sum over the rows. 64 sequences of 32 heads of
+// 128 x 128 are 272 MB: 50 us, 5.4 TB/s, as against 46 at the rate at which a large tensor
+// is scaled in place (5.9). One sequence takes 4 us on the card, and 12 with the call.
 #include "kda_lin_device.h"
 
 namespace kda {

@@ -4,7 +4,13 @@
 // 32 tokens to a chunk. A wave holds 16 value channels: S[m] register r of lane l
 // is value channel l % 16 and key channel 64 (m / 4) + 16 (l / 16) + 4 r + m % 4, so
 // that one read of 4 neighbouring key channels serves 4 products, both where k is
-// multiplied into the state and where the state is read.
+// multiplied into the state and where the state is read. (A piece of 4 key channels is
+// 16 bytes as 8 are in bf16: 32 tokens fill the LDS that 64 fill there.)
+//
+// Bound by the matrix instructions, at an eighth of the bf16 rate: a chunk of 32 tokens
+// takes 5.9 us of one workgroup. Sequences of 4000, 37 and 411 tokens, H = 16, 128
+// channels: 110 us (36 for the ends, 76 for the outputs); 8.2 GFLOP, 53 us at the rate of
+// a large fp32 product (154 TFLOP/s).
 #pragma once
 
 #include "kda_attn_device.h"
