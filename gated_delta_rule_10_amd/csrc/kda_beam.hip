@@ -18,7 +18,7 @@
 // in each wave instead of a bar took 42 in all. 4 rows of 32000 fp32: 5.4 and 7.1.
 //
 // Reordering moves bytes: 16 x 8 beams that all go on from few, 8 layers of 2 MB states,
-// 1.6 GB read and written: 300 us, 5.4 TB/s.
+// 1.6 GB read and written: 290 us, 5.55 TB/s.
 #include <cfloat>
 
 #include "kda_attn_internal.h"
@@ -449,10 +449,12 @@ __global__ __launch_bounds__(kThreads) void select_join_kernel(SelectArgs a, int
     write(lane, best.list);
 }
 
-// Workgroups per row: up to 4 to a compute unit in all, of at least 2048 tokens.
+// Workgroups per row: up to 4 to a compute unit in all, of at least 4096 tokens (us: 16 x 8 rows of 100003
+// bf16 at 2, 4 and 8 workgroups 29, 21, 24; 1 x 4 rows of 128000 at 2048, 4096 and 8192 tokens 22, 17, 18: the
+// joins have fewer lists).
 int splits_of(int32_t N, int32_t W, int32_t V) {
     const int64_t rows = static_cast<int64_t>(N) * W;
-    const int64_t want = (4 * compute_units() + rows - 1) / rows, most = (static_cast<int64_t>(V) + 2047) / 2048;
+    const int64_t want = (4 * compute_units() + rows - 1) / rows, most = (static_cast<int64_t>(V) + 4095) / 4096;
     return static_cast<int>(min(static_cast<int64_t>(64), max(static_cast<int64_t>(1), min(want, most))));
 }
 
@@ -542,9 +544,10 @@ hipError_t launch_beam_select(const SelectArgs &a, hipStream_t st) {
 }
 
 hipError_t launch_state_reorder(const ReorderArgs &a, hipStream_t st) {
-    // pieces of 16 KB, fewer and longer ones where the card is full anyway
+    // A piece of 16 KB to a workgroup, up to 64 workgroups to a compute unit (16 of them, with several pieces
+    // each: 302 us instead of 290 for the case above; 128: 290; pieces of 32 KB: 298).
     const int64_t pieces = (a.slot_bytes / 16 + kPiece - 1) / kPiece, groups = static_cast<int64_t>(a.N) * a.layers;
-    const int64_t x = max(static_cast<int64_t>(1), min(pieces, (16 * compute_units() + groups - 1) / groups));
+    const int64_t x = max(static_cast<int64_t>(1), min(pieces, (64 * compute_units() + groups - 1) / groups));
     hipLaunchKernelGGL(reorder_kernel, dim3(static_cast<unsigned>(x * groups)), dim3(kThreads), 0, st, a, static_cast<int>(x));
     return hipGetLastError();
 }
