@@ -1,13 +1,15 @@
 // Linear attention with one decay per head, one token per sequence
 // (kda_lin_decode_step): S = e^g S + k v^T in place, o = scale S^T q.
 //
-// Bound by the state, read and written once. A workgroup takes half of the
-// columns of a (sequence, head), as in kda_decode.hip: a wave's load covers rows
-// of V / 2 columns, 16 bytes a lane. Unlike the delta rule, a row's update needs
+// Bound by the state, read and written once. A workgroup of 16 waves takes a
+// (sequence, head): a wave's load covers rows of V columns, 16 bytes a lane, and
+// 4 loads of a lane the state. Unlike the delta rule, a row's update needs
 // nothing but the row, so each piece is written back as soon as it has arrived,
 // and only the output waits for the sum over the rows. 64 sequences of 32 heads of
-// 128 x 128 are 272 MB: 50 us, 5.4 TB/s, as against 46 at the rate at which a large tensor
-// is scaled in place (5.9). One sequence takes 4 us on the card, and 12 with the call.
+// 128 x 128 are 272 MB: 48.6 us, 5.6 TB/s, as against 46 at the rate at which a large tensor
+// is scaled in place (5.9). (8 waves: 49.3, or 50.9 for half of the columns each; 4 waves
+// 50.4; 200 sequences 148, 154, 156 and 155.) One sequence takes 4.5 us on the card (halves: 4.1), and
+// 12 with the call.
 #include "kda_lin_device.h"
 
 namespace kda {
@@ -15,19 +17,19 @@ namespace {
 
 typedef float f4 __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 8, kSplit = 2;
+constexpr int kWaves = 16;
 
 // Nontemporal: a state is touched once per step, and the caches of a model's layers exceed the
 // Infinity Cache (measured for the same access in kda_decode.hip).
 template <int K, int V, typename TIn, typename TOut>
 __global__ __launch_bounds__(64 * kWaves) void lin_decode_kernel(LinArgs a) {
-    constexpr int NC = V / kSplit, LPR = NC / 4, RPI = 64 / LPR, ITERS = K / (kWaves * RPI);
+    constexpr int LPR = V / 4, RPI = 64 / LPR, ITERS = K / (kWaves * RPI);
     static_assert(ITERS * kWaves * RPI == K && K <= 64 * kWaves, "rows are covered by the waves' loads");
     __shared__ float2 kq[K];
     __shared__ f4 red[kWaves][LPR];
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int c4 = lane % LPR, rsub = lane / LPR;
-    const int bh = blockIdx.x / kSplit, col0 = NC * (blockIdx.x % kSplit) + 4 * c4;
+    const int bh = blockIdx.x, col0 = 4 * c4;
     const int b = bh / a.H, h = bh - b * a.H, hk = h / (a.H / a.Hk);
     float ki = 0.f, qi = 0.f;
     if (tid < K) {
@@ -77,7 +79,7 @@ __global__ __launch_bounds__(64 * kWaves) void lin_decode_kernel(LinArgs a) {
 }
 
 template <int K, int V> hipError_t launch_dims(const LinArgs &a, hipStream_t st) {
-    const dim3 grid(a.N * a.H * kSplit), block(64 * kWaves);
+    const dim3 grid(a.N * a.H), block(64 * kWaves);
     if (a.in_dtype == KDA_F32)
         hipLaunchKernelGGL((lin_decode_kernel<K, V, float, float>), grid, block, 0, st, a);
     else if (a.out_dtype == KDA_BF16)
