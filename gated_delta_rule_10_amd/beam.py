@@ -66,8 +66,10 @@ def kda_beam_select(logits: torch.Tensor, scores: torch.Tensor, K: int, *, done:
     with _on(device):
         s = _handle(stream, device)
         with _alloc_on(stream):
-            kinds = (torch.float32, torch.int32, torch.int32)
-            best, parent, token = (_out(t, (N, K), dt, device) for t, dt in zip(out or (None,) * 3, kinds))
+            best, parent, token = out or (None, None, None)
+            best = _out(best, (N, K), torch.float32, device)
+            parent = _out(parent, (N, K), torch.int32, device)
+            token = _out(token, (N, K), torch.int32, device)
             if workspace is None:
                 need = lib.kda_beam_select_workspace_size(N, W, V, K)
                 if need:
@@ -97,22 +99,25 @@ def kda_state_reorder(states: torch.Tensor, slots: torch.Tensor, parent: torch.T
     if states.dim() < 3:
         raise ValueError("states must be [layers, num_slots, ...]")
     layers, num_slots = states.shape[:2]
-    if layers < 1 or not states[0].is_contiguous():
-        raise ValueError("states: every layer's part must be contiguous")
+    row = 1  # elements: of a slot's row in the end
+    for i, (n, stride) in enumerate(zip(states.shape[:0:-1], states.stride()[:0:-1])):
+        if n > 1 and stride != row:
+            raise ValueError("states: every layer's part must be contiguous")
+        if i < states.dim() - 2:
+            row *= n
+    size = states.element_size()
     device = states.device
     for name, t in (("slots", slots), ("parent", parent)):
         if t.dtype != torch.int32 or t.dim() != 2 or t.shape != slots.shape:
             raise ValueError(f"{name} must be int32 [N, W]")
     N, W = slots.shape
-    size = states.element_size()
-    slot_bytes = states[0, 0].numel() * size if num_slots else 0
     with _on(device):
         s = _handle(stream, device)
         with _alloc_on(stream):
             slots_out = _out(slots_out, (N, W), torch.int32, device)
         _dense(device, slots=slots, parent=parent, slots_out=slots_out)
-        st = lib.kda_state_reorder(states.data_ptr(), states.stride(0) * size, layers, num_slots, slot_bytes,
-                                   slots.data_ptr(), parent.data_ptr(), slots_out.data_ptr(), N, W, s)
+        st = lib.kda_state_reorder(states.data_ptr(), states.stride(0) * size, layers, num_slots, row * size, slots.data_ptr(),
+                                   parent.data_ptr(), slots_out.data_ptr(), N, W, s)
     if st != KDA_OK:
         raise KDAError(st, "kda_state_reorder")
     return slots_out

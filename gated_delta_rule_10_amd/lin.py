@@ -36,9 +36,11 @@ def load_library() -> ctypes.CDLL:
     return lib
 
 
-def _tokens(t: torch.Tensor, name: str) -> int:
-    """Token stride of a [T, heads, d] GPU tensor; any strides will do where there is no token."""
-    return _rows(t.new_empty((0,) + t.shape[1:]) if t.dim() == 3 and t.shape[0] == 0 else t, name)
+def _tokens(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor) -> Tuple[int, int, int]:
+    """Token strides of [T, heads, d] GPU tensors; any strides will do where there is no token."""
+    if v.dim() == 3 and v.shape[0] == 0:
+        q, k, v = (t.new_empty((0,) + t.shape[1:]) if t.dim() == 3 and t.shape[0] == 0 else t for t in (q, k, v))
+    return _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
 
 
 def _decay(g: torch.Tensor, T: int, H: int, device) -> int:
@@ -61,7 +63,8 @@ def _decay(g: torch.Tensor, T: int, H: int, device) -> int:
 
 
 def _heads(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor) -> None:
-    if k.shape != q.shape or v.shape[0] != q.shape[0] or k.dtype != q.dtype or v.dtype != q.dtype:
+    dtype, shape = q.dtype, q.shape
+    if k.shape != shape or v.shape[0] != shape[0] or k.dtype != dtype or v.dtype != dtype:
         raise ValueError("inconsistent q/k/v shapes or dtypes")
 
 
@@ -84,7 +87,7 @@ def kda_lin_chunk_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_dec
     final_state defaults to that same cache (updated in place). Returns (o [T, H, d_v], final_state).
     """
     lib = load_library()
-    sq, sk, sv = _tokens(q, "q"), _tokens(k, "k"), _tokens(v, "v")
+    sq, sk, sv = _tokens(q, k, v)
     N = _offsets(cu_seqlens)
     _heads(q, k, v)
     T, Hk, d_k = q.shape
@@ -140,7 +143,7 @@ def kda_lin_decode_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_d
     slot_idx: int32 [B] or None. Returns o [B, H, d_v].
     """
     lib = load_library()
-    sq, sk, sv = _tokens(q, "q"), _tokens(k, "k"), _tokens(v, "v")
+    sq, sk, sv = _tokens(q, k, v)
     _heads(q, k, v)
     B, Hk, d_k = q.shape
     H, d_v = v.shape[1], v.shape[2]
