@@ -81,11 +81,21 @@ template <int K, int V, int PARTS> struct LinBf16 {
     // in LDS: q, k and v of a chunk; P
     static constexpr int kQ = 0, kK = OUT ? C * K * 2 : 0, kV = kK + C * K * 2;
     static constexpr int kTiles = kV + C * V * 2, kScores = PARTS * C * C * 2;
+    static constexpr int kOutBytes = PARTS == 1 ? 2 : 4, kOuts = C * V * kOutBytes;  // the outputs of a chunk
 
-    // Piece c of token t lies at piece c ^ swz(t) of its row: 16 rows read at one piece, and 4 rows
-    // read at 4 pieces (the transposing reads), fall on different banks.
-    static __device__ __forceinline__ int swz16(int t) { return ((t & 3) << 2) | ((t >> 2) & 3); }
-    static __device__ __forceinline__ int swz8(int t) { return (((t >> 1) & 1) << 2) | ((t >> 2) & 3); }
+    // Piece c of token t lies at piece c ^ swz(t) of its row, so that what is read at once falls on different
+    // banks. A read of 16 bytes a lane is served in groups of 16 lanes, 0 to 3, 12 to 15 and 20 to 27 the
+    // first and the other 16 of 32 the second (so the bank conflicts counted for such patterns say): half of
+    // 16 rows at one piece, the other half at the next one. A transposing read is served in groups of 32: of 8
+    // rows apart by 1 or 8, either 2 pieces each or 4 half ones, for which k's rows with bit 3 of t set have the
+    // halves of their pieces changed over. (With order 0, 1, 2, 3 instead of 0, 2, 3, 1 in the low bits, and
+    // halves in place, 40 % of LDS cycles are conflicts: 8 x 2000 tokens 142 us instead of 140.)
+    static __device__ __forceinline__ int low(int t) { return (((t >> 1) ^ (t >> 2)) & 2) | ((t >> 3) & 1); }
+    static __device__ __forceinline__ int swz16(int t) { return ((t & 3) << 2) | low(t); }
+    static __device__ __forceinline__ int swz8(int t) { return ((t & 2) << 1) | low(t); }
+    static __device__ __forceinline__ u32x4 halves(const u32x4 &x, bool changed) {
+        return changed ? u32x4{x[2], x[3], x[0], x[1]} : x;
+    }
     template <int CH> static __device__ __forceinline__ int at(int t, int c) {
         return t * (CH * 16) + 16 * (c ^ (CH == 16 ? swz16(t) : swz8(t)));
     }
@@ -135,7 +145,11 @@ template <int K, int V, int PARTS> struct LinBf16 {
     // whether some of this thread's values is an infinity or NaN
     __device__ __forceinline__ bool to_lds(char *lds, int tid) {
         if (OUT) store_rows<CK>(q, lds + kQ, tid);
-        store_rows<CK>(k, lds + kK, tid);
+#pragma unroll
+        for (int i = 0; i < LK; ++i) {
+            const int t = (i * NT + tid) / CK;
+            *reinterpret_cast<u32x4 *>(lds + kK + at<CK>(t, tid % CK)) = halves(k[i], t & 8);
+        }
         store_rows<CV>(v, lds + kV, tid);
         if (!OUT) return false;
         uint32_t odd = 0;
@@ -156,7 +170,7 @@ template <int K, int V, int PARTS> struct LinBf16 {
     }
     static __device__ __forceinline__ bf16x8 keys(const char *lds, int y, int m, int lane) {  // rows of S[m]
         const int i = lane & 15;
-        return transposed<CK>(lds + kK, 32 * y + 8 * (lane >> 4) + (i >> 2), 4 * (m >> 1) + (i & 3), 8 * (m & 1));
+        return transposed<CK>(lds + kK, 32 * y + 8 * (lane >> 4) + (i >> 2), 4 * (m >> 1) + (i & 3), 8 * ((m ^ (lane >> 4)) & 1));
     }
     static __device__ __forceinline__ bf16x8 values(const char *lds, int y, int w, int lane) {  // channels 16 w + ..
         const int i = lane & 15;
@@ -172,7 +186,10 @@ template <int K, int V, int PARTS> struct LinBf16 {
         const int l = lane & 15, g = lane >> 4, i = i0 + l, j = j0 + 4 * g;  // p[r]: row i, column j + r
         f32x4 p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int x = 0; x < K / 32; ++x) p = mma16(row<CK>(lds + kK, j0 + l, 4 * x + g), row<CK>(lds + kQ, i, 4 * x + g), p);
+        for (int x = 0; x < K / 32; ++x) {
+            const u32x4 kx = halves(__builtin_bit_cast(u32x4, row<CK>(lds + kK, j0 + l, 4 * x + g)), l & 8);
+            p = mma16(__builtin_bit_cast(bf16x8, kx), row<CK>(lds + kQ, i, 4 * x + g), p);
+        }
         const float hi = d.hi[i], lo = d.lo[i];
         const f32x4 dh = *reinterpret_cast<const f32x4 *>(d.hi + j), dl = *reinterpret_cast<const f32x4 *>(d.lo + j);
 #pragma unroll
@@ -277,27 +294,28 @@ template <int K, int V, int PARTS> struct LinBf16 {
             }
     }
 
-    // rows of o through the wave's own columns of v's tile, whose values are in registers by now
-    __device__ __forceinline__ void store(bf16_t *out, int64_t stride, char *lds, int count, int w, int lane) const {
+    // the wave's columns of the outputs into their tile
+    __device__ __forceinline__ void stage(char *outs, int w, int lane) const {
         const int l = lane & 15, g = lane >> 4;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const bf16x2 x = pack_bf16(o[b][0], o[b][1]), y = pack_bf16(o[b][2], o[b][3]);
-            *reinterpret_cast<bf16x4 *>(lds + kV + at<CV>(16 * b + l, 2 * w + (g >> 1)) + 8 * (g & 1)) = (bf16x4){x[0], x[1], y[0], y[1]};
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int t = 32 * i + (lane >> 1), c = 2 * w + (lane & 1);
-            const u32x4 x = *reinterpret_cast<const u32x4 *>(lds + kV + at<CV>(t, c));
-            if (t < count) *reinterpret_cast<u32x4 *>(out + t * stride + 8 * c) = x;
+            if (PARTS == 1) {
+                const bf16x2 x = pack_bf16(o[b][0], o[b][1]), y = pack_bf16(o[b][2], o[b][3]);
+                *reinterpret_cast<bf16x4 *>(outs + at<CV>(16 * b + l, 2 * w + (g >> 1)) + 8 * (g & 1)) = (bf16x4){x[0], x[1], y[0], y[1]};
+            } else {
+                *reinterpret_cast<f32x4 *>(outs + wide_at(16 * b + l, 4 * w + g)) = o[b];
+            }
         }
     }
-    __device__ __forceinline__ void store(float *out, int64_t stride, char *, int count, int w, int lane) const {
+    static __device__ __forceinline__ int wide_at(int t, int c) { return t * (V * 4) + 16 * (c ^ (t & 15)); }
+    // whole rows of that tile, `count` of them, to memory
+    static __device__ __forceinline__ void store(char *out, int64_t stride, const char *outs, int count, int tid) {
+        constexpr int P = V * kOutBytes / 16;
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const int t = 16 * b + (lane & 15);
-            if (t < count) *reinterpret_cast<f32x4 *>(out + t * stride + 16 * w + 4 * (lane >> 4)) = o[b];
+        for (int i = 0; i < C * P / NT; ++i) {
+            const int t = (i * NT + tid) / P, c = tid % P;
+            const u32x4 x = *reinterpret_cast<const u32x4 *>(outs + (PARTS == 1 ? at<CV>(t, c) : wide_at(t, c)));
+            if (t < count) __builtin_nontemporal_store(x, reinterpret_cast<u32x4 *>(out + t * stride + 16 * c));
         }
     }
 

@@ -174,6 +174,7 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
     constexpr int C = W::C;
     __shared__ __align__(16) char tiles[W::kTiles];
     __shared__ __align__(16) char scores[W::kScores];
+    __shared__ __align__(16) char outs[W::kOuts];
     __shared__ __align__(16) float table[2][4][C];
     __shared__ int strange[2];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -194,7 +195,8 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
 
     const T *qp = static_cast<const T *>(a.q) + t0 * a.qs + hk * K, *kp = static_cast<const T *>(a.k) + t0 * a.ks + hk * K;
     const T *vp = static_cast<const T *>(a.v) + t0 * a.vs + h * V;
-    TOut *op = static_cast<TOut *>(a.o) + (static_cast<int64_t>(t0) * a.H + h) * V;
+    const int64_t os = static_cast<int64_t>(a.H) * V * sizeof(TOut);
+    char *op = static_cast<char *>(a.o) + t0 * os + static_cast<int64_t>(h) * V * sizeof(TOut);
     const bool summing = w == W::NW - 1;  // the last wave sums the decays, a chunk ahead
     auto decay = [&](int c) { return lane < min(C, tokens - c * C) ? log_decay_of(a, t0 + c * C + lane, h) : 0.f; };
     auto tabulate = [&](float g, int b, int rows) {
@@ -212,6 +214,10 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
     auto load = [&](int c) {
         s.load(qp, kp, vp, a, min(C, tokens - c * C), tid);
         qp += C * a.qs, kp += C * a.ks, vp += C * a.vs;
+    };
+    auto store = [&](int c) {
+        W::store(op, os, outs, min(C, tokens - c * C), tid);
+        op += C * os;
     };
     float g = 0.f;
     if (chunks > 0) load(0);
@@ -231,14 +237,18 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
             if (c + 2 < chunks) g = decay(c + 2);
         }
         W::scores(scores, tiles, d, a.scale, w, lane);
+        // Whole rows, a chunk late, past the caches: 8 x 2000 tokens 142 us, through them 143.5; the waves' own
+        // columns, 32 bytes of a row, 145 (past the caches 154). After the next chunk's loads: 151.
+        if (c > 0) store(c - 1);
         if (c + 1 < chunks) load(c + 1);
         s.from_state(tiles, d, a.scale, lane);
         __syncthreads();
         s.from_chunk(scores, tiles, __builtin_amdgcn_readfirstlane(strange[b]) != 0, w, lane);
-        s.store(op, static_cast<int64_t>(a.H) * V, tiles, min(C, tokens - c * C), w, lane);
+        s.stage(outs, w, lane);
         s.advance(tiles, d, w, lane);
-        op += static_cast<int64_t>(C) * a.H * V;
     }
+    __syncthreads();
+    if (chunks > 0) store(chunks - 1);
     if (x.seg == x.segs - 1 && a.sT && slot >= 0) s.give(a.sT + held, w, lane);
 }
 

@@ -29,7 +29,7 @@ template <int K, int V, bool OUT_> struct LinF32 {
     static constexpr int CK = K / 4, CV = V / 4;              // 16-byte pieces of a row
     static constexpr int LK = C * CK / NT, LV = C * CV / NT;  // of a thread
     static constexpr int kQ = 0, kK = OUT ? C * K * 4 : 0, kV = kK + C * K * 4;  // in LDS
-    static constexpr int kTiles = kV + C * V * 4, kScores = OUT ? C * C * 4 : 0;
+    static constexpr int kTiles = kV + C * V * 4, kScores = OUT ? C * C * 4 : 0, kOuts = C * V * 4;
 
     // piece c of row t: 16 rows read at one piece, and one piece of 4 rows in a row's order, fall on different banks
     template <int CH> static __device__ __forceinline__ int at(int t, int c) { return t * (CH * 16) + 16 * (c ^ (CH == 8 ? (t >> 1) & 7 : t & 15)); }
@@ -157,11 +157,18 @@ template <int K, int V, bool OUT_> struct LinF32 {
             }
     }
 
-    __device__ __forceinline__ void store(float *out, int64_t stride, char *, int count, int w, int lane) const {
+    // the wave's columns of the outputs into their tile
+    __device__ __forceinline__ void stage(char *outs, int w, int lane) const {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int t = 16 * b + (lane & 15);
-            if (t < count) *reinterpret_cast<f32x4 *>(out + t * stride + 16 * w + 4 * (lane >> 4)) = o[b];
+        for (int b = 0; b < 2; ++b) *reinterpret_cast<f32x4 *>(outs + at<CV>(16 * b + (lane & 15), 4 * w + (lane >> 4))) = o[b];
+    }
+    // whole rows of that tile, `count` of them, to memory
+    static __device__ __forceinline__ void store(char *out, int64_t stride, const char *outs, int count, int tid) {
+#pragma unroll
+        for (int i = 0; i < LV; ++i) {
+            const int t = i * (NT / CV) + tid / CV, c = tid % CV;
+            const f32x4 x = row<CV>(outs, t, c);
+            if (t < count) *reinterpret_cast<f32x4 *>(out + t * stride + 16 * c) = x;
         }
     }
 
