@@ -89,7 +89,7 @@ template <int K, int V, int PARTS> struct LinBf16 {
     // 16 rows at one piece, the other half at the next one. A transposing read is served in groups of 32: of 8
     // rows apart by 1 or 8, either 2 pieces each or 4 half ones, for which k's rows with bit 3 of t set have the
     // halves of their pieces changed over. (With order 0, 1, 2, 3 instead of 0, 2, 3, 1 in the low bits, and
-    // halves in place, 40 % of LDS cycles are conflicts: 8 x 2000 tokens 142 us instead of 140.)
+    // halves in place, 40 % of LDS cycles are conflicts: 8 x 2000 tokens 2 us more of 140.)
     static __device__ __forceinline__ int low(int t) { return (((t >> 1) ^ (t >> 2)) & 2) | ((t >> 3) & 1); }
     static __device__ __forceinline__ int swz16(int t) { return ((t & 3) << 2) | low(t); }
     static __device__ __forceinline__ int swz8(int t) { return ((t & 2) << 1) | low(t); }

@@ -115,10 +115,10 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_ends_kernel(LinAr
     W s;
     s.clear();
     double sum = 0.0;  // from the chunk's end to the segment's
-    auto decay = [&](int i) { return lane < C ? log_decay_of(a, x.t0 + R - (i + 1) * C + lane, h) : 0.f; };
+    auto decay = [&](int i) { return lane < C ? a.g[(x.t0 + R - (i + 1) * C + lane) * a.gs + h] : 0.f; };
     auto tabulate = [&](float g, int b) {
         double all;
-        const double y = sums(g, all);
+        const double y = sums(log_decay(g), all);  // (g was on its way until here)
         if (lane < C) left[b][lane] = __builtin_amdgcn_exp2f(static_cast<float>(sum + (all - y)));
         if (lane == 0) over[b] = sum < kNothing;
         sum += all;
@@ -198,10 +198,10 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
     const int64_t os = static_cast<int64_t>(a.H) * V * sizeof(TOut);
     char *op = static_cast<char *>(a.o) + t0 * os + static_cast<int64_t>(h) * V * sizeof(TOut);
     const bool summing = w == W::NW - 1;  // the last wave sums the decays, a chunk ahead
-    auto decay = [&](int c) { return lane < min(C, tokens - c * C) ? log_decay_of(a, t0 + c * C + lane, h) : 0.f; };
+    auto decay = [&](int c) { return lane < min(C, tokens - c * C) ? a.g[(t0 + c * C + lane) * a.gs + h] : 0.f; };
     auto tabulate = [&](float g, int b, int rows) {
         double all;
-        const double y = sums(g, all);
+        const double y = sums(log_decay(g), all);  // (g was on its way until here)
         if (lane < C) {
             const float hi = static_cast<float>(y);
             table[b][0][lane] = hi;
@@ -236,10 +236,11 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
             tabulate(g, b ^ 1, tokens - (c + 1) * C);
             if (c + 2 < chunks) g = decay(c + 2);
         }
-        W::scores(scores, tiles, d, a.scale, w, lane);
-        // Whole rows, a chunk late, past the caches: 8 x 2000 tokens 142 us, through them 143.5; the waves' own
-        // columns, 32 bytes of a row, 145 (past the caches 154). After the next chunk's loads: 151.
+        // Whole rows, a chunk late, past the caches, before the next chunk's loads. (8 x 2000 tokens, 135 us:
+        // behind the scores 1.5 more, behind the loads 12, through the caches 1.5; the waves' own columns, 32
+        // bytes of a row, 5, and those past the caches 14.)
         if (c > 0) store(c - 1);
+        W::scores(scores, tiles, d, a.scale, w, lane);
         if (c + 1 < chunks) load(c + 1);
         s.from_state(tiles, d, a.scale, lane);
         __syncthreads();

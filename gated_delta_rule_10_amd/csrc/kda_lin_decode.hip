@@ -37,7 +37,7 @@ __global__ __launch_bounds__(64 * kWaves) void lin_decode_kernel(LinArgs a) {
         qi = io<TIn>::load(static_cast<const TIn *>(a.q) + b * a.qs + hk * K + tid);
     }
     const float4 v = io<TIn>::load4(static_cast<const TIn *>(a.v) + b * a.vs + h * V + col0);
-    const float g = log_decay_of(a, b, h);
+    const float g = log_decay(a.g[b * a.gs + h]);
     const int slot = slot_of(a, b);
     float *S = a.sT + (static_cast<int64_t>(slot) * a.H + h) * (K * V) + col0;
     f4 s[ITERS];

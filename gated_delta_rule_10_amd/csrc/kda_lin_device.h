@@ -11,10 +11,7 @@ namespace kda {
 // Log decays below this count as this where they are summed: e^-110 is 0 in fp32, and sums of
 // them stay finite, so that differences of sums across a -infinity are not NaN. (A NaN stays one.)
 constexpr float kLowestDecay = -110.f;
-__device__ __forceinline__ float log_decay_of(const LinArgs &a, int64_t t, int h) {
-    const float g = a.g[t * a.gs + h];
-    return g < kLowestDecay ? kLowestDecay : g;
-}
+__device__ __forceinline__ float log_decay(float g) { return g < kLowestDecay ? kLowestDecay : g; }
 
 // Slot of sequence n's state, -1 if it holds nothing.
 __device__ __forceinline__ int slot_of(const LinArgs &a, int n) {

@@ -168,7 +168,7 @@ template <int K, int V, bool OUT_> struct LinF32 {
         for (int i = 0; i < LV; ++i) {
             const int t = i * (NT / CV) + tid / CV, c = tid % CV;
             const f32x4 x = row<CV>(outs, t, c);
-            if (t < count) *reinterpret_cast<f32x4 *>(out + t * stride + 16 * c) = x;
+            if (t < count) __builtin_nontemporal_store(x, reinterpret_cast<f32x4 *>(out + t * stride + 16 * c));
         }
     }
 
