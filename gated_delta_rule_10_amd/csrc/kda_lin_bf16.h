@@ -21,7 +21,7 @@
 // registers of a lane, and the chunk's tiles are read by 8 waves at once. (Four waves of
 // 32 channels, two workgroups to a compute unit: 1446 us against 1421, and 16 prompts of
 // 217 to 3448 tokens 252 against 199.) A chunk's loads, products, LDS reads and
-// conversions hardly overlap within a wave: a workgroup alone takes 3.3 us a chunk.
+// conversions hardly overlap within a wave: a workgroup alone takes 3 us a chunk.
 #pragma once
 
 #include "kda_attn_device.h"

@@ -11,11 +11,11 @@
 //
 // What bounds it (H = 32, 128 channels, bf16): long prompts the memory. 131072
 // tokens are 4.37 GB, 930 us at the rate of a large copy (4.7 TB/s); with k and v
-// read twice, 1390 us; it takes 1389 to 1430, 430 to 450 for the ends (4.9 TB/s)
-// and 950 to 1125 for the outputs. The same in pieces of 8192 to 65536 tokens, whose
+// read twice, 1390 us; it takes 1370 to 1445 by the card's state, 440 for the ends
+// (4.9 TB/s) and 930 to 1040 for the outputs. The same in pieces of 8192 to 65536 tokens, whose
 // k and v the Infinity Cache could hold for the second walk, is slower (6 to 47 %): the
 // launches drain the card between them. Few prompts are bound by the walk: one
-// workgroup alone takes 3.3 us a chunk of 64 tokens.
+// workgroup alone takes 3 us a chunk of 64 tokens.
 #include "kda_attn_internal.h"
 #include "kda_lin_bf16.h"
 #include "kda_lin_device.h"
@@ -36,23 +36,32 @@ struct Segments {
     double *sum;
 };
 
-// What a workgroup works on: segment `seg` of `segs` of sequence n, `tokens` of them from t0 on.
+// What a workgroup works on: segment `seg` of `segs` of sequence n, `tokens` of them from t0 on. Segments
+// are found by their piece, if they are not their sequence's last (then no other such segment has it, and no
+// later sequence begins in it or before), or by their place, which is piece + n.
 struct Span {
     int n, seg, segs, t0, tokens;
-    __device__ __forceinline__ Span(const LinArgs &a, int R, int place, int lane) {
-        n = seq_of_slot(a.cu, a.N, a.T, 1, R, place, lane);
+    __device__ __forceinline__ void set(const LinArgs &a, int R, int piece) {
         int start, count;
         seq_rows(a.cu, n, a.T, start, count);
-        seg = place - (start / R + n);
+        seg = piece - start / R;
         segs = max(1, (count + R - 1) / R);
         t0 = start + seg * R;
         tokens = min(R, count - seg * R);
+    }
+    __device__ __forceinline__ void at_place(const LinArgs &a, int R, int place, int lane) {
+        n = seq_of_slot(a.cu, a.N, a.T, 1, R, place, lane);
+        set(a, R, place - n);
+    }
+    __device__ __forceinline__ void at_piece(const LinArgs &a, int R, int piece, int lane) {
+        n = wave_last_upto(a.N, piece, lane, [&](int i) { return static_cast<int64_t>(clampi(a.cu[i], 0, a.T)) / R; });
+        set(a, R, piece);
     }
 };
 
 // The place whose turn it is, in the order of the grid, where there are more workgroups than the card
 // holds: up to 64 places go by their tokens, most first, so that a long one is not left over at the end (16
-// prompts of 259 to 3509 tokens, the longest last, H = 32: 216 us, and 277 as they come). A place to a lane.
+// prompts of 259 to 3509 tokens, the longest last, H = 32: 216 us, and 277 as they come, before later steps). A place to a lane.
 __device__ __forceinline__ int place_of(const LinArgs &a, int R, int turn, int places, int lane) {
     int start, count, first = 0, of = 0, rank = 0;
     seq_rows(a.cu, min(lane, a.N - 1), a.T, start, count);
@@ -106,11 +115,12 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_ends_kernel(LinAr
     __shared__ __align__(16) float left[2][C];
     __shared__ int over[2];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int place = blockIdx.x / a.H, h = blockIdx.x - place * a.H, hk = h / (a.H / a.Hk);
-    const Span x(a, R, place, lane);
+    const int64_t piece = blockIdx.x;
+    const int g0 = blockIdx.x / a.H, h = blockIdx.x - g0 * a.H, hk = h / (a.H / a.Hk);
+    Span x;
+    x.at_piece(a, R, g0, lane);
     if (x.seg < 0 || x.seg >= x.segs - 1) return;
     const int chunks = R / C;  // all whole
-    const int64_t piece = static_cast<int64_t>(place - x.n) * a.H + h;
     const T *kp = static_cast<const T *>(a.k) + (x.t0 + R - C) * a.ks + hk * K, *vp = static_cast<const T *>(a.v) + (x.t0 + R - C) * a.vs + h * V;
     W s;
     s.clear();
@@ -180,7 +190,8 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int turn = blockIdx.x / a.H, h = blockIdx.x - turn * a.H, hk = h / (a.H / a.Hk);
     const int place = sorted ? place_of(a, R, turn, sorted, lane) : turn;
-    const Span x(a, R, place, lane);
+    Span x;
+    x.at_place(a, R, place, lane);
     if (x.seg < 0 || x.seg >= x.segs) return;
     const int t0 = x.t0, tokens = x.tokens, chunks = (tokens + C - 1) / C, slot = slot_of(a, x.n);
     const int64_t held = (static_cast<int64_t>(slot) * a.H + h) * (K * V);
@@ -255,25 +266,31 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
 
 // The states at the starts of each sequence's segments from the third on: that of the one before,
 // decayed over it, added to what it wrote itself. Four elements of the state to a thread.
-template <int KV> __global__ __launch_bounds__(256) void lin_join_kernel(LinArgs a, Segments ws, int R, int seqs) {
+template <int KV> __global__ __launch_bounds__(256) void lin_join_kernel(LinArgs a, Segments ws, int R) {
     constexpr int PER = KV / 4 / 256;
-    const int e = (blockIdx.x % PER) * 256 + threadIdx.x, nh = blockIdx.x / PER, h = nh % a.H;
+    const int e = (blockIdx.x % PER) * 256 + threadIdx.x, lane = threadIdx.x & 63;
+    const int at = blockIdx.x / PER, h = at % a.H;
+    // the sequence: of those that have three segments, number at / H
+    int start, count, before = at / a.H, n = -1;
+    for (int first = 0; first < a.N && n < 0; first += 64) {
+        seq_rows(a.cu, min(first + lane, a.N - 1), a.T, start, count);
+        uint64_t m = __ballot(first + lane < a.N && count - R > R);
+        for (; m && before > 0; --before) m &= m - 1;
+        if (m) n = first + __ffsll(static_cast<unsigned long long>(m)) - 1;
+    }
+    if (n < 0) return;
+    seq_rows(a.cu, n, a.T, start, count);
+    const int segs = (count + R - 1) / R;
+    const int64_t piece = static_cast<int64_t>(start / R) * a.H + h;
+    f32x4 *p = reinterpret_cast<f32x4 *>(ws.state + piece * KV) + e;
     const int64_t step = static_cast<int64_t>(a.H) * (KV / 4);
-    for (int n = nh / a.H; n < a.N; n += seqs) {
-        int start, count;
-        seq_rows(a.cu, n, a.T, start, count);
-        const int segs = (count + R - 1) / R;
-        if (segs < 3) continue;
-        const int64_t piece = static_cast<int64_t>(start / R) * a.H + h;
-        f32x4 *p = reinterpret_cast<f32x4 *>(ws.state + piece * KV) + e;
-        f32x4 x = p[step];
-        for (int g = 2; g < segs; ++g) {
-            const float d = __builtin_amdgcn_exp2f(static_cast<float>(ws.sum[piece + static_cast<int64_t>(g - 1) * a.H]));
-            const f32x4 own = p[g * step];
+    f32x4 x = p[step];
+    for (int g = 2; g < segs; ++g) {
+        const float d = __builtin_amdgcn_exp2f(static_cast<float>(ws.sum[piece + static_cast<int64_t>(g - 1) * a.H]));
+        const f32x4 own = p[g * step];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = fmaf(d, x[i], own[i]);
-            p[g * step] = x;
-        }
+        for (int i = 0; i < 4; ++i) x[i] = fmaf(d, x[i], own[i]);
+        p[g * step] = x;
     }
 }
 
@@ -289,12 +306,12 @@ struct Plan {
 int64_t room_of(int32_t V) { return compute_units() * (V == 64 ? 2 : 1); }
 
 // The host knows the number of tokens and sequences, not the lengths. Where sequences and heads alone fill
-// the card, only a sequence of more than four times the mean length is cut (16 of 217 to 3448, H = 32: 209
-// us, and 267 where those of twice the mean are cut); else segments are as long as lets all of them run at
-// once (1 x 4000, H = 32: 63 chunks uncut 204 us, 8 to a segment 64, 4 in two rounds 79, 16 on half of the
-// card 96). From 128 chunks on, two rounds of half as many end more evenly (1 x 131072: 1421 against 1503
-// us). Cutting is worth it from a few chunks on: uncut, a chunk takes 3.3 us (fp32 11.8), cut 4.5 (16) with
-// both walks, and 20 for two launches more.
+// the card, only a sequence of more than four times the mean length is cut (16 of 217 to 3448, H = 32: 194
+// us, 190 without the two launches that find nothing to do, and 256 where those of twice the mean are cut);
+// else segments are as long as lets all of them run at once (1 x 4000, H = 32: 63 chunks uncut 192 us, 8 to
+// a segment 60, 4 in two rounds 72, 16 on half of the card 90). From 128 chunks on, two rounds of half as
+// many end more evenly (1 x 131072: 1407 against 1495 us). Cutting is worth it from a few chunks on: uncut, a
+// chunk takes 3 us (fp32 11.8), cut about 4.5 (16) with both walks, and 20 for two launches more.
 Plan plan_of(int32_t N, int32_t T, int32_t H, int32_t V, kda_dtype_t in_dtype) {
     const int64_t room = room_of(V), rows = static_cast<int64_t>(N) * H;
     const int64_t mean = (static_cast<int64_t>(T) + 64 * static_cast<int64_t>(N) - 1) / (64 * static_cast<int64_t>(N));  // chunks of 64
@@ -313,23 +330,26 @@ size_t sums_bytes(size_t pieces) { return (pieces * sizeof(double) + 255) / 256 
 template <typename Ends, typename All, typename TOut, int K, int V> hipError_t launch(const LinArgs &a, hipStream_t st) {
     const Plan p = plan_of(a.N, a.T, a.H, V, a.in_dtype);
     Segments ws{};
-    const dim3 grid(static_cast<unsigned>(p.places * a.H)), block(All::NT);
+    const dim3 block(All::NT);
     if (p.cut) {
         const size_t pieces = pieces_of(p, a.T, a.H);
         ws.sum = static_cast<double *>(a.ws);
         ws.state = reinterpret_cast<float *>(static_cast<char *>(a.ws) + sums_bytes(pieces));
         ws.first = ws.state + pieces * (K * V);
-        hipLaunchKernelGGL((lin_ends_kernel<Ends, K, V>), grid, block, 0, st, a, ws, p.R);
+        // at most T / R segments are not their sequence's last, and at most T / 2R sequences have three
+        const int ends = a.T / p.R, seqs = min(a.N, a.T / p.R / 2);
+        hipLaunchKernelGGL((lin_ends_kernel<Ends, K, V>), dim3(ends * a.H), block, 0, st, a, ws, p.R);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        // (a launch holds less than 2^32 threads; of more than 5 H < 2^22 rows, if the card is full)
-        const int seqs = min(min(a.N, 64), max(1, (1 << 18) / a.H));
-        hipLaunchKernelGGL((lin_join_kernel<K * V>), dim3(seqs * a.H * (K * V / 1024)), dim3(256), 0, st, a, ws, p.R, seqs);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        if (seqs > 0) {
+            hipLaunchKernelGGL((lin_join_kernel<K * V>), dim3(seqs * a.H * (K * V / 1024)), dim3(256), 0, st, a, ws, p.R);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
     }
     const bool sorted = a.N > 1 && p.places <= 64 && p.places * a.H > room_of(V);
-    hipLaunchKernelGGL((lin_segments_kernel<All, TOut, K, V>), grid, block, 0, st, a, ws, p.R, sorted ? static_cast<int>(p.places) : 0);
+    hipLaunchKernelGGL((lin_segments_kernel<All, TOut, K, V>), dim3(static_cast<unsigned>(p.places * a.H)), block, 0, st, a, ws, p.R,
+                       sorted ? static_cast<int>(p.places) : 0);
     return hipGetLastError();
 }
 
