@@ -9,13 +9,14 @@
 // e^(its sum of g), plus its own. They read k and v a second time, and are worth
 // it where a few sequences would leave the card empty.
 //
-// What bounds it (H = 32, 128 channels, bf16): long prompts the memory. 131072
-// tokens are 4.37 GB, 930 us at the rate of a large copy (4.7 TB/s); with k and v
-// read twice, 1390 us; it takes 1370 to 1445 by the card's state, 440 for the ends
-// (4.9 TB/s) and 930 to 1040 for the outputs. The same in pieces of 8192 to 65536 tokens, whose
-// k and v the Infinity Cache could hold for the second walk, is slower (6 to 47 %): the
-// launches drain the card between them. Few prompts are bound by the walk: one
-// workgroup alone takes 3 us a chunk of 64 tokens.
+// What bounds it (H = 32, 128 channels, bf16): 131072 tokens are 4.37 GB, 930 us at the
+// rate of a large copy (4.7 TB/s), and take 1370 to 1445 by the card's state: 930 to
+// 1040 for the outputs (4.5 GB, 4.3 to 4.8 TB/s: memory), 440 for the ends, which are bound
+// by the walk of the heads that forget slowly (128 chunks at 3.4 us, two workgroups to
+// a compute unit; the others stop early, so that 1.3 GB are read). The same in pieces of
+// 8192 to 65536 tokens, whose k and v the Infinity Cache could hold for the second
+// walk, is slower (6 to 47 %): the launches drain the card between them. Few prompts
+// are bound by the walk: one workgroup alone takes 3 us a chunk of 64 tokens.
 #include "kda_attn_internal.h"
 #include "kda_lin_bf16.h"
 #include "kda_lin_device.h"
