@@ -169,3 +169,29 @@ def test_calls_at_the_same_time():
     [t.join() for t in threads]
     for g in got:
         assert g is not None and all(torch.equal(a, b) for a, b in zip(g, ref))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_several_long_sequences_among_many(dt):
+    """Cut sequences before, between and behind more than 64 short and empty ones."""
+    lens = [2] * 3 + [500] + [0] * 66 + [700] + [1] * 69 + [450, 0, 258, 5]
+    x = lc.Inputs(40, lens, 1, 1, 64, 64, dt, rate=0.01)
+    o, s = lin.kda_lin_chunk_fwd(*x.args(), initial_state=x.s0)
+    x.check(o, s, x.s0, 1.0)
+
+
+def test_single_tokens_in_a_graph():
+    """A captured step, replayed: the state goes on from replay to replay as from call to call."""
+    x = lc.Inputs(41, [1] * 5, 4, 2, 128, 128, "bf16")
+    cache, eager = x.s0.clone(), x.s0.clone()
+    o = torch.empty_like(x.v)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lin.kda_lin_decode_step(x.q, x.k, x.v, x.g, cache, o=o)
+    cache.copy_(x.s0)
+    for _ in range(4):
+        x.v.mul_(0.5)
+        g.replay()
+        want = lin.kda_lin_decode_step(x.q, x.k, x.v, x.g, eager)
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(cache, eager)
