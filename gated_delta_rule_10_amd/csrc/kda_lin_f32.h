@@ -9,7 +9,7 @@
 //
 // Bound by the matrix instructions, at an eighth of the bf16 rate: a chunk of 32 tokens
 // takes 5.9 us of one workgroup. Sequences of 4000, 37 and 411 tokens, H = 16, 128
-// channels: 110 us (36 for the ends, 76 for the outputs); 8.2 GFLOP, 53 us at the rate of
+// channels: 110 us (35 for the ends, 73 for the outputs); 8.2 GFLOP, 53 us at the rate of
 // a large fp32 product (154 TFLOP/s).
 #pragma once
 
