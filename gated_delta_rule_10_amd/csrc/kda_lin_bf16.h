@@ -14,8 +14,9 @@
 // shared in LDS. q, k and v are exact bf16 operands. V e^(..) is three bf16 parts
 // (24 bits, all of fp32): its rounding would stay in the state (two parts: states
 // off by 2.6e-6 of their size instead of 4e-7, and 150 us of 1450 less for 131072 tokens,
-// H = 32). S and P only go into the outputs: one part for bf16 outputs, which round
-// them as much again (two: 140 us more), two for fp32 ones.
+// H = 32). S and P only go into the outputs and are two parts (16 bits), also for bf16 outputs:
+// one part would be rounded as much as those are, and they would be off by 0.0024 of their
+// size instead of 0.0017.
 //
 // 16 value channels to a wave and 8 waves to a workgroup, one to a compute unit: S is 32
 // registers of a lane, and the chunk's tiles are read by 8 waves at once. (Four waves of
@@ -70,10 +71,11 @@ __device__ __forceinline__ int opaque(int lane) {
     return lane;
 }
 
-// PARTS: of S and P; 0 where there are no outputs
-template <int K, int V, int PARTS> struct LinBf16 {
+// TOut: of the outputs; void where there are none
+template <int K, int V, typename TOut> struct LinBf16 {
     using T = bf16_t;
-    static constexpr bool OUT = PARTS > 0;
+    static constexpr bool OUT = !__is_void(TOut), kHalf = __is_same(TOut, bf16_t);
+    static constexpr int PARTS = OUT ? 2 : 0;  // of S and P
     static constexpr int C = 64, NW = V / 16, NT = 64 * NW, M = K / 16;
     static constexpr int kWavesPerSimd = OUT ? 2 : 4;
     static constexpr int CK = K / 8, CV = V / 8;              // 16-byte pieces of a row
@@ -81,7 +83,7 @@ template <int K, int V, int PARTS> struct LinBf16 {
     // in LDS: q, k and v of a chunk; P
     static constexpr int kQ = 0, kK = OUT ? C * K * 2 : 0, kV = kK + C * K * 2;
     static constexpr int kTiles = kV + C * V * 2, kScores = PARTS * C * C * 2;
-    static constexpr int kOutBytes = PARTS == 1 ? 2 : 4, kOuts = C * V * kOutBytes;  // the outputs of a chunk
+    static constexpr int kOutBytes = kHalf ? 2 : 4, kOuts = C * V * kOutBytes;  // the outputs of a chunk
 
     // Piece c of token t lies at piece c ^ swz(t) of its row, so that what is read at once falls on different
     // banks. A read of 16 bytes a lane is served in groups of 16 lanes, 0 to 3, 12 to 15 and 20 to 27 the
@@ -299,7 +301,7 @@ template <int K, int V, int PARTS> struct LinBf16 {
         const int l = lane & 15, g = lane >> 4;
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            if (PARTS == 1) {
+            if (kHalf) {
                 const bf16x2 x = pack_bf16(o[b][0], o[b][1]), y = pack_bf16(o[b][2], o[b][3]);
                 *reinterpret_cast<bf16x4 *>(outs + at<CV>(16 * b + l, 2 * w + (g >> 1)) + 8 * (g & 1)) = (bf16x4){x[0], x[1], y[0], y[1]};
             } else {
@@ -314,7 +316,7 @@ template <int K, int V, int PARTS> struct LinBf16 {
 #pragma unroll
         for (int i = 0; i < C * P / NT; ++i) {
             const int t = (i * NT + tid) / P, c = tid % P;
-            const u32x4 x = *reinterpret_cast<const u32x4 *>(outs + (PARTS == 1 ? at<CV>(t, c) : wide_at(t, c)));
+            const u32x4 x = *reinterpret_cast<const u32x4 *>(outs + (kHalf ? at<CV>(t, c) : wide_at(t, c)));
             if (t < count) __builtin_nontemporal_store(x, reinterpret_cast<u32x4 *>(out + t * stride + 16 * c));
         }
     }

@@ -356,8 +356,8 @@ template <typename Ends, typename All, typename TOut, int K, int V> hipError_t l
 
 template <int K, int V> hipError_t launch_dims(const LinArgs &a, hipStream_t st) {
     if (a.in_dtype == KDA_F32) return launch<LinF32<K, V, false>, LinF32<K, V, true>, float, K, V>(a, st);
-    if (a.out_dtype == KDA_BF16) return launch<LinBf16<K, V, 0>, LinBf16<K, V, 1>, bf16_t, K, V>(a, st);
-    return launch<LinBf16<K, V, 0>, LinBf16<K, V, 2>, float, K, V>(a, st);
+    if (a.out_dtype == KDA_BF16) return launch<LinBf16<K, V, void>, LinBf16<K, V, bf16_t>, bf16_t, K, V>(a, st);
+    return launch<LinBf16<K, V, void>, LinBf16<K, V, float>, float, K, V>(a, st);
 }
 
 }  // namespace

@@ -43,8 +43,8 @@
  *    inputs are multiplied in fp32. With bf16 inputs q, k and v are exact, the
  *    decayed values go into the state with 24 bits, so that states are right to
  *    fp32, and the decayed scores and the state that q reads are rounded for the
- *    outputs: to one bf16 number (by at most 2^-8 of each term) for bf16 outputs,
- *    to the sum of two (2^-16) for fp32 ones. Single tokens are fp32 throughout.
+ *    outputs to the sum of two bf16 numbers (by at most 2^-16 of each term),
+ *    whatever the outputs' type. Single tokens are fp32 throughout.
  *    Results do not depend on timing: no atomics. They may differ in the last bits
  *    between batches, which decide where long sequences are cut into segments.
  *  - Range: products and states have to stay below 2^120 in magnitude. An
