@@ -316,14 +316,18 @@ __global__ __launch_bounds__(kThreads) void select_pieces_kernel(SelectArgs a, i
 
 // A request's choice, four waves. A wave holds 16 lists of 64 at a time, each turned by 4 lanes more than
 // the one before: their candidates are at their starts. What is below the bar for sure is sorted out in
-// fp32, by sums that are off by less than the bar is lowered; what passes is computed in fp64.
+// fp32, by sums that are off by less than the bar is lowered; what passes is computed in fp64. A row's
+// maximum and the logarithm of its sum of e^(x - maximum) stay apart: in the sum of a large maximum (all
+// tokens at a mask of the type's lowest value) and a logarithm, the logarithm is lost.
 constexpr int kLists = 16;
 
 __global__ __launch_bounds__(kThreads) void select_join_kernel(SelectArgs a, int S) {
-    __shared__ double lse[64], score[64], lv[kWaves][64];
+    __shared__ double log_sum[64], score[64], lv[kWaves][64];
     __shared__ uint32_t li[kWaves][64];
-    __shared__ float tops[kWaves][64], offset[64 * 64];
+    __shared__ float tops[kWaves][64];
+    __shared__ float2 offset[64 * 64];  // of a list: its row's maximum, and score - logarithm
     __shared__ List<double, 256> some;
+    __shared__ float top_of[64];
     __shared__ uint8_t ended[64];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6), n = blockIdx.x;
     const Pieces p = pieces_of(a.ws, static_cast<int64_t>(a.N) * a.W, S);
@@ -351,16 +355,18 @@ __global__ __launch_bounds__(kThreads) void select_join_kernel(SelectArgs a, int
         if (row && !over && i < S) sum = {p.top[(row0 + r) * S + i], p.sum[(row0 + r) * S + i]};
         sum.join_lanes(group);
         if (row) {
-            const double l = static_cast<double>(sum.m) + log(sum.s), c = static_cast<double>(a.scores[row0 + r]);
-            for (int j = i; j < S; j += group) offset[r * S + j] = over ? NAN : static_cast<float>(c - l);
+            const double l = log(sum.s), c = static_cast<double>(a.scores[row0 + r]);
+            for (int j = i; j < S; j += group) offset[r * S + j] = make_float2(sum.m, over ? NAN : static_cast<float>(c - l));
             if (i == 0) {
-                lse[r] = l;
+                top_of[r] = sum.m;
+                log_sum[r] = l;
                 score[r] = c;
                 ended[r] = over;
             }
         }
     }
     __syncthreads();
+    auto candidate = [&](float x, int r) { return (static_cast<double>(x) - static_cast<double>(top_of[r])) - log_sum[r] + score[r]; };
     const Key<double> done = tid < a.W && ended[tid] ? Key<double>{score[tid], static_cast<uint32_t>(tid) * a.V + a.done_token} : no_key<double>();
     // all lanes' own maxima give a bar that K candidates reach
     float top = static_cast<float>(done.v), far = 0.f;
@@ -369,9 +375,10 @@ __global__ __launch_bounds__(kThreads) void select_join_kernel(SelectArgs a, int
 #pragma unroll
         for (int j = 0; j < kLists; ++j)
             if (list + j * kWaves < lists) {
-                const float x = v[j] + offset[list + j * kWaves];
+                const float2 o = offset[list + j * kWaves];
+                const float below = v[j] - o.x, x = below + o.y;
                 top = fmaxf(top, x);
-                if (x > -INFINITY) far = fmaxf(far, fabsf(v[j]));
+                if (x > -INFINITY) far = fmaxf(far, fabsf(below));
             }
     }
     tops[w][lane] = top;
@@ -385,8 +392,8 @@ __global__ __launch_bounds__(kThreads) void select_join_kernel(SelectArgs a, int
         all[i] = tops[i][lane];
         far = fmaxf(far, static_cast<float>(lv[i][0]));
     }
-    // v + offset rounds the offset and the sum, by 2^-24 of |offset| <= |v| + |x| and of |x|, in the K and in
-    // the one compared with them
+    // x rounds v - maximum (`below`), the offset and their sum, by 2^-24 of |below|, of |offset| <= |below| + |x|
+    // and of |x|, in the K and in the one compared with them
     float bar = reached_by(all, a.K);
     if (bar > -INFINITY) bar -= 1e-6f * (fabsf(bar) + far);
     for (int list = w; list < lists; list += kLists * kWaves) {
@@ -394,21 +401,23 @@ __global__ __launch_bounds__(kThreads) void select_join_kernel(SelectArgs a, int
 #pragma unroll
         for (int j = 0; j < kLists; ++j) {
             const int at = list + j * kWaves;
-            const float x = at < lists ? v[j] + offset[at] : -INFINITY;
+            const float2 o = offset[min(at, lists - 1)];
+            const float x = at < lists ? (v[j] - o.x) + o.y : -INFINITY;
             const bool in = x >= bar && x > -INFINITY;
             if (!__any(in)) continue;
             const int r = at / S;
-            some.add({static_cast<double>(v[j]) - lse[r] + score[r], static_cast<uint32_t>(r) * a.V + token[j]}, in, lane);
+            some.add({candidate(v[j], r), static_cast<uint32_t>(r) * a.V + token[j]}, in, lane);
         }
     }
     some.add(done, done.v > -INFINITY && done.v >= static_cast<double>(bar), lane);
     __syncthreads();
     auto write = [&](int rank, const Key<double> &k) {
         if (rank >= a.K) return;
-        const bool found = k.v > -INFINITY;
+        const float c = static_cast<float>(k.v);
+        const bool found = c > -INFINITY;
         const int64_t at = static_cast<int64_t>(n) * a.K + rank;
         const uint32_t r = k.i / static_cast<uint32_t>(a.V);
-        a.out_scores[at] = static_cast<float>(k.v);
+        a.out_scores[at] = c;
         a.out_parent[at] = found ? static_cast<int32_t>(r) : -1;
         a.out_token[at] = found ? static_cast<int32_t>(k.i - r * a.V) : -1;
     };
@@ -433,11 +442,10 @@ __global__ __launch_bounds__(kThreads) void select_join_kernel(SelectArgs a, int
     for (int list = w; list < lists; list += kLists * kWaves) {
 #pragma unroll 1
         for (int j = 0; j < kLists; ++j) {
-            const int at = list + j * kWaves, r = min(at, lists - 1) / S;
-            const int64_t place = (row0 * S + min(at, lists - 1)) * 64 + lane;
-            const float x = p.value[place];
-            best.insert({static_cast<double>(x) - lse[r] + score[r], static_cast<uint32_t>(r) * a.V + p.token[place]},
-                        at < lists && x > -INFINITY && x + offset[min(at, lists - 1)] >= bar);
+            const int at = list + j * kWaves, is = min(at, lists - 1), r = is / S;
+            const int64_t place = (row0 * S + is) * 64 + lane;
+            const float x = p.value[place], c = (x - offset[is].x) + offset[is].y;
+            best.insert({candidate(x, r), static_cast<uint32_t>(r) * a.V + p.token[place]}, at < lists && c >= bar && c > -INFINITY);
         }
     }
     __syncthreads();  // lv is free

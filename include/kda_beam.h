@@ -30,9 +30,11 @@ extern "C" {
  * over beams w and tokens x of a vocabulary of V, in falling order; of equal ones
  * the lowest (w, x) first. A beam with done[n][w] != 0 has ended: its one
  * candidate is (w, done_token) with c = scores[n][w], and its logits are not read.
- * What is -infinity or NaN is no candidate: masked tokens (logits of -infinity),
- * the tokens of a beam whose logits hold a NaN or +infinity, and a beam whose
- * score is -infinity (one that holds nothing, as all but one of the first step's).
+ * What is -infinity (in fp32) or NaN is no candidate: masked tokens (logits of
+ * -infinity; a token at a finite mask, such as the type's lowest value, is a
+ * candidate like any other), the tokens of a beam whose logits hold a NaN or
+ * +infinity, and a beam whose score is -infinity (one that holds nothing, as all
+ * but one of the first step's).
  * Where fewer than K candidates are left, the other places get score -infinity,
  * parent -1 and token -1.
  *
