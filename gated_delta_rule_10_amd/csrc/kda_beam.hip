@@ -145,35 +145,78 @@ template <> struct Batch<bf16_t> {
     }
 };
 
-// A lane's running maximum and sum of e^(x - maximum); the sum is NaN from a NaN or +infinity on.
+// What a sum of e^x is counted in, from its largest x (`top`): e^base 2^R, base 0 but for tops so large that
+// their product with log2 e would lose its integers, R the integer nearest to what is left in powers of 2.
+constexpr float kLog2eRest = 1.925963033500844e-08f;  // log2 e less its fp32 number
+constexpr double kLn2 = 0.6931471805599453;
+struct Unit {
+    float base, top, R;  // top less base
+    explicit __device__ __forceinline__ Unit(float m) {
+        const float x = m == -INFINITY ? 0.f : m;
+        base = fabsf(x) < 0x1p21f ? 0.f : x;
+        top = base == 0.f ? x : 0.f;
+        R = rintf(top * kLog2e);
+    }
+};
+
+// A lane's running maximum and sum of e^x, in units of the maximum; the sum is NaN from a NaN or +infinity on.
+//
+// e^x = 2^n 2^f, n the integer nearest to x log2 e: f is rounded at 1/2, not at x's distance from the maximum,
+// which for equal tokens far below one other would leave the sum off by 6e-7. A term is right to 2^-23 (2^f) and
+// 2^-25 (f), a sum of two of them to 2^-24 more, and the rest is fp64, the change to another unit a power of 2:
+// a sum is right to 2^-22. n is found by rounding to the ones of a float about 1.5 2^23, in whose low bits
+// it stays.
 struct RowSum {
     float m;
     double s;
-    template <int E> __device__ __forceinline__ float add(const float (&x)[E]) {
-        float top = x[0];
-#pragma unroll
-        for (int i = 1; i < E; ++i) top = fmaxf(top, x[i]);
-        const float now = fmaxf(m, top), ref = now == -INFINITY ? 0.f : now;
-        float part = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) part += __builtin_amdgcn_exp2f((x[i] - ref) * kLog2e);
-        s = s * static_cast<double>(__builtin_amdgcn_exp2f((m - ref) * kLog2e)) + static_cast<double>(part);
+    // the sum's factor where its maximum grows to `now`
+    __device__ __forceinline__ void grow(float now) {
+        const Unit from(m), to(now);
+        const float steps = from.R - to.R;
+        if (m == -INFINITY || from.base == to.base)
+            s = ldexp(s, m == -INFINITY ? -4000 : static_cast<int>(steps));
+        else
+            s *= exp((static_cast<double>(from.base) - static_cast<double>(to.base)) + static_cast<double>(steps) * kLn2);
         m = now;
-        return top;
     }
-    __device__ __forceinline__ void join(float om, double os) {
-        const float now = fmaxf(m, om), ref = now == -INFINITY ? 0.f : now;
-        s = s * static_cast<double>(__builtin_amdgcn_exp2f((m - ref) * kLog2e)) +
-            os * static_cast<double>(__builtin_amdgcn_exp2f((om - ref) * kLog2e));
-        m = now;
+    template <int E> __device__ __forceinline__ float add(const float (&x)[E]) {
+        float most = x[0];
+#pragma unroll
+        for (int i = 1; i < E; ++i) most = fmaxf(most, x[i]);
+        grow(fmaxf(m, most));
+        const Unit u(m);
+        const float ones = 12582912.f - u.R, least = u.top - 80.f;  // e^-80 of 2^31 tokens is nothing in fp64
+        double part[2] = {0.0, 0.0};
+        float two = 0.f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const float below = x[i] - u.base, z = below < least ? least : below;  // (NaN stays NaN)
+            const float t = __builtin_fmaf(z, kLog2e, ones), n = t - ones;
+            const float f = __builtin_fmaf(z, kLog2eRest, __builtin_fmaf(z, kLog2e, -n));
+            const float power = __uint_as_float((__float_as_uint(t) << 23) + 0x3F800000u);  // 2^(n - R)
+            two = __builtin_fmaf(__builtin_amdgcn_exp2f(f), power, i % 2 ? two : 0.f);
+            if (i % 2 || i == E - 1) part[i / 2 % 2] += static_cast<double>(two);
+        }
+        s += part[0] + part[1];
+        return most;
+    }
+    __device__ __forceinline__ void join(RowSum other) {
+        const float now = fmaxf(m, other.m);
+        grow(now);
+        other.grow(now);
+        s += other.s;
     }
     // of groups of `lanes` (a power of two) lanes
     __device__ __forceinline__ void join_lanes(int lanes) {
         float now = m;
         for (int d = lanes / 2; d > 0; d >>= 1) now = fmaxf(now, __shfl_xor(now, d));
-        s *= static_cast<double>(__builtin_amdgcn_exp2f((m - (now == -INFINITY ? 0.f : now)) * kLog2e));
-        m = now;
+        grow(now);
         for (int d = lanes / 2; d > 0; d >>= 1) s += __shfl_xor(s, d);
+    }
+    // ln of the sum of e^(x - m)
+    __device__ __forceinline__ double log_sum() const {
+        const Unit u(m);
+        return log(s) + (static_cast<double>(u.R) * kLn2 - static_cast<double>(u.top));
     }
 };
 
@@ -308,7 +351,7 @@ __global__ __launch_bounds__(kThreads) void select_pieces_kernel(SelectArgs a, i
     p.value[at * 64 + lane] = best.list.v;
     p.token[at * 64 + lane] = static_cast<int32_t>(best.list.i);
     if (lane == 0) {
-        for (int i = 1; i < kWaves; ++i) sum.join(lm[i], ls[i]);
+        for (int i = 1; i < kWaves; ++i) sum.join({lm[i], ls[i]});
         p.top[at] = sum.m;
         p.sum[at] = sum.s;
     }
@@ -355,7 +398,7 @@ __global__ __launch_bounds__(kThreads) void select_join_kernel(SelectArgs a, int
         if (row && !over && i < S) sum = {p.top[(row0 + r) * S + i], p.sum[(row0 + r) * S + i]};
         sum.join_lanes(group);
         if (row) {
-            const double l = log(sum.s), c = static_cast<double>(a.scores[row0 + r]);
+            const double l = sum.log_sum(), c = static_cast<double>(a.scores[row0 + r]);
             for (int j = i; j < S; j += group) offset[r * S + j] = make_float2(sum.m, over ? NAN : static_cast<float>(c - l));
             if (i == 0) {
                 top_of[r] = sum.m;

@@ -46,9 +46,10 @@ extern "C" {
  *   out_parent  [N, K]     int32: w
  *   out_token   [N, K]     int32: x
  *
- * Sums and comparisons: e^logit in fp32, sums of them and c in fp64 (a row's
- * logarithm is right to about 1e-7, which decides between candidates of
- * different beams; those of one beam are compared by their logits).
+ * Sums and comparisons: e^logit is right to 2^-23 of itself, sums of them and c
+ * are fp64 (of two terms fp32), so that a row's logarithm is right to 2^-22,
+ * which decides between candidates of different beams; those of one beam are
+ * compared by their logits.
  * Sizes: N >= 1, 1 <= W <= 64, V >= 1, 1 <= K <= 64, W V < 2^31, N W < 2^20,
  * 0 <= done_token < V if done is given.
  * workspace: kda_beam_select_workspace_size bytes of device scratch, whatever
