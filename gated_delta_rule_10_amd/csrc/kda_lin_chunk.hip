@@ -306,22 +306,38 @@ struct Plan {
 // Workgroups that the card holds: a compute unit, one of 8 waves (d_v = 128) or two of 4.
 int64_t room_of(int32_t V) { return compute_units() * (V == 64 ? 2 : 1); }
 
-// The host knows the number of tokens and sequences, not the lengths. Where sequences and heads alone fill
-// the card, only a sequence of more than four times the mean length is cut (16 of 217 to 3448, H = 32: 194
-// us, 190 without the two launches that find nothing to do, and 256 where those of twice the mean are cut);
-// else segments are as long as lets all of them run at once (1 x 4000, H = 32: 63 chunks uncut 192 us, 8 to
-// a segment 60, 4 in two rounds 72, 16 on half of the card 90). From 128 chunks on, two rounds of half as
-// many end more evenly (1 x 131072: 1407 against 1495 us). Cutting is worth it from a few chunks on: uncut, a
-// chunk takes 3 us (fp32 11.8), cut about 4.5 (16) with both walks, and 20 for two launches more.
+// The host knows the number of tokens and sequences, not the lengths.
+//
+// Where sequences and heads alone fill the card, only a sequence of more than four times the mean length is cut
+// (16 of 217 to 3448, H = 32: 214 us, 4 less without the two launches that find nothing to do; cutting those of
+// twice the mean was a third slower).
+//
+// Else segments are as long as lets all of them run at once (1 x 4000, H = 32: 63 chunks uncut 192 us, 8 to a
+// segment 60, 4 in two rounds 72, 16 on half of the card 90). From 128 chunks on, two rounds of half as many end
+// more evenly (H = 32, halved and not: 1 x 131072 1590 and 1616 us, 1 x 80000 982 and 992, 1 x 66000 820 and
+// 821; halved from 64 on, 1 x 60000 753 and 750).
+//
+// Sequences of the mean length are cut where that is faster (H = 32, cut and uncut: 1 x 400 26.5 and 29.7 us, 1 x
+// 300 24 and 23; d = 64, 1 x 500 18.6 and 21.4, 1 x 300 18.6 and 14.6; fp32, 1 x 200 43 and 46). Where it is not,
+// only longer ones are, if one that had all the tokens would gain 100 us or more: one of 40000 among 31 of 30, H = 4:
+// 130 us, uncut 2212; 16 of 214 to 3509, H = 8: 86 and 197; 8 of 30 and 2000, H = 8, below that line, 41 and 118. A
+// batch of equal ones pays 4 us for the launches that find nothing (16 x 512, H = 8: 39.6 and 35.9).
 Plan plan_of(int32_t N, int32_t T, int32_t H, int32_t V, kda_dtype_t in_dtype) {
     const int64_t room = room_of(V), rows = static_cast<int64_t>(N) * H;
     const int64_t mean = (static_cast<int64_t>(T) + 64 * static_cast<int64_t>(N) - 1) / (64 * static_cast<int64_t>(N));  // chunks of 64
     int64_t L = max(static_cast<int64_t>(2), ((static_cast<int64_t>(T) / 64 + N) * H + room - 1) / room);
     if (L >= 128) L = (L + 1) / 2;
-    const int64_t walk = in_dtype == KDA_F32 ? 118 : 33, both = in_dtype == KDA_F32 ? 160 : 45;  // tenths of us
-    const bool full = rows >= room;
-    if (full) L = max(L, 4 * mean);
-    if (64 * L >= T || (!full && 200 + both * L >= walk * mean)) return {(T + 63) / 64 * 64 + 64, N, false};
+    // tenths of us: a chunk's walk, and with both walks of a sequence that is cut; launches
+    const bool f32 = in_dtype == KDA_F32, narrow = V == 64;
+    const int64_t walk = f32 ? (narrow ? 49 : 118) : narrow ? 22 : 35, both = f32 ? (narrow ? 70 : 146) : narrow ? 30 : 55;
+    const int64_t launches = 100, gain = 1000;
+    if (rows >= room) {
+        L = max(L, 4 * mean);
+    } else if (launches + both * L >= walk * mean) {
+        L = max(L, mean);
+        if (launches + both * L + gain > walk * (T / 64)) L = T;
+    }
+    if (64 * L >= T) return {(T + 63) / 64 * 64 + 64, N, false};
     return {static_cast<int>(64 * L), T / (64 * L) + N, true};
 }
 
