@@ -46,7 +46,7 @@ struct Span {
         int start, count;
         seq_rows(a.cu, n, a.T, start, count);
         seg = piece - start / R;
-        segs = max(1, (count + R - 1) / R);
+        segs = (count - 1) / R + 1;  // one of no tokens, too
         t0 = start + seg * R;
         tokens = min(R, count - seg * R);
     }
@@ -281,7 +281,7 @@ template <int KV> __global__ __launch_bounds__(256) void lin_join_kernel(LinArgs
     }
     if (n < 0) return;
     seq_rows(a.cu, n, a.T, start, count);
-    const int segs = (count + R - 1) / R;
+    const int segs = (count - 1) / R + 1;
     const int64_t piece = static_cast<int64_t>(start / R) * a.H + h;
     f32x4 *p = reinterpret_cast<f32x4 *>(ws.state + piece * KV) + e;
     const int64_t step = static_cast<int64_t>(a.H) * (KV / 4);
