@@ -41,10 +41,8 @@ template <int K, int V, bool OUT_> struct LinF32 {
 #pragma unroll
         for (int m = 0; m < M; ++m) S[m] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    // what no chunk writes: the scores of the first 16 rows for the last 16 columns are 0
-    static __device__ __forceinline__ void prepare(char *scores, int tid) {
-        if (OUT && tid < 64) *reinterpret_cast<f32x4 *>(scores + at<8>(tid & 15, 4 + (tid >> 4))) = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+    // (no product reads the scores of the first 16 rows for the last 16 columns, which no chunk writes)
+    static __device__ __forceinline__ void prepare(char *, int) {}
 
     // Rows from `count` on are the last one again: their scores are masked and their values weigh 0.
     template <int CH, int L> static __device__ __forceinline__ void load_rows(f32x4 (&x)[L], const T *p, int64_t stride, int count, int tid) {
