@@ -14,8 +14,9 @@ using namespace kda;
 
 namespace {
 
-// Launches stay below 2^32 threads: N H workgroups of up to 512, and a bounded number more for
-// segments of long sequences.
+// Launches stay below 2^32 threads: single tokens N H workgroups of kLinDecodeThreads, prompts N H of up to
+// 512 and a bounded number more for segments of long sequences.
+static_assert(((int64_t(1) << 22) - 1) * kLinDecodeThreads < int64_t(1) << 32, "a launch's threads");
 bool sizes_ok(int32_t N, int32_t T, int32_t H) {
     return N >= 1 && T >= 0 && T < INT32_MAX - 1023 && H >= 1 && static_cast<int64_t>(T) * H < INT32_MAX - 1023 &&
            static_cast<int64_t>(N) * H < int64_t(1) << 22;

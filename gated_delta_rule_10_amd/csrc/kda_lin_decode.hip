@@ -17,7 +17,7 @@ namespace {
 
 typedef float f4 __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 16;
+constexpr int kWaves = kLinDecodeThreads / 64;
 
 // Nontemporal: a state is touched once per step, and the caches of a model's layers exceed the
 // Infinity Cache (measured for the same access in kda_decode.hip).

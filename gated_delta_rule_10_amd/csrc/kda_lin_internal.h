@@ -25,6 +25,9 @@ struct LinArgs {
     kda_dtype_t in_dtype, out_dtype;
 };
 
+// Threads of a workgroup of single tokens.
+constexpr int kLinDecodeThreads = 1024;
+
 hipError_t launch_lin_chunk(const LinArgs &a, hipStream_t stream);
 hipError_t launch_lin_decode(const LinArgs &a, hipStream_t stream);  // N sequences of one token
 
