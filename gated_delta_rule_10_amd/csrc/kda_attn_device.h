@@ -137,7 +137,8 @@ template <typename Key> __device__ __forceinline__ int wave_last_upto(int N, int
     while (len > 1) {
         const int step = (len + 63) / 64, at = lane * step;
         const bool upto = at < len && key(lo + at) <= s;
-        const int i = max(__popcll(__ballot(upto)) - 1, 0) * step;
+        const int some = static_cast<int>(__popcll(__ballot(upto)));  // (unsigned: less 1, none would be 2^32 - 1)
+        const int i = (some > 0 ? some - 1 : 0) * step;
         lo += i;
         len = min(step, len - i);
     }

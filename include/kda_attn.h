@@ -40,8 +40,8 @@
  *    (t, h, i) is at t * stride + h * d + i, with the token stride in elements,
  *    at least heads * d, at most 2^24 and a multiple of 8. Outputs are dense.
  *  - cu_seqlens [N + 1] int32: sequence n has rows [cu_seqlens[n],
- *    cu_seqlens[n + 1]) of the packed token axis. Rows from cu_seqlens[N] on
- *    are neither read nor written.
+ *    cu_seqlens[n + 1]) of the packed token axis. Rows before
+ *    cu_seqlens[0] and from cu_seqlens[N] on are neither read nor written.
  *  - Device-side contents that break the rules below never cause an access
  *    outside the given arrays: offsets are clamped to [0, T], cached lengths
  *    to the page table's reach, and a page outside [0, num_pages) holds

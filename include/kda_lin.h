@@ -65,8 +65,8 @@ extern "C" {
 
 /*
  * Linear attention over N packed sequences. Sequence n has rows
- * [cu_seqlens[n], cu_seqlens[n + 1]) of the packed token axis; rows from
- * cu_seqlens[N] on are neither read nor written.
+ * [cu_seqlens[n], cu_seqlens[n + 1]) of the packed token axis; rows before
+ * cu_seqlens[0] and from cu_seqlens[N] on are neither read nor written.
  *
  *   q, k        [T_total, Hk, d_k]  in_dtype    v [T_total, H, d_v] in_dtype
  *   log_decay   [T_total, H] or [H] fp32
