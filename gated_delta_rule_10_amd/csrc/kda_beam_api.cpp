@@ -38,8 +38,15 @@ kda_status_t kda_beam_select(const void *logits, int64_t stride, const float *sc
         if (!given(p)) return KDA_ERR_INVALID_ARG;
     if (!aligned16(done) || (done && (done_token < 0 || done_token >= V)) || !aligned16(workspace)) return KDA_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < beam_select_workspace(N, W, V)) return KDA_ERR_WORKSPACE;
-    // a request's new scores may only take the place of its own
-    if (out_scores == scores && K != W) return KDA_ERR_INVALID_ARG;
+    // A request's new scores may only take the place of its own: other requests' scores and beams that have ended are
+    // still read while outputs are written.
+    const size_t beams = static_cast<size_t>(N) * W, outs = static_cast<size_t>(N) * K * 4;
+    const void *out[] = {out_scores, out_parent, out_token};
+    for (int i = 0; i < 3; ++i) {
+        const bool in_place = i == 0 && out_scores == scores && K == W;
+        if ((!in_place && overlap(out[i], outs, scores, beams * 4)) || overlap(out[i], outs, done, beams)) return KDA_ERR_INVALID_ARG;
+        if (overlap(out[i], outs, out[(i + 1) % 3], outs)) return KDA_ERR_INVALID_ARG;
+    }
     SelectArgs a{};
     a.logits = logits; a.stride = stride; a.scores = scores; a.done = done; a.done_token = done_token;
     a.N = N; a.W = W; a.V = V; a.K = K; a.dtype = dtype;
@@ -51,7 +58,9 @@ kda_status_t kda_state_reorder(void *states, int64_t layer_stride, int32_t layer
                                int64_t slot_bytes, const int32_t *slots, const int32_t *parent, int32_t *slots_out,
                                int32_t N, int32_t W, hipStream_t stream) {
     if (!beams_ok(N, W) || layers < 1 || num_slots < 1 || static_cast<int64_t>(N) * layers >= 1 << 22) return KDA_ERR_INVALID_ARG;
-    if (!given(states) || !given(slots) || !given(parent) || !given(slots_out) || slots_out == slots || slots_out == parent) return KDA_ERR_INVALID_ARG;
+    if (!given(states) || !given(slots) || !given(parent) || !given(slots_out)) return KDA_ERR_INVALID_ARG;
+    const size_t beams = static_cast<size_t>(N) * W * sizeof(int32_t);  // every workgroup reads its request's
+    if (overlap(slots_out, beams, slots, beams) || overlap(slots_out, beams, parent, beams)) return KDA_ERR_INVALID_ARG;
     if (slot_bytes < 16 || slot_bytes % 16 != 0 || slot_bytes > int64_t(1) << 36) return KDA_ERR_INVALID_ARG;
     if (layers > 1 && (layer_stride % 16 != 0 || layer_stride / slot_bytes < num_slots)) return KDA_ERR_INVALID_ARG;
     ReorderArgs a{};

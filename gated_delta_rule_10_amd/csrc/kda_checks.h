@@ -4,6 +4,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cstddef>
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
@@ -17,6 +18,12 @@ inline bool given(const void *p) { return p && aligned16(p); }
 inline bool head_dim_ok(int32_t d) { return d == 64 || d == 128; }
 inline bool dtype_valid(kda_dtype_t d) { return d == KDA_F32 || d == KDA_BF16; }
 inline bool dtype_pair_ok(kda_dtype_t in, kda_dtype_t out) { return in == KDA_BF16 || out == KDA_F32; }
+
+// whether two arrays (a null pointer is none) share bytes
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x < y + nb && y < x + na;
+}
 
 // token strides of q, k and v
 inline bool stride_ok(int64_t stride, int64_t heads, int32_t d) {

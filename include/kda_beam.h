@@ -42,7 +42,7 @@ extern "C" {
  *               elements, V <= stride <= 2^31
  *   scores      [N, W]     fp32, finite or -infinity
  *   done        [N, W]     uint8, or NULL (none has ended)
- *   out_scores  [N, K]     fp32: c, rounded once (where K = W, it may be scores itself)
+ *   out_scores  [N, K]     fp32: c, rounded once
  *   out_parent  [N, K]     int32: w
  *   out_token   [N, K]     int32: x
  *
@@ -51,7 +51,8 @@ extern "C" {
  * which decides between candidates of different beams; those of one beam are
  * compared by their logits.
  * Sizes: N >= 1, 1 <= W <= 64, V >= 1, 1 <= K <= 64, W V < 2^31, N W < 2^20,
- * 0 <= done_token < V if done is given.
+ * 0 <= done_token < V if done is given. Outputs share no memory with scores, done
+ * or each other, but out_scores may be scores itself where K = W.
  * workspace: kda_beam_select_workspace_size bytes of device scratch, whatever
  * they hold. Calls that may overlap must not share one.
  */
@@ -79,7 +80,7 @@ size_t kda_beam_select_workspace_size(int32_t N, int32_t W, int32_t V, int32_t K
  *               [0, num_slots) holds nothing and is not read or written.
  *   parent      [N, W] int32
  *   slots_out   [N, W] int32 output: their slots afterwards, a permutation of
- *               each request's. Not the same memory as slots or parent.
+ *               each request's. Shares no memory with slots or parent.
  *
  * Sizes: N >= 1, 1 <= W <= 64, N W < 2^20, layers >= 1, num_slots >= 1,
  * slot_bytes a multiple of 16 from 16 to 2^36, layer_stride a multiple of 16
