@@ -71,7 +71,12 @@ size_t kda_beam_select_workspace_size(int32_t N, int32_t W, int32_t V, int32_t K
  * rising order of both, and the parent's state is copied there. So a state is
  * only moved where a parent has several children, and no slot is both read and
  * written. A parent outside [0, W) is none: the beam takes a slot with whatever
- * it holds.
+ * it holds. So does a beam but the first that goes on from a parent whose slot
+ * holds nothing (below): there is no state to copy, and the slot's own is another
+ * beam's that has ended. Such a beam's state has to be written anew (a prompt
+ * without an initial state, or a first token whose g is -infinity over finite
+ * values) before it is read; kda_beam_select chooses no beam whose score is
+ * -infinity, which is what a beam that holds nothing should have.
  *
  *   states      of every layer [num_slots] rows of slot_bytes (a state cache
  *               [num_slots, H, d_k, d_v], or any other per-sequence state),
