@@ -55,6 +55,8 @@ kda_status_t kda_lin_chunk_fwd(const void *q, const void *k, const void *v, cons
     if (!stride_ok(q_stride, Hk, d_k) || !stride_ok(k_stride, Hk, d_k) || !stride_ok(v_stride, H, d_v) ||
         !decay_ok(decay_stride, H))
         return KDA_ERR_INVALID_ARG;
+    const size_t states = static_cast<size_t>(state_slots ? num_slots : N) * H * d_k * d_v * sizeof(float);
+    if (initial_state != final_state && overlap(initial_state, states, final_state, states)) return KDA_ERR_INVALID_ARG;
     const size_t need = lin_chunk_workspace(N, T_total, H, d_k, d_v, in_dtype);
     if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     LinArgs a{};

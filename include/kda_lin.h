@@ -77,9 +77,10 @@ extern "C" {
  *               sequences must differ.
  *   initial_state  NULL for zeros
  *   final_state    output, NULL if not wanted; may be the same pointer as
- *                  initial_state. A sequence without tokens leaves
- *                  final_state = initial_state (or 0).
- *   o           [T_total, H, d_v]   out_dtype output (dense)
+ *                  initial_state, else shares no memory with it. A sequence
+ *                  without tokens leaves final_state = initial_state (or 0).
+ *   o           [T_total, H, d_v]   out_dtype output (dense), shares no memory
+ *               with the inputs
  *
  * Sizes: N >= 1, H >= 1, 0 <= T_total < 2^31 - 1024, T_total H < 2^31 - 1024,
  * N H < 2^22; num_slots >= 1 with state_slots. `scale` is finite and multiplies
