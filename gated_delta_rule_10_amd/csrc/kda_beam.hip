@@ -12,10 +12,13 @@
 // list overflows (many equal logits, rising ones), the workgroup looks at its
 // piece again and keeps the K best in order, one insertion after the other.
 //
-// 16 x 8 rows of 100003 bf16 logits (25.6 MB, K = 16): 13 us for the rows (2 TB/s: a row
-// is short, and a wave's exponentials and comparisons take as long as its loads) and 9
-// for the joins, which are a chain of short steps that only N workgroups take; sorted lists
-// in each wave instead of a bar took 42 in all. 4 rows of 32000 fp32: 5.6 and 6.6.
+// 16 x 8 rows of 100003 bf16 logits, K = 16, a third of the beams ended (17 MB are read): 16 us
+// for the rows (1 TB/s: a row is short, and a wave's exponentials and comparisons take longer
+// than its loads, vector instructions 55 % busy) and 9 for the joins, which are a chain of short
+// steps that only N workgroups take; sorted lists in each wave instead of a bar took 42 in all.
+// 4 rows of 32000 fp32: 6.5 and 7. Where many tokens reach the bar, lists overflow and rows are gone
+// through again: the same rows all equal 69 us in all, all but 50 of a row at the lowest finite
+// number 81 (at -infinity 23).
 //
 // Reordering moves bytes: 16 x 8 beams that all go on from few, 8 layers of 2 MB states,
 // 1.6 GB read and written: 290 us, 5.55 TB/s.

@@ -16,13 +16,14 @@
 // off by 2.6e-6 of their size instead of 4e-7, and 150 us of 1450 less for 131072 tokens,
 // H = 32). S and P only go into the outputs and are two parts (16 bits), also for bf16 outputs:
 // one part would be rounded as much as those are, and they would be off by 0.0024 of their
-// size instead of 0.0017.
+// size instead of 0.0017 (131072 tokens 1420 us instead of 1550).
 //
 // 16 value channels to a wave and 8 waves to a workgroup, one to a compute unit: S is 32
 // registers of a lane, and the chunk's tiles are read by 8 waves at once. (Four waves of
 // 32 channels, two workgroups to a compute unit: 1446 us against 1421, and 16 prompts of
-// 217 to 3448 tokens 252 against 199.) A chunk's loads, products, LDS reads and
-// conversions hardly overlap within a wave: a workgroup alone takes 3 us a chunk.
+// 217 to 3448 tokens 252 against 199, both with one part of S and P.) A chunk's loads,
+// products, LDS reads and conversions hardly overlap within a wave: a workgroup alone
+// takes 3.5 us a chunk.
 #pragma once
 
 #include "kda_attn_device.h"
@@ -65,7 +66,7 @@ __device__ __forceinline__ void widen(const bf16x8 &v, float (&x)[8]) {
 // The lane's number as a value that the compiler does not see through: addresses in LDS, an exclusive
 // or away from it, are then made where they are used instead of being kept over the chunks. The walk to
 // the ends has room for 4 waves on a SIMD that way; the outputs' has two at most for their state and
-// outputs, and is faster with the addresses kept (1421 against 1467 us).
+// outputs, and is faster with the addresses kept (1421 against 1467 us, with one part of S and P).
 __device__ __forceinline__ int opaque(int lane) {
     __asm__ volatile("" : "+v"(lane));
     return lane;

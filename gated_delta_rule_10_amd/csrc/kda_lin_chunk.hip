@@ -10,13 +10,14 @@
 // it where a few sequences would leave the card empty.
 //
 // What bounds it (H = 32, 128 channels, bf16): 131072 tokens are 4.37 GB, 930 us at the
-// rate of a large copy (4.7 TB/s), and take 1370 to 1445 by the card's state: 930 to
-// 1040 for the outputs (4.5 GB, 4.3 to 4.8 TB/s: memory), 440 for the ends, which are bound
+// rate of a large copy (4.7 TB/s), and take 1550 to 1600 by the card's state: 1090 to
+// 1210 for the outputs (4.5 GB, 3.7 to 4.1 TB/s, matrix cores 36 % and vector instructions
+// 46 % busy: a chunk's steps hardly overlap), 440 to 460 for the ends, which are bound
 // by the walk of the heads that forget slowly (128 chunks at 3.4 us, two workgroups to
 // a compute unit; the others stop early, so that 1.3 GB are read). The same in pieces of
 // 8192 to 65536 tokens, whose k and v the Infinity Cache could hold for the second
 // walk, is slower (6 to 47 %): the launches drain the card between them. Few prompts
-// are bound by the walk: one workgroup alone takes 3 us a chunk of 64 tokens.
+// are bound by the walk: one workgroup alone takes 3.5 us a chunk of 64 tokens.
 #include "kda_attn_internal.h"
 #include "kda_lin_bf16.h"
 #include "kda_lin_device.h"
@@ -62,7 +63,9 @@ struct Span {
 
 // The place whose turn it is, in the order of the grid, where there are more workgroups than the card
 // holds: up to 64 places go by their tokens, most first, so that a long one is not left over at the end (16
-// prompts of 259 to 3509 tokens, the longest last, H = 32: 216 us, and 277 as they come, before later steps). A place to a lane.
+// prompts of 259 to 3509 tokens, the longest last, H = 32: 216 us, and 277 as they come, before later steps). A place to
+// a lane. More than 64 go as they come, and have less to lose (80 prompts of 50 to 1912 tokens, H = 32: 499 us the
+// longest first, 511 mixed, 523 the longest last).
 __device__ __forceinline__ int place_of(const LinArgs &a, int R, int turn, int places, int lane) {
     int start, count, first = 0, of = 0, rank = 0;
     seq_rows(a.cu, min(lane, a.N - 1), a.T, start, count);
@@ -248,9 +251,9 @@ __global__ __launch_bounds__(W::NT, W::kWavesPerSimd) void lin_segments_kernel(L
             tabulate(g, b ^ 1, tokens - (c + 1) * C);
             if (c + 2 < chunks) g = decay(c + 2);
         }
-        // Whole rows, a chunk late, past the caches, before the next chunk's loads. (8 x 2000 tokens, 135 us:
-        // behind the scores 1.5 more, behind the loads 12, through the caches 1.5; the waves' own columns, 32
-        // bytes of a row, 5, and those past the caches 14.)
+        // Whole rows, a chunk late, past the caches, before the next chunk's loads. (8 x 2000 tokens,
+        // 135 us when scores had one part, 157 now: behind the scores 1.5 more, behind the loads 12, through
+        // the caches 1.5; the waves' own columns, 32 bytes of a row, 5, and those past the caches 14.)
         if (c > 0) store(c - 1);
         W::scores(scores, tiles, d, a.scale, w, lane);
         if (c + 1 < chunks) load(c + 1);

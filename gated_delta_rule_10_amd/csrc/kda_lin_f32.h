@@ -9,8 +9,10 @@
 //
 // Bound by the matrix instructions, at an eighth of the bf16 rate: a chunk of 32 tokens
 // takes 5.9 us of one workgroup. Sequences of 4000, 37 and 411 tokens, H = 16, 128
-// channels: 110 us (35 for the ends, 73 for the outputs); 8.2 GFLOP, 53 us at the rate of
-// a large fp32 product (154 TFLOP/s).
+// channels: 111 us (35 for the ends, 73 for the outputs). The definition's operations are
+// 4.7 GFLOP, 30 us at the rate of a large fp32 product (154 TFLOP/s); these are 7.9, 51 us: 0.9
+// more for the scores and their products with v in tiles of 16 x 16, and 2.3 for the
+// ends' updates, which the outputs repeat.
 #pragma once
 
 #include "kda_attn_device.h"
