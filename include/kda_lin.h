@@ -32,8 +32,8 @@
  *    at least heads * d, at most 2^24 and a multiple of 8. Outputs are dense.
  *  - log_decay is fp32: g of token t and head h at t * decay_stride + h. A
  *    decay_stride of 0 gives every token of a head the same g ([H]); otherwise
- *    it is at least H and at most 2^24. g <= 0; -infinity forgets the state
- *    whole (a token that starts anew). g below -110 counts as -110 where it is
+ *    it is at least H and at most 2^24. g <= 0; -infinity forgets a finite
+ *    state whole (a token that starts anew). g below -110 counts as -110 where it is
  *    summed, and e^-110 is 0 in fp32.
  *  - Device-side contents that break the rules below never cause an access
  *    outside the given arrays: offsets are clamped to [0, T], and a slot outside
